@@ -41,8 +41,15 @@ MOE_LAYOUT_PADDED_LL = 1
  MOE_BUF_WORKSPACE) = range(16)
 
 (MOE_KERNEL_LAYOUT, MOE_KERNEL_DISPATCH, MOE_KERNEL_COMBINE, MOE_KERNEL_DISPATCH_BWD,
- MOE_KERNEL_COMBINE_BWD) = range(5)
-KERNEL_NAMES = ("layout", "dispatch", "combine", "dispatch_bwd", "combine_bwd")
+ MOE_KERNEL_COMBINE_BWD, MOE_KERNEL_EXPERT_GEMM, MOE_KERNEL_EXPERT_BWD_ROWS, MOE_KERNEL_EXPERT_BWD_WEIGHTS,
+ MOE_KERNEL_SWIGLU, MOE_KERNEL_SWIGLU_BWD) = range(10)
+KERNEL_NAMES = ("layout", "dispatch", "combine", "dispatch_bwd", "combine_bwd", "expert_gemm", "expert_bwd_rows",
+                "expert_bwd_weights", "swiglu", "swiglu_bwd")
+
+# order of a row buffer of the expert products and the activation
+MOE_ROWS_RECV, MOE_ROWS_PACKED = 0, 1
+MOE_GRAD_BF16, MOE_GRAD_F32 = 0, 1
+MOE_MAX_FEATURES = 65536
 
 
 class MoeError(RuntimeError):
@@ -77,7 +84,9 @@ EXPORTS = ("moe_status_str", "moe_size_hint", "moe_ctx_create", "moe_ctx_destroy
            "moe_combine_backward", "moe_ctx_set_max_workgroups", "moe_hook_create", "moe_hook_destroy",
            "moe_hook_record", "moe_hook_wait", "moe_poll_error", "moe_timing_begin", "moe_timing_end",
            "moe_timing_launches", "moe_dispatch_noalloc",
-           "moe_dispatch_layout_prefetch")
+           "moe_dispatch_layout_prefetch", "moe_expert_gemm", "moe_expert_gemm_fp8",
+           "moe_expert_gemm_backward_rows", "moe_expert_gemm_backward_weights", "moe_swiglu", "moe_swiglu_fp8",
+           "moe_swiglu_backward")
 
 _lib = None
 
@@ -119,6 +128,14 @@ def load_library(path=LIB_PATH):
                                 ctypes.POINTER(ctypes.c_int32)],
         "moe_dispatch_noalloc": [ctypes.POINTER(moe_config), vp, vp, i32, ctypes.POINTER(moe_dispatch_buffers),
                                  ctypes.POINTER(moe_handle), vp, vp],
+        "moe_expert_gemm": [vp, vp, i32, vp, i32, i32, ctypes.POINTER(moe_handle), vp, i32, vp],
+        "moe_expert_gemm_fp8": [vp, vp, vp, i32, vp, vp, i32, i32, ctypes.POINTER(moe_handle), vp, i32, vp],
+        "moe_expert_gemm_backward_rows": [vp, vp, i32, vp, i32, i32, ctypes.POINTER(moe_handle), vp, i32, vp],
+        "moe_expert_gemm_backward_weights": [vp, vp, i32, vp, i32, i32, i32, ctypes.POINTER(moe_handle), vp, i32,
+                                             i32, vp],
+        "moe_swiglu": [vp, vp, i32, i32, ctypes.POINTER(moe_handle), vp, vp],
+        "moe_swiglu_fp8": [vp, vp, i32, i32, ctypes.POINTER(moe_handle), vp, vp, vp],
+        "moe_swiglu_backward": [vp, vp, vp, i32, i32, ctypes.POINTER(moe_handle), vp, vp],
     }
     for name, args in sigs.items():
         f = getattr(lib, name)
@@ -487,6 +504,175 @@ def moe_combine_backward(ctx, grad_out, topk_weights, expert_out, handle, grad_e
                                                _ptr(grad_expert_out), _ptr(grad_weights), _stream()),
            "moe_combine_backward")
     return grad_expert_out, grad_weights
+
+
+# ---------------------------------------------------------------- expert products
+def _expert_rows(ctx, t, dtype, width, order, name):
+    """A row buffer of an expert product: [rows, width] of the dtype on the
+    context's device, with every row that its order can address."""
+    _as_dev(t, dtype, name)
+    c = ctx.cfg
+    if t.device.index != ctx.device:
+        raise ValueError("%s is on %s, the context on cuda:%d" % (name, t.device, ctx.device))
+    if order == MOE_ROWS_PACKED or c.layout == MOE_LAYOUT_CONTIGUOUS:
+        need = c.max_tokens * c.topk
+    elif order == MOE_ROWS_RECV:
+        need = c.num_experts * c.max_tokens * c.num_ranks
+    else:
+        raise ValueError("row order must be MOE_ROWS_RECV or MOE_ROWS_PACKED")
+    if t.dim() != 2 or t.shape[1] != width or t.shape[0] < need:
+        raise ValueError("%s must be [%d, %d], is %s" % (name, need, width, tuple(t.shape)))
+    return t
+
+
+def _expert_out(ctx, width, dtype, order):
+    c = ctx.cfg
+    n = (c.num_experts * c.max_tokens * c.num_ranks
+         if order == MOE_ROWS_RECV and c.layout == MOE_LAYOUT_PADDED_LL else c.max_tokens * c.topk)
+    return torch.empty((n, width), dtype=dtype, device=torch.device("cuda", ctx.device))
+
+
+def _expert_mats(ctx, t, dtype, shape, name):
+    _as_dev(t, dtype, name)
+    if t.device.index != ctx.device:
+        raise ValueError("%s is on %s, the context on cuda:%d" % (name, t.device, ctx.device))
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must be %s, is %s" % (name, shape, tuple(t.shape)))
+    return t
+
+
+def _mats_shape(ctx, weights):
+    if weights.dim() != 3 or weights.shape[0] != ctx.cfg.num_experts:
+        raise ValueError("weights must be [%d, out_features, in_features]" % ctx.cfg.num_experts)
+    return weights.shape[1], weights.shape[2]
+
+
+def moe_expert_gemm(ctx, rows, weights, handle, out=None, rows_order=MOE_ROWS_RECV, out_order=MOE_ROWS_RECV):
+    """Each expert's rows times its matrix: rows bf16 [rows, K], weights bf16
+    [E, N, K] -> out bf16 [rows, N].  The orders say how the row buffers are
+    laid out (the receive layout, or packed by expert)."""
+    N, K = _mats_shape(ctx, weights)
+    _check_handle(ctx, handle)
+    _expert_mats(ctx, weights, torch.bfloat16, (ctx.cfg.num_experts, N, K), "weights")
+    _expert_rows(ctx, rows, torch.bfloat16, K, rows_order, "rows")
+    if out is None:
+        out = _expert_out(ctx, N, torch.bfloat16, out_order)
+    _expert_rows(ctx, out, torch.bfloat16, N, out_order, "out")
+    _check(load_library().moe_expert_gemm(ctx.handle, _ptr(rows), rows_order, _ptr(weights), K, N,
+                                          ctypes.byref(handle.c), _ptr(out), out_order, _stream()), "moe_expert_gemm")
+    return out
+
+
+def moe_expert_gemm_fp8(ctx, rows, row_scales, weights, weight_scales, handle, out=None, rows_order=MOE_ROWS_RECV,
+                        out_order=MOE_ROWS_RECV):
+    """moe_expert_gemm of E4M3 codes (uint8): rows [rows, K] with fp32 row_scales
+    [rows, K/128], weights [E, N, K] with fp32 weight_scales [E, ceil(N/128), K/128]
+    -> out bf16 [rows, N]."""
+    N, K = _mats_shape(ctx, weights)
+    _check_handle(ctx, handle)
+    _expert_mats(ctx, weights, torch.uint8, (ctx.cfg.num_experts, N, K), "weights")
+    _expert_rows(ctx, rows, torch.uint8, K, rows_order, "rows")
+    _expert_rows(ctx, row_scales, torch.float32, K // 128, rows_order, "row_scales")
+    _expert_mats(ctx, weight_scales, torch.float32, (ctx.cfg.num_experts, -(-N // 128), K // 128), "weight_scales")
+    if out is None:
+        out = _expert_out(ctx, N, torch.bfloat16, out_order)
+    _expert_rows(ctx, out, torch.bfloat16, N, out_order, "out")
+    _check(load_library().moe_expert_gemm_fp8(ctx.handle, _ptr(rows), _ptr(row_scales), rows_order, _ptr(weights),
+                                              _ptr(weight_scales), K, N, ctypes.byref(handle.c), _ptr(out), out_order,
+                                              _stream()), "moe_expert_gemm_fp8")
+    return out
+
+
+def moe_expert_gemm_backward_rows(ctx, grad_out, weights, handle, grad_rows=None, out_order=MOE_ROWS_RECV,
+                                  rows_order=MOE_ROWS_RECV):
+    """Gradient of moe_expert_gemm for its rows: bf16 [rows, K]."""
+    N, K = _mats_shape(ctx, weights)
+    _check_handle(ctx, handle)
+    _expert_mats(ctx, weights, torch.bfloat16, (ctx.cfg.num_experts, N, K), "weights")
+    _expert_rows(ctx, grad_out, torch.bfloat16, N, out_order, "grad_out")
+    if grad_rows is None:
+        grad_rows = _expert_out(ctx, K, torch.bfloat16, rows_order)
+    _expert_rows(ctx, grad_rows, torch.bfloat16, K, rows_order, "grad_rows")
+    _check(load_library().moe_expert_gemm_backward_rows(ctx.handle, _ptr(grad_out), out_order, _ptr(weights), K, N,
+                                                        ctypes.byref(handle.c), _ptr(grad_rows), rows_order,
+                                                        _stream()), "moe_expert_gemm_backward_rows")
+    return grad_rows
+
+
+def moe_expert_gemm_backward_weights(ctx, grad_out, rows, handle, grad_weights=None, out_order=MOE_ROWS_RECV,
+                                     rows_order=MOE_ROWS_RECV, accumulate=False):
+    """Gradient of moe_expert_gemm for its matrices: [E, N, K], bf16 (the
+    default) or fp32 as grad_weights is.  accumulate: add to grad_weights."""
+    c = ctx.cfg
+    if grad_out.dim() != 2 or rows.dim() != 2:
+        raise ValueError("grad_out and rows must have two dimensions")
+    N, K = grad_out.shape[1], rows.shape[1]
+    _check_handle(ctx, handle)
+    _expert_rows(ctx, grad_out, torch.bfloat16, N, out_order, "grad_out")
+    _expert_rows(ctx, rows, torch.bfloat16, K, rows_order, "rows")
+    if grad_weights is None:
+        if accumulate:
+            raise ValueError("accumulate needs grad_weights")
+        grad_weights = torch.empty((c.num_experts, N, K), dtype=torch.bfloat16, device=rows.device)
+    if grad_weights.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("grad_weights must be bfloat16 or float32")
+    _expert_mats(ctx, grad_weights, grad_weights.dtype, (c.num_experts, N, K), "grad_weights")
+    kind = MOE_GRAD_F32 if grad_weights.dtype is torch.float32 else MOE_GRAD_BF16
+    _check(load_library().moe_expert_gemm_backward_weights(ctx.handle, _ptr(grad_out), out_order, _ptr(rows), rows_order,
+                                                           K, N, ctypes.byref(handle.c), _ptr(grad_weights), kind,
+                                                           int(bool(accumulate)), _stream()),
+           "moe_expert_gemm_backward_weights")
+    return grad_weights
+
+
+def _gate_up_features(gate_up):
+    if gate_up.dim() != 2 or gate_up.shape[1] % 2:
+        raise ValueError("gate_up must be [rows, 2 * features]")
+    return gate_up.shape[1] // 2
+
+
+def moe_swiglu(ctx, gate_up, handle, out=None, order=MOE_ROWS_RECV):
+    """silu(gate) * up of rows bf16 [rows, 2I] (gate first) -> bf16 [rows, I]."""
+    features = _gate_up_features(gate_up)
+    _check_handle(ctx, handle)
+    _expert_rows(ctx, gate_up, torch.bfloat16, 2 * features, order, "gate_up")
+    if out is None:
+        out = _expert_out(ctx, features, torch.bfloat16, order)
+    _expert_rows(ctx, out, torch.bfloat16, features, order, "out")
+    _check(load_library().moe_swiglu(ctx.handle, _ptr(gate_up), features, order, ctypes.byref(handle.c), _ptr(out),
+                                     _stream()), "moe_swiglu")
+    return out
+
+
+def moe_swiglu_fp8(ctx, gate_up, handle, out=None, scales=None, order=MOE_ROWS_RECV):
+    """moe_swiglu as E4M3 codes (uint8 [rows, I]) and fp32 scales [rows, I/128]."""
+    features = _gate_up_features(gate_up)
+    _check_handle(ctx, handle)
+    _expert_rows(ctx, gate_up, torch.bfloat16, 2 * features, order, "gate_up")
+    if out is None:
+        out = _expert_out(ctx, features, torch.uint8, order)
+    if scales is None:
+        scales = _expert_out(ctx, features // 128, torch.float32, order)
+    _expert_rows(ctx, out, torch.uint8, features, order, "out")
+    _expert_rows(ctx, scales, torch.float32, features // 128, order, "scales")
+    _check(load_library().moe_swiglu_fp8(ctx.handle, _ptr(gate_up), features, order, ctypes.byref(handle.c), _ptr(out),
+                                         _ptr(scales), _stream()), "moe_swiglu_fp8")
+    return out, scales
+
+
+def moe_swiglu_backward(ctx, grad_out, gate_up, handle, grad_gate_up=None, order=MOE_ROWS_RECV):
+    """Gradient of moe_swiglu: bf16 [rows, 2I] (grad_gate_up may be gate_up)."""
+    features = _gate_up_features(gate_up)
+    _check_handle(ctx, handle)
+    _expert_rows(ctx, gate_up, torch.bfloat16, 2 * features, order, "gate_up")
+    _expert_rows(ctx, grad_out, torch.bfloat16, features, order, "grad_out")
+    if grad_gate_up is None:
+        grad_gate_up = _expert_out(ctx, 2 * features, torch.bfloat16, order)
+    _expert_rows(ctx, grad_gate_up, torch.bfloat16, 2 * features, order, "grad_gate_up")
+    _check(load_library().moe_swiglu_backward(ctx.handle, _ptr(grad_out), _ptr(gate_up), features, order,
+                                              ctypes.byref(handle.c), _ptr(grad_gate_up), _stream()),
+           "moe_swiglu_backward")
+    return grad_gate_up
 
 
 # ---------------------------------------------------------------- prepared calls

@@ -3,13 +3,15 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libmoe_ep.so")
 
 HIPCC_FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-fvisibility=hidden",
     # keep every binary32 operation as written (combine is specified with
     # separately rounded multiply and add; the kernels also say so explicitly)
@@ -23,11 +25,20 @@ HIPCC_FLAGS = [
 def build(verbose: bool = False) -> str:
     srcs = sorted(glob.glob(os.path.join(PKG, "csrc", "*.hip")))
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = ["/opt/rocm/bin/hipcc", *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"),
-           "-I", os.path.join(PKG, "csrc"), "-o", tmp, *srcs]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    hipcc = "/opt/rocm/bin/hipcc"
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
+    with tempfile.TemporaryDirectory() as objs:   # one compiler per source, in parallel
+        outs = [os.path.join(objs, os.path.basename(f) + ".o") for f in srcs]
+        cmds = [[hipcc, *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc"), "-c", f,
+                 "-o", o] for f, o in zip(srcs, outs)]
+        with ThreadPoolExecutor(min(len(cmds), os.cpu_count() or 1, 8)) as pool:
+            list(pool.map(run, cmds))
+        run([hipcc, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *outs])
     os.replace(tmp, LIB)
     return LIB
 

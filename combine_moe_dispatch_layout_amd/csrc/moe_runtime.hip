@@ -15,22 +15,31 @@
 #include <new>
 #include <vector>
 
+#include "moe_context.h"
 #include "moe_ep.h"
 #include "moe_internal.h"
 
-#define MOE_API extern "C" __attribute__((visibility("default")))
-
 using namespace moe;
+
+namespace moe {
+
+int device_cus(int dev) {
+    static std::mutex mu;
+    static int cus[64];
+    if (dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (cus[dev] == 0) {
+        int n = 0;
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess) cus[dev] = n;
+    }
+    return cus[dev];
+}
+
+}  // namespace moe
 
 namespace {
 
 constexpr uint32_t kTagMagic = 0x4d6f4500u;   // "MoE\0"
-
-struct Geometry {
-    int El, ksend, ntiles_max, rbits;
-    int64_t cap, row_bytes, nb;
-    int64_t send_rows, recv_rows;
-};
 
 int bits_for(int n) {   // bits needed to hold values 0..n-1
     int b = 0;
@@ -69,18 +78,6 @@ moe_status check_config(const moe_config* c, Geometry* g) {
     return MOE_OK;
 }
 
-// Workspace layout (device, one allocation, 256-byte aligned pieces).  The
-// first pieces -- error word, arrival counter and the grand totals, sized for
-// the largest supported E + R -- sit at the same offsets for every
-// configuration, so that a workspace shared by calls of different
-// configurations (the allocation-free dispatch's static scratch) keeps the
-// words that must read zero at the start of a layout zero: each layout zeroes
-// the totals it used before it ends.
-struct Workspace {
-    size_t off_err, off_done, off_sink, off_cnt_e, off_cnt_r, off_eoff, off_roff, off_tile_cnt, off_grand_tot,
-        off_erank, off_srank, total;
-};
-
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 int tile_stride(const Geometry& g) { return (g.ntiles_max + 3) & ~3; }
@@ -116,8 +113,6 @@ uint32_t config_tag(const moe_config* c) {
     for (size_t i = 0; i < sizeof(f); ++i) h = (h ^ b[i]) * 16777619u;
     return (h & 0xffffff00u) ^ kTagMagic;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Work split of a row-streaming kernel: each wavefront handles `chunks`
 // 16-byte chunks per lane of one token row (a "slice"), at most `cap`.  Rows
@@ -157,67 +152,7 @@ moe_status status_of_flags(uint32_t v) {
 
 }  // namespace
 
-struct moe_ctx {
-    moe_config cfg;
-    Geometry g;
-    Workspace wl;
-    int device;
-    char* ws;
-    uint32_t tag;
-    // last layout computed into the workspace, and the mode it ran in
-    const int64_t* layout_idx;
-    int32_t layout_T;
-    int32_t layout_mode;
-    bool layout_valid;
-    // tuning overrides (0 = heuristic)
-    int pack_chunks, combine_chunks;
-    // cap on the workgroups of the high-throughput kernels (0 = none)
-    int max_blocks;
-    // host-side launch log on stderr (environment MOE_EP_LOG=1 at context creation)
-    bool log;
-    // timing
-    bool timing;
-    int max_launches;
-    std::vector<hipEvent_t> ev0, ev1;
-    std::vector<int> kid;
-
-    uint32_t* err() { return reinterpret_cast<uint32_t*>(ws + wl.off_err); }
-};
-
 namespace {
-
-bool on_ctx_device(const moe_ctx* ctx) {
-    int dev = -1;
-    return hipGetDevice(&dev) == hipSuccess && dev == ctx->device;
-}
-
-const char* kernel_name(int id) {
-    static const char* names[MOE_KERNEL_COUNT] = {"layout", "dispatch", "combine", "dispatch_backward",
-                                                  "combine_backward"};
-    return id >= 0 && id < MOE_KERNEL_COUNT ? names[id] : "?";
-}
-
-// Record timing events around one launch when timing is on; log it when asked.
-// ctx may be NULL (the allocation-free dispatch): then nothing is recorded.
-struct TimedLaunch {
-    moe_ctx* ctx;
-    hipStream_t s;
-    int slot;
-    TimedLaunch(moe_ctx* c, hipStream_t st, int id) : ctx(c), s(st), slot(-1) {
-        if (c == nullptr) return;
-        if (c->log)
-            std::fprintf(stderr, "[moe_ep] ctx %p: %s on stream %p (max_workgroups %d)\n", static_cast<void*>(c),
-                         kernel_name(id), static_cast<void*>(st), c->max_blocks);
-        if (c->timing && (int)c->kid.size() < c->max_launches) {
-            slot = (int)c->kid.size();
-            c->kid.push_back(id);
-            (void)hipEventRecord(c->ev0[slot], st);
-        }
-    }
-    void done() {
-        if (slot >= 0) (void)hipEventRecord(ctx->ev1[slot], s);
-    }
-};
 
 // What the launches of one call need besides their arguments: the
 // configuration, the device workspace (a context's, or the static scratch of
@@ -250,19 +185,6 @@ Exec ctx_exec(moe_ctx* ctx) {
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-// Compute units of a device (cached per device; 0 if the query fails).
-int device_cus(int dev) {
-    static std::mutex mu;
-    static int cus[64];
-    if (dev < 0 || dev >= 64) return 0;
-    std::lock_guard<std::mutex> lock(mu);
-    if (cus[dev] == 0) {
-        int n = 0;
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess) cus[dev] = n;
-    }
-    return cus[dev];
-}
 
 // Token rows of at least this many bytes are read into the Infinity Cache
 // during the layout; at most this many (the first rows, which the dispatch

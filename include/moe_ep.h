@@ -39,8 +39,9 @@
  *    [-1, E) (the slot is treated as empty, -1), a row index outside its
  *    buffer or a low-latency window overflow (the row is not placed), a reused
  *    layout made from other routing (the changed tokens are dropped, see
- *    moe_dispatch) and Inf or NaN in an fp8 dispatch (those blocks'
- *    codes and scales are unspecified).
+ *    moe_dispatch), Inf or NaN in an fp8 dispatch or activation (those blocks'
+ *    codes and scales are unspecified) and expert offsets of a handle that are
+ *    not ascending or pass its rows (those experts are taken to have no rows).
  *  - bf16 buffers are passed as raw 16-bit storage; fp8 buffers hold OCP
  *    E4M3FN codes, one byte per channel.
  *  - With MOE_EP_LOG=1 in the environment when a context is created, each
@@ -57,8 +58,9 @@
 extern "C" {
 #endif
 
-#define MOE_EP_ABI_VERSION 5   /* 3: moe_timing_launches; 4: stale-layout and non-finite
-                                  flags, moe_dispatch_noalloc; 5: moe_dispatch_layout_prefetch */
+#define MOE_EP_ABI_VERSION 6   /* 3: moe_timing_launches; 4: stale-layout and non-finite
+                                  flags, moe_dispatch_noalloc; 5: moe_dispatch_layout_prefetch;
+                                  6: expert products and gated activation, MOE_KERNEL_COUNT 10 */
 
 /* ---------------------------------------------------------------- status */
 typedef enum moe_status {
@@ -77,8 +79,8 @@ typedef enum moe_status {
                                   topk_idx entries that differ from the ones its layout was
                                   computed from (rewritten in place in between); every such
                                   token was dropped (pos -1, no rows written) */
-    MOE_ERR_NONFINITE = 9      /* from moe_poll_error: an fp8 dispatch met Inf or NaN in a
-                                  128-channel block of x; that block's codes and scale are
+    MOE_ERR_NONFINITE = 9      /* from moe_poll_error: an fp8 dispatch (or moe_swiglu_fp8) met Inf
+                                  or NaN in a 128-channel block; that block's codes and scale are
                                   unspecified (every other block is exact) */
 } moe_status;
 
@@ -106,6 +108,7 @@ typedef enum moe_layout {
 #define MOE_MAX_RANKS   64
 #define MOE_MAX_TOPK    32
 #define MOE_MAX_HIDDEN  32768
+#define MOE_MAX_FEATURES 65536   /* columns and rows of an expert's weight matrix */
 
 typedef struct moe_config {
     int32_t max_tokens;   /* M >= 1: upper bound on num_tokens of every call; in
@@ -338,6 +341,106 @@ moe_status moe_combine_backward(moe_ctx* ctx, const void* grad_out, const float*
                                 const void* expert_out, const moe_handle* handle,
                                 void* grad_expert_out, float* grad_weights, void* stream);
 
+/* ---------------------------------------------------------------- expert products */
+/* What the experts compute between dispatch and combine (an addition: the pages
+ * stop at the receive rows).  Expert e multiplies the rows that the dispatch
+ * placed for it with its own matrix W[e], bf16 [out_features, in_features],
+ * the E matrices one after another.  The rows of an expert are a ragged segment
+ * (also empty) that the kernels find from handle->expert_offsets, so no count
+ * ever goes to the host.
+ *
+ * Row order.  Each row buffer is in one of two orders:
+ *   MOE_ROWS_RECV    the receive layout of the handle (row pos[t, j]): what
+ *                    moe_dispatch writes and moe_combine reads
+ *   MOE_ROWS_PACKED  expert-major without gaps: expert e's rows are
+ *                    [expert_offsets[e], expert_offsets[e+1])
+ * They are the same in MOE_LAYOUT_CONTIGUOUS.  In MOE_LAYOUT_PADDED_LL a packed
+ * buffer has max_tokens * topk rows instead of E * max_tokens * R: the first
+ * product reads the receive rows and writes packed ones, the activation and
+ * the second product's input stay packed, and its output goes back to the
+ * receive layout.
+ *
+ * For every call: rows that no slot points at are neither read nor written;
+ * the buffers of one call may not overlap, but for moe_swiglu_backward's; a handle
+ * from another configuration gives MOE_ERR_HANDLE; with no tokens the call
+ * returns MOE_OK at once.  All sums are binary32 in a fixed order, rounded once.
+ * NaN and infinities stay in the rows and columns that hold them.  Features
+ * are multiples of 8 (E4M3: see there) and at most MOE_MAX_FEATURES, else
+ * MOE_ERR_UNSUPPORTED; row buffers and matrices are 16-byte aligned.  The
+ * workgroup cap (moe_ctx_set_max_workgroups) leaves compute units to these
+ * products and does not apply to them. */
+typedef enum moe_rows_order {
+    MOE_ROWS_RECV = 0,
+    MOE_ROWS_PACKED = 1
+} moe_rows_order;
+
+/* out[r, n] = bf16_rne( sum over c of rows[r, c] * W[e][n, c] ), e the expert of row r.
+ *   rows     bf16 [rows, in_features] in rows_order
+ *   weights  bf16 [E, out_features, in_features]
+ *   out      bf16 [rows, out_features] in out_order */
+moe_status moe_expert_gemm(moe_ctx* ctx, const void* rows, int32_t rows_order, const void* weights,
+                           int32_t in_features, int32_t out_features, const moe_handle* handle,
+                           void* out, int32_t out_order, void* stream);
+
+/* The product of E4M3 rows and matrices with binary32 scales: for inference on
+ * an FP8 dispatch.
+ *   rows           E4M3 codes [rows, in_features]; in_features a multiple of 128
+ *   row_scales     fp32 [rows, in_features/128]: recv_scales of the dispatch, or
+ *                  moe_swiglu_fp8's out_scales; same order as rows
+ *   weights        E4M3 codes [E, out_features, in_features]
+ *   weight_scales  fp32 [E, ceil(out_features/128), in_features/128], one for each
+ *                  128 x 128 block
+ * out[r, n] = bf16_rne( sum over blocks b of row_scales[r, b] * weight_scales[e][n/128, b]
+ *                       * (sum over the block's c of rows[r, c] * W[e][n, c]) ) */
+moe_status moe_expert_gemm_fp8(moe_ctx* ctx, const void* rows, const float* row_scales,
+                               int32_t rows_order, const void* weights, const float* weight_scales,
+                               int32_t in_features, int32_t out_features, const moe_handle* handle,
+                               void* out, int32_t out_order, void* stream);
+
+/* Gradient of moe_expert_gemm with respect to the rows:
+ * grad_rows[r, c] = bf16_rne( sum over n of grad_out[r, n] * W[e][n, c] ). */
+moe_status moe_expert_gemm_backward_rows(moe_ctx* ctx, const void* grad_out, int32_t out_order,
+                                         const void* weights, int32_t in_features,
+                                         int32_t out_features, const moe_handle* handle,
+                                         void* grad_rows, int32_t rows_order, void* stream);
+
+/* Gradient of moe_expert_gemm with respect to the matrices:
+ * grad_weights[e][n, c] = sum over e's rows r of grad_out[r, n] * rows[r, c]
+ *   grad_type   type of grad_weights: MOE_GRAD_BF16 (rounded once) or MOE_GRAD_F32
+ *   accumulate  0: grad_weights is written (zeros for an expert without rows, also
+ *               with no tokens at all); 1: the gradient is added to what it holds
+ *               (in binary32, then rounded to grad_type) */
+typedef enum moe_grad_type {
+    MOE_GRAD_BF16 = 0,
+    MOE_GRAD_F32 = 1
+} moe_grad_type;
+moe_status moe_expert_gemm_backward_weights(moe_ctx* ctx, const void* grad_out, int32_t out_order,
+                                            const void* rows, int32_t rows_order,
+                                            int32_t in_features, int32_t out_features,
+                                            const moe_handle* handle, void* grad_weights,
+                                            int32_t grad_type, int32_t accumulate, void* stream);
+
+/* The gated activation between two products: for a row of gate and up values
+ * side by side (bf16 [rows, 2 * features], gate first),
+ * out[r, c] = bf16_rne( g * s * u ), s = 1 / (1 + exp(-g)), computed in binary32.
+ * Input and output rows are in the same order. */
+moe_status moe_swiglu(moe_ctx* ctx, const void* gate_up, int32_t features, int32_t order,
+                      const moe_handle* handle, void* out, void* stream);
+
+/* The same as E4M3 codes [rows, features] with fp32 scales [rows, features/128] (features
+ * a multiple of 128), quantised from the binary32 values by moe_dispatch's
+ * rule: a' = max(max|v|, 1e-4) of a block, codes E4M3(v * (448/a')), scale
+ * a'/448.  A block with Inf or NaN is reported as in moe_dispatch. */
+moe_status moe_swiglu_fp8(moe_ctx* ctx, const void* gate_up, int32_t features, int32_t order,
+                          const moe_handle* handle, void* out, float* out_scales, void* stream);
+
+/* Gradient of moe_swiglu (of moe_swiglu_fp8 with the rounding passed through):
+ * d gate = d out * u * s * (1 + g * (1 - s)), d up = d out * g * s; grad_gate_up is bf16
+ * [rows, 2 * features] and may be gate_up itself. */
+moe_status moe_swiglu_backward(moe_ctx* ctx, const void* grad_out, const void* gate_up,
+                               int32_t features, int32_t order, const moe_handle* handle,
+                               void* grad_gate_up, void* stream);
+
 /* ---------------------------------------------------------------- overlap */
 /* Resource control (DeepTech release article, feature list: flexible GPU
  * resource control and SM-count control for the high-throughput kernels; the
@@ -393,7 +496,12 @@ typedef enum moe_kernel_id {
     MOE_KERNEL_COMBINE = 2,  /* gather-reduce */
     MOE_KERNEL_DISPATCH_BWD = 3,  /* dispatch backward (gather-sum) */
     MOE_KERNEL_COMBINE_BWD = 4,   /* combine backward (weighted scatter + dot products) */
-    MOE_KERNEL_COUNT = 5
+    MOE_KERNEL_EXPERT_GEMM = 5,        /* expert products, bf16 and fp8 */
+    MOE_KERNEL_EXPERT_BWD_ROWS = 6,
+    MOE_KERNEL_EXPERT_BWD_WEIGHTS = 7,
+    MOE_KERNEL_SWIGLU = 8,             /* gated activation, bf16 and fp8 */
+    MOE_KERNEL_SWIGLU_BWD = 9,
+    MOE_KERNEL_COUNT = 10
 } moe_kernel_id;
 
 moe_status moe_timing_begin(moe_ctx* ctx, int32_t max_launches);
