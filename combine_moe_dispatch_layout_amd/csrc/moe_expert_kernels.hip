@@ -21,6 +21,8 @@
 #include "moe_expert.h"
 #include "moe_internal.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -33,8 +35,6 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 #define LDS_PTR(T, p) ((__attribute__((address_space(3))) T*)(p))
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
 constexpr int kStepBytes = 128;          // contraction bytes of a KC stage row: 64 bf16 or 128 fp8
 constexpr int kStepC = 64;               // contraction elements of a bf16 stage
 constexpr int kTileP = 256;              // i extent of a tile
@@ -54,8 +54,25 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const void* p, int6
 struct Tile {
     int e, row, rows;   // expert, first row within its segment, rows of the tile
     int64_t start;      // packed row of the segment's first row
-    int tiles;          // row tiles of the launch
+    int col;            // column tile
 };
+
+// Block b runs on XCD b % 8, and about 256 blocks (32 for each XCD) run together: blocks of one
+// XCD take 32 consecutive tiles of each run of 256, so that they share operand panels in its L2.
+__device__ __forceinline__ int64_t xcd_tile(int b) {
+    const int i = b >> 3;
+    return ((int64_t)(i >> 5) << 8) + ((b & 7) << 5) + (i & 31);
+}
+
+// Order of the tiles of one matrix with `nj` row tiles and `ni` column tiles: bands of kBand row
+// tiles, column by column, so that 32 consecutive tiles touch about 4 + 8 panels.
+constexpr int kBand = 4;
+__device__ __forceinline__ void band_order(int l, int nj, int ni, int* j, int* i) {
+    const int band = l / (kBand * ni), rest = l - band * kBand * ni;
+    const int height = min(kBand, nj - band * kBand);
+    *i = rest / height;
+    *j = band * kBand + rest - *i * height;
+}
 
 __device__ __forceinline__ int64_t seg_base(const Segments& s, int e, int64_t start, bool padded) {
     return padded ? (int64_t)e * s.cap + s.first : start;
@@ -69,10 +86,9 @@ __device__ __forceinline__ int seg_rows(const Segments& s, int lo, int hi) {
     return min(hi - lo, s.seg_cap);
 }
 
-// Row tile t of the launch, where expert e has ceil(rows / bq) of them.  Every
-// wavefront of the block scans the offsets by itself (E <= 1024: at most 16
-// per lane).
-__device__ __forceinline__ Tile find_tile(const Segments& s, int t, int bq) {
+// Tile t of the launch, where expert e has ceil(rows / bq) x ni of them; e = -1 past the last.
+// Every wavefront of the block scans the offsets by itself (E <= 1024: at most 16 per lane).
+__device__ __forceinline__ Tile find_tile(const Segments& s, int64_t t, int bq, int ni) {
     const int lane = threadIdx.x & 63;
     const int per = (s.E + 63) / 64;
     const int e0 = min(lane * per, s.E), e1 = min(e0 + per, s.E);
@@ -84,29 +100,30 @@ __device__ __forceinline__ Tile find_tile(const Segments& s, int t, int bq) {
         const int u = __shfl_up(incl, off, 64);
         if (lane >= off) incl += u;
     }
+    const int band = (int)(t / ni);   // row tiles before t's expert are at most this many
     Tile r;
-    r.tiles = __builtin_amdgcn_readlane(incl, 63);
-    const uint64_t here = __ballot(t < incl);
-    const int owner = here ? __ffsll((unsigned long long)here) - 1 : 63;
-    int rest = t - (incl - own), fe = -1, frow = 0, frows = 0, fstart = 0;
+    const uint64_t here = __ballot(band < incl);
+    r.e = -1;
+    if (here == 0) return r;
+    const int owner = __ffsll((unsigned long long)here) - 1;
+    int before = incl - own, fe = -1, fbefore = 0, fn = 0, flo = 0;
     for (int e = e0; e < e1; ++e) {
         const int lo = s.eoff[e], n = seg_rows(s, lo, s.eoff[e + 1]), m = (n + bq - 1) / bq;
-        if (fe < 0) {
-            if (rest < m) {
-                fe = e;
-                frow = rest * bq;
-                frows = min(bq, n - frow);
-                fstart = lo;
-            } else {
-                rest -= m;
-            }
+        if (fe < 0 && band < before + m) {
+            fe = e;
+            fbefore = before;
+            fn = n;
+            flo = lo;
         }
+        before += m;
     }
     r.e = __builtin_amdgcn_readlane(fe, owner);
-    r.row = __builtin_amdgcn_readlane(frow, owner);
-    r.rows = __builtin_amdgcn_readlane(frows, owner);
-    r.start = __builtin_amdgcn_readlane(fstart, owner);
-    if (here == 0) r.e = -1;
+    r.start = __builtin_amdgcn_readlane(flo, owner);
+    const int n = __builtin_amdgcn_readlane(fn, owner);
+    int j;
+    band_order((int)(t - (int64_t)__builtin_amdgcn_readlane(fbefore, owner) * ni), (n + bq - 1) / bq, ni, &j, &r.col);
+    r.row = j * bq;
+    r.rows = min(bq, n - r.row);
     return r;
 }
 
@@ -125,16 +142,18 @@ __device__ __forceinline__ int kc_key(int r) {
 // subtiles s and s + 1 are eight consecutive outputs (one 16-byte store).
 __device__ __forceinline__ int p_frag_row(int s, int i) { return 32 * (s >> 1) + 8 * (i >> 2) + 4 * (s & 1) + (i & 3); }
 
-template <int ROWS, bool ISP>
+template <int ROWS, bool ISP, int NW>
 struct LoadKC {
     static constexpr int kBytes = ROWS * kStepBytes;
-    static constexpr int kInstr = kBytes / 1024 >= kWaves ? kBytes / 1024 / kWaves : 1;
-    __amdgpu_buffer_rsrc_t rsrc;
+    static constexpr int kInstr = kBytes / 1024 >= NW ? kBytes / 1024 / NW : 1;
+    const char* base;
+    int64_t bytes;    // of the valid rows
     uint32_t voff[kInstr];
     uint32_t chunk;   // byte offset of the lane's chunk within a stage row
     int kbytes, lds;
-    __device__ __forceinline__ void init(const void* base, int64_t ld, int valid, int kb, int w, int lane) {
-        rsrc = descriptor(base, (int64_t)valid * ld);
+    __device__ __forceinline__ void init(const void* b, int64_t ld, int valid, int kb, int w, int lane) {
+        base = static_cast<const char*>(b);
+        bytes = (int64_t)valid * ld;
         kbytes = kb;
         lds = (w * kInstr * 1024) & (kBytes - 1);   // a small tile's loads are repeated by several waves
 #pragma unroll
@@ -145,23 +164,31 @@ struct LoadKC {
             voff[i] = (uint32_t)(r * ld) + c * 16;
         }
     }
-    // all of a lane's chunks have the same column only where the key repeats every 8 rows or the
-    // instruction index does not change it; P's key depends on r & 8, so keep it per instruction
-    __device__ __forceinline__ void issue(char* stage, int step) const {
-#pragma unroll
-        for (int i = 0; i < kInstr; ++i) {
-            const uint32_t col = ISP ? chunk ^ ((i & 1) << 6) : chunk;
-            const uint32_t v = (int)col + step * kStepBytes < kbytes ? voff[i] + step * kStepBytes : kOob;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, LDS_PTR(void, stage + lds + i * 1024), 16, v, 0, 0, 0);
-        }
+    // The descriptor moves along the rows, so a lane's offsets stay the same.  What it would read past
+    // a row's end is the next row: columns behind a last step of fewer than 128 bytes are masked.
+    struct Step {
+        __amdgpu_buffer_rsrc_t rsrc;
+        int left;
+    };
+    __device__ __forceinline__ Step step_of(int step) const {
+        const int64_t at = (int64_t)step * kStepBytes;
+        return Step{descriptor(base + at, at < kbytes ? bytes - at : 0), kbytes - step * kStepBytes};
+    }
+    __device__ __forceinline__ void issue(char* stage, const Step& st, int i) const {
+        // P's key, and so the column, depends on r & 8, which is the instruction's parity
+        const uint32_t col = ISP ? chunk ^ ((i & 1) << 6) : chunk;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rsrc, LDS_PTR(void, stage + (lds + i * 1024)), 16,
+                                                 (int)col < st.left ? voff[i] : kOob, 0, 0, 0);
     }
     __device__ __forceinline__ static bf16x8 frag(const char* stage, int row, int c) {
-        return *reinterpret_cast<const bf16x8*>(stage + row * kStepBytes + ((c ^ kc_key<ISP>(row)) << 4));
+        return *reinterpret_cast<const bf16x8*>(stage + (row * kStepBytes + ((c ^ kc_key<ISP>(row)) << 4)));
     }
+    // fp8: a lane group's 32 of the 128 channels are chunks g and g + 4 (both operands agree, so the
+    // order within the contraction is free): with chunks 2 g and 2 g + 1 half the LDS cycles are conflicts
     __device__ __forceinline__ static i32x8 frag8(const char* stage, int row, int g) {
-        const i32x4 lo = *reinterpret_cast<const i32x4*>(stage + row * kStepBytes + (((2 * g) ^ kc_key<ISP>(row)) << 4));
-        const i32x4 hi =
-            *reinterpret_cast<const i32x4*>(stage + row * kStepBytes + (((2 * g + 1) ^ kc_key<ISP>(row)) << 4));
+        const int at = row * kStepBytes, key = kc_key<ISP>(row);
+        const i32x4 lo = *reinterpret_cast<const i32x4*>(stage + (at + ((g ^ key) << 4)));
+        const i32x4 hi = *reinterpret_cast<const i32x4*>(stage + (at + (((g + 4) ^ key) << 4)));
         return i32x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     }
 };
@@ -172,9 +199,10 @@ struct LoadKC {
 // the 32 lanes that read together meet eight different keys.
 __device__ __forceinline__ int mc_key(int c) { return (c & 3) | ((c >> 1) & 4); }
 
+template <int NW>
 struct LoadMC {
     static constexpr int kBytes = kStepC * 512;
-    static constexpr int kInstr = kBytes / 1024 / kWaves;
+    static constexpr int kInstr = kBytes / 1024 / NW;
     const char* base;
     int64_t ld, left;   // bytes of a contraction row; bytes from base to the operand's end
     uint32_t voff[kInstr];
@@ -192,20 +220,24 @@ struct LoadMC {
             voff[i] = col0 * 2 + chunk * 16 < row_bytes ? (uint32_t)(c * row_bytes) + chunk * 16 : kOob;
         }
     }
-    __device__ __forceinline__ void issue(char* stage, int step) const {
+    struct Step {
+        __amdgpu_buffer_rsrc_t rsrc;
+    };
+    __device__ __forceinline__ Step step_of(int step) const {
         const int64_t at = (int64_t)step * kStepC * ld;
-        const __amdgpu_buffer_rsrc_t rsrc = descriptor(base + at, left - at);
-#pragma unroll
-        for (int i = 0; i < kInstr; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, LDS_PTR(void, stage + lds + i * 1024), 16, voff[i], 0, 0, 0);
+        return Step{descriptor(base + at, left - at)};
+    }
+    __device__ __forceinline__ void issue(char* stage, const Step& st, int i) const {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rsrc, LDS_PTR(void, stage + (lds + i * 1024)), 16, voff[i], 0, 0,
+                                                 0);
     }
     // columns 16 sub .. +15 as fragment rows, contraction rows c0 + 8 g .. +7 for lane group g
     __device__ __forceinline__ static bf16x8 frag(const char* stage, int sub, int c0, int lane) {
         const int g = lane >> 4, t = lane & 15;
         const int key = (t >> 2) | ((g & 1) << 2);
-        const char* at = stage + (c0 + 8 * g + (t >> 2)) * 512 + ((sub ^ key) << 5) + (t & 3) * 8;
-        const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(LDS_PTR(bf16x4, at));
-        const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(LDS_PTR(bf16x4, at + 4 * 512));
+        const int at = (c0 + 8 * g + (t >> 2)) * 512 + ((sub ^ key) << 5) + (t & 3) * 8;
+        const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(LDS_PTR(bf16x4, stage + at));
+        const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(LDS_PTR(bf16x4, stage + (at + 4 * 512)));
         return bf16x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     }
 };
@@ -250,97 +282,155 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-extern __shared__ __align__(1024) char g_lds[];
+// One stage: P's tile, Q's tile, fp8's scales.
+struct Stage {
+    char *p, *q, *scales;
+};
 
 // ---------------------------------------------------------------- tile body
 // One tile of kTileP x BQ outputs.  WP x WQ wavefronts; each owns
-// (kTileP / WP) x (BQ / WQ) outputs as 16 x 16 subtiles.
-template <int BQ, int WP, int STAGES, bool FP8, bool PMC, bool QMC>
+// (kTileP / WP) x (BQ / WQ) outputs as PS x QS subtiles of 16 x 16.
+//
+// Two stages in LDS.  A step's matrix instructions are issued in groups, one P fragment times the QS
+// Q fragments each; P fragments are read kAhead groups before they are used, Q fragments a whole
+// half step before.  After the group whose reads are the last from the stage, one barrier says that
+// every wavefront is done with it and that the other stage has arrived; the remaining groups issue
+// the loads that refill the freed stage, for two steps on, and read the first fragments of the other.
+// So nothing is waited for but loads that had a step's time to arrive.
+template <int NW, int BQ, int WP, bool FP8, bool PMC, bool QMC>
 struct TileBody {
-    static_assert(WP <= kWaves, "");
-    static constexpr int WQ = kWaves / WP;
+    static_assert(WP <= NW, "");
+    static constexpr int WQ = NW / WP;
     static constexpr int PS = kTileP / WP / 16, QS = BQ / WQ / 16;
     static_assert(PS % 2 == 0 && QS >= 1, "");
-    static constexpr int kPBytes = kTileP * kStepBytes;
-    static constexpr int kQBytes = QMC ? LoadMC::kBytes : BQ * kStepBytes;
-    static constexpr int kStage = kPBytes + kQBytes + (FP8 ? kScaleBytes : 0);
-    static constexpr int kLds = kStage * STAGES;
 
-    using LP = LoadKC<kTileP, true>;
-    using LQ = LoadKC<BQ, false>;
+    using LP = LoadKC<kTileP, true, NW>;
+    using LQ = LoadKC<BQ, false, NW>;
+    using MC = LoadMC<NW>;
+    using Frag = typename std::conditional<FP8, i32x8, bf16x8>::type;
 
+    static constexpr int kHalves = FP8 ? 1 : 2;      // matrix instructions of one step along the contraction
+    static constexpr int kGroups = kHalves * PS;
+    static constexpr int kRing = FP8 || PS < 4 ? 2 : 4;   // P fragments held
+    static constexpr int kAhead = kRing - 1;
+    static_assert(kAhead <= PS, "the first half's Q fragments are replaced in the second half");
+
+    __device__ __forceinline__ static Frag read_p(const Stage& st, int i, int w, int lane) {
+        const int wp = w % WP, g = lane >> 4, t = lane & 15, h = i / PS, p = i % PS;
+        if constexpr (FP8) return LP::frag8(st.p, wp * PS * 16 + p_frag_row(p, t), g);
+        else if constexpr (PMC) return MC::frag(st.p, wp * PS + p, h * 32, lane);
+        else return LP::frag(st.p, wp * PS * 16 + p_frag_row(p, t), h * 4 + g);
+    }
+    __device__ __forceinline__ static Frag read_q(const Stage& st, int h, int q, int w, int lane) {
+        const int wq = w / WP, g = lane >> 4, t = lane & 15;
+        if constexpr (FP8) return LQ::frag8(st.q, wq * QS * 16 + q * 16 + t, g);
+        else if constexpr (QMC) return MC::frag(st.q, wq * QS + q, h * 32, lane);
+        else return LQ::frag(st.q, wq * QS * 16 + q * 16 + t, h * 4 + g);
+    }
+    // fp8: the product of the scales of Q's row and of P's 128-column block
+    __device__ __forceinline__ static float read_scale(const Stage& st, int q, int w, int lane) {
+        return *reinterpret_cast<const float*>(st.scales + ((w / WP) * QS * 16 + q * 16 + (lane & 15)) * 4) *
+               *reinterpret_cast<const float*>(st.scales + (1024 + (w % WP) * (kTileP / WP) / 128 * 4));
+    }
+
+    // qc: Q fragments of this step's first half, read already, and at the end the next step's.
     template <class OpP, class OpQ>
-    __device__ __forceinline__ static void run(const OpP& lp, const OpQ& lq, const LoadScales& ls, int steps,
-                                               f32x4 (&acc)[PS][QS], int w, int lane) {
+    __device__ __forceinline__ static void step_of(const Stage& cur, const Stage& nxt, int step, const OpP& lp, const OpQ& lq,
+                                                   const LoadScales& ls, Frag (&pr)[kRing], Frag (&qc)[QS], float (&sc)[QS],
+                                                   f32x4 (&acc)[PS][QS], int w, int lane) {
+        constexpr int kLoadsP = OpP::kInstr, kLoads = OpP::kInstr + OpQ::kInstr + (FP8 ? 1 : 0);
+        constexpr int kBefore = kGroups - kAhead;                  // groups before the barrier
+        constexpr int kQGroups = PS < kBefore ? PS : kBefore;      // they read the second half's Q
+        const auto sp = lp.step_of(step + 2);
+        const auto sq = lq.step_of(step + 2);
+        Frag qn[QS];
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            if (i == kBefore) {
+                wait_loads<0>();
+                lds_barrier();
+            }
+            if (i < kBefore) {
+                pr[(i + kAhead) % kRing] = read_p(cur, i + kAhead, w, lane);
+                if (!FP8 && i < kQGroups) {
+#pragma unroll
+                    for (int q = i * QS / kQGroups; q < (i + 1) * QS / kQGroups; ++q) qn[q] = read_q(cur, 1, q, w, lane);
+                }
+            } else {
+                const int j = i - kBefore;
+                pr[(i + kAhead) % kRing] = read_p(nxt, j, w, lane);
+                if constexpr (!FP8) {
+#pragma unroll
+                    for (int q = j * QS / kAhead; q < (j + 1) * QS / kAhead; ++q) qc[q] = read_q(nxt, 0, q, w, lane);
+                }
+                // past the end these read nothing and write zeros
+#pragma unroll
+                for (int l = j * kLoads / kAhead; l < (j + 1) * kLoads / kAhead; ++l) {
+                    if (l < kLoadsP) lp.issue(cur.p, sp, l);
+                    else if (l < kLoadsP + OpQ::kInstr) lq.issue(cur.q, sq, l - kLoadsP);
+                    else ls.issue(cur.scales, step + 2);
+                }
+            }
+            const int p = i % PS;
+#pragma unroll
+            for (int q = 0; q < QS; ++q) {
+                if constexpr (FP8) {
+                    const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        pr[i % kRing], qc[q], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[p][q][r] = __builtin_fmaf(d[r], sc[q], acc[p][q][r]);
+                    if (i == kGroups - 1) {   // this fragment was used for the last time
+                        qc[q] = read_q(nxt, 0, q, w, lane);
+                        sc[q] = read_scale(nxt, q, w, lane);
+                    }
+                } else {
+                    acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pr[i % kRing], i < PS ? qc[q] : qn[q], acc[p][q],
+                                                                       0, 0, 0);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // The stages are distinct LDS arrays: so the compiler knows that reads of one do not wait for loads
+    // into the other.
+    template <class OpP, class OpQ>
+    __device__ __forceinline__ static void run(const Stage& s0, const Stage& s1, const OpP& lp, const OpQ& lq,
+                                               const LoadScales& ls, int steps, f32x4 (&acc)[PS][QS], int w, int lane) {
         constexpr int kLoads = OpP::kInstr + OpQ::kInstr + (FP8 ? 1 : 0);
-        const int wp = w % WP, wq = w / WP;
-        auto issue = [&](int step, int slot) {
-            char* st = g_lds + slot * kStage;
-            lp.issue(st, step);
-            lq.issue(st + kPBytes, step);
-            if constexpr (FP8) ls.issue(st + kPBytes + kQBytes, step);
+        auto fill = [&](const Stage& st, int step) {
+            const auto sp = lp.step_of(step);
+            const auto sq = lq.step_of(step);
+#pragma unroll
+            for (int l = 0; l < OpP::kInstr; ++l) lp.issue(st.p, sp, l);
+#pragma unroll
+            for (int l = 0; l < OpQ::kInstr; ++l) lq.issue(st.q, sq, l);
+            if constexpr (FP8) ls.issue(st.scales, step);
         };
+        fill(s0, 0);
+        fill(s1, 1);
 #pragma unroll
         for (int p = 0; p < PS; ++p)
 #pragma unroll
             for (int q = 0; q < QS; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-        lds_barrier();   // the previous tile's reads are done
+        Frag pr[kRing], qc[QS];
+        float sc[QS];
+        wait_loads<kLoads>();
+        lds_barrier();
 #pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s) issue(s, s);
-        int cur = 0, nxt = STAGES - 1;
-        for (int step = 0; step < steps; ++step) {
-            wait_loads<(STAGES - 2) * kLoads>();
-            lds_barrier();
-            issue(step + STAGES - 1, nxt);   // past the end: reads nothing, writes zeros
-            const char* sp = g_lds + cur * kStage;
-            const char* sq = sp + kPBytes;
-            const int g = lane >> 4, t = lane & 15;
-            if constexpr (FP8) {
-                const float* sc = reinterpret_cast<const float*>(sq + kQBytes);
-                const float sw = sc[256 + wp * (kTileP / WP) / 128];
-                i32x8 fq[QS];
-                float s[QS];
+        for (int i = 0; i < kAhead; ++i) pr[i] = read_p(s0, i, w, lane);
 #pragma unroll
-                for (int q = 0; q < QS; ++q) {
-                    const int row = wq * QS * 16 + q * 16 + t;
-                    fq[q] = LQ::frag8(sq, row, g);
-                    s[q] = sc[row] * sw;
-                }
-#pragma unroll
-                for (int p = 0; p < PS; ++p) {
-                    const i32x8 fp = LP::frag8(sp, wp * PS * 16 + p_frag_row(p, t), g);
-#pragma unroll
-                    for (int q = 0; q < QS; ++q) {
-                        const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            fp, fq[q], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[p][q][r] = __builtin_fmaf(d[r], s[q], acc[p][q][r]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    bf16x8 fq[QS];
-#pragma unroll
-                    for (int q = 0; q < QS; ++q) {
-                        if constexpr (QMC) fq[q] = LoadMC::frag(sq, wq * QS + q, kk * 32, lane);
-                        else fq[q] = LQ::frag(sq, wq * QS * 16 + q * 16 + t, kk * 4 + g);
-                    }
-#pragma unroll
-                    for (int p = 0; p < PS; ++p) {
-                        bf16x8 fp;
-                        if constexpr (PMC) fp = LoadMC::frag(sp, wp * PS + p, kk * 32, lane);
-                        else fp = LP::frag(sp, wp * PS * 16 + p_frag_row(p, t), kk * 4 + g);
-#pragma unroll
-                        for (int q = 0; q < QS; ++q)
-                            acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp, fq[q], acc[p][q], 0, 0, 0);
-                    }
-                }
-            }
-            cur = cur == STAGES - 1 ? 0 : cur + 1;
-            nxt = nxt == STAGES - 1 ? 0 : nxt + 1;
+        for (int q = 0; q < QS; ++q) {
+            qc[q] = read_q(s0, 0, q, w, lane);
+            if constexpr (FP8) sc[q] = read_scale(s0, q, w, lane);
         }
-        wait_loads<0>();   // nothing may still be on its way into LDS when it is reused
+        int step = 0;
+        for (; step + 1 < steps; step += 2) {
+            step_of(s0, s1, step, lp, lq, ls, pr, qc, sc, acc, w, lane);
+            step_of(s1, s0, step + 1, lp, lq, ls, pr, qc, sc, acc, w, lane);
+        }
+        if (step < steps) step_of(s0, s1, step, lp, lq, ls, pr, qc, sc, acc, w, lane);
+        wait_loads<0>();   // nothing may be on its way into LDS when the workgroup ends
     }
 
     // bf16 stores of the tile: out points at the tile's first output, ld its row length; i < ni, j < nj
@@ -374,9 +464,11 @@ struct TileBody {
 // ---------------------------------------------------------------- rows products
 // A tile of the forward or the rows gradient: rows [row, row + rows) of expert
 // e against output columns [i0, i0 + 256).
-template <int BQ, int WP, int STAGES, bool FP8, bool PMC>
-__device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& tl, int i0, int w, int lane) {
-    using B = TileBody<BQ, WP, STAGES, FP8, PMC, false>;
+template <int NW, int BQ, int WP, bool FP8, bool PMC>
+__device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& tl, int i0, const Stage& s0,
+                                          const Stage& s1, int w,
+                                          int lane) {
+    using B = TileBody<NW, BQ, WP, FP8, PMC, false>;
     constexpr int kSize = FP8 ? 1 : 2;
     const int cdim = PMC ? a.N : a.K, idim = PMC ? a.K : a.N;
     const int64_t qrow = seg_base(a.seg, tl.e, tl.start, a.q_padded) + tl.row;
@@ -395,58 +487,58 @@ __device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& t
                 lane);
     }
     if constexpr (PMC) {
-        LoadMC lp;
+        LoadMC<NW> lp;
         lp.init(wmat, (int64_t)a.K * 2, a.N, i0, w, lane);
-        B::run(lp, lq, ls, steps, acc, w, lane);
+        B::run(s0, s1, lp, lq, ls, steps, acc, w, lane);
     } else {
         typename B::LP lp;
         lp.init(wmat + i0 * qld, qld, ni, (int)qld, w, lane);
-        B::run(lp, lq, ls, steps, acc, w, lane);
+        B::run(s0, s1, lp, lq, ls, steps, acc, w, lane);
     }
     B::store(static_cast<uint16_t*>(a.out) + orow * idim + i0, idim, ni, tl.rows, acc, w, lane);
 }
 
-// Stages of a tile's ring: what fits in 160 KB of LDS.
-constexpr int kLdsBytes = 160 * 1024 - 1024;
+constexpr int kTileBytes = 256 * kStepBytes;   // of one operand's stage
+constexpr int kWaves = 8;   // of a workgroup (one workgroup a compute unit)
 
 template <bool FP8, bool PMC>
-__global__ __launch_bounds__(kThreads) void k_expert_rows(ExpertGemmArgs a) {
+__global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_rows(ExpertGemmArgs a) {
+    __shared__ __align__(1024) char p0[kTileBytes], p1[kTileBytes], q0[kTileBytes], q1[kTileBytes];
+    __shared__ __align__(1024) char c0[FP8 ? kScaleBytes : 16], c1[FP8 ? kScaleBytes : 16];
+    const Stage s0 = {p0, q0, c0}, s1 = {p1, q1, c1};
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int ntiles = ((PMC ? a.K : a.N) + kTileP - 1) / kTileP;
-    // block b runs on XCD b % 8: give each XCD a contiguous run of tiles
-    const int b = blockIdx.x;
-    const Tile first = find_tile(a.seg, 0, 256);
-    const int total = first.tiles * ntiles;
-    const int per = (total + 7) / 8;
-    if (b / 8 >= per) return;
-    const int t = (b % 8) * per + b / 8;
-    if (t >= total) return;
-    const Tile tl = find_tile(a.seg, t / ntiles, 256);
+    const Tile tl = find_tile(a.seg, xcd_tile(blockIdx.x), 256, ntiles);
     if (tl.e < 0) return;
-    const int i0 = (t % ntiles) * kTileP;
-    if (tl.rows > 128) rows_tile<256, 2, 2, FP8, PMC>(a, tl, i0, w, lane);
-    else if (tl.rows > 64) rows_tile<128, 2, 3, FP8, PMC>(a, tl, i0, w, lane);
-    else if (tl.rows > 32) rows_tile<64, 4, 3, FP8, PMC>(a, tl, i0, w, lane);
-    else rows_tile<32, 8, 4, FP8, PMC>(a, tl, i0, w, lane);
+    const int i0 = tl.col * kTileP;
+    if (tl.rows > 128) rows_tile<kWaves, 256, 2, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
+    else if (tl.rows > 64) rows_tile<kWaves, 128, 4, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
+    else if (tl.rows > 32) rows_tile<kWaves, 64, 4, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
+    else rows_tile<kWaves, 32, 8, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
 }
 
 // ---------------------------------------------------------------- weights gradient
-__global__ __launch_bounds__(kThreads) void k_expert_weights_grad(ExpertGemmArgs a) {
-    using B = TileBody<256, 2, 2, false, true, true>;
+__global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad(ExpertGemmArgs a) {
+    using B = TileBody<kWaves, 256, 2, false, true, true>;
+    __shared__ __align__(1024) char p0[kTileBytes], p1[kTileBytes], q0[kTileBytes], q1[kTileBytes];
+    const Stage s0 = {p0, q0, nullptr}, s1 = {p1, q1, nullptr};
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int kt = (a.K + kTileP - 1) / kTileP, nt = (a.N + 255) / 256;
-    const int b = blockIdx.x;
-    const int e = b / (kt * nt), rest = b % (kt * nt);
-    const int i0 = (rest % kt) * kTileP, j0 = (rest / kt) * 256;
+    const int64_t t0 = xcd_tile(blockIdx.x);
+    const int e = (int)(t0 / (kt * nt));
+    if (e >= a.seg.E) return;
+    int ti, tj;
+    band_order((int)(t0 - (int64_t)e * kt * nt), nt, kt, &tj, &ti);
+    const int i0 = ti * kTileP, j0 = tj * 256;
     const int lo = a.seg.eoff[e];
     const int rows = seg_rows(a.seg, lo, a.seg.eoff[e + 1]);
     const int64_t prow = seg_base(a.seg, e, lo, a.p_padded), qrow = seg_base(a.seg, e, lo, a.q_padded);
-    LoadMC lp, lq;
+    LoadMC<kWaves> lp, lq;
+    LoadScales ls;
     lp.init(static_cast<const char*>(a.p) + (rows ? prow * a.K * 2 : 0), (int64_t)a.K * 2, rows, i0, w, lane);
     lq.init(static_cast<const char*>(a.q) + (rows ? qrow * a.N * 2 : 0), (int64_t)a.N * 2, rows, j0, w, lane);
     f32x4 acc[B::PS][B::QS];
-    LoadScales ls;
-    B::run(lp, lq, ls, (rows + kStepC - 1) / kStepC, acc, w, lane);
+    B::run(s0, s1, lp, lq, ls, (rows + kStepC - 1) / kStepC, acc, w, lane);
     const int ni = min(kTileP, a.K - i0), nj = min(256, a.N - j0);
     const int64_t at = ((int64_t)e * a.N + j0) * a.K + i0;
     const int wp = w % 2, wq = w / 2, g = lane >> 4, t = lane & 15;
@@ -480,18 +572,12 @@ __global__ __launch_bounds__(kThreads) void k_expert_weights_grad(ExpertGemmArgs
     }
 }
 
-hipError_t allow_lds(const void* f) {
-    return hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBytes);
-}
-
 template <bool FP8, bool PMC>
 hipError_t launch_rows(const ExpertGemmArgs& a, int64_t pairs, hipStream_t s) {
     const int64_t ntiles = ((PMC ? a.K : a.N) + kTileP - 1) / kTileP;
     const int64_t mtiles = pairs / 256 + (pairs < a.seg.E ? pairs : a.seg.E);   // at least one expert per ragged end
-    const int64_t blocks = (mtiles * ntiles + 7) / 8 * 8;
-    hipError_t e = allow_lds(reinterpret_cast<const void*>(&k_expert_rows<FP8, PMC>));
-    if (e != hipSuccess) return e;
-    k_expert_rows<FP8, PMC><<<dim3((unsigned)blocks), dim3(kThreads), kLdsBytes, s>>>(a);
+    const int64_t blocks = (mtiles * ntiles + 255) / 256 * 256;
+    k_expert_rows<FP8, PMC><<<dim3((unsigned)blocks), dim3(64 * kWaves), 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -506,10 +592,9 @@ hipError_t launch_expert_gemm_bwd_rows(const ExpertGemmArgs& a, int64_t pairs, h
 }
 
 hipError_t launch_expert_gemm_bwd_weights(const ExpertGemmArgs& a, hipStream_t s) {
-    const int64_t blocks = (int64_t)a.seg.E * ((a.K + kTileP - 1) / kTileP) * ((a.N + 255) / 256);
-    hipError_t e = allow_lds(reinterpret_cast<const void*>(&k_expert_weights_grad));
-    if (e != hipSuccess) return e;
-    k_expert_weights_grad<<<dim3((unsigned)blocks), dim3(kThreads), kLdsBytes, s>>>(a);
+    const int64_t tiles = (int64_t)a.seg.E * ((a.K + kTileP - 1) / kTileP) * ((a.N + 255) / 256);
+    const int64_t blocks = (tiles + 255) / 256 * 256;
+    k_expert_weights_grad<<<dim3((unsigned)blocks), dim3(64 * kWaves), 0, s>>>(a);
     return hipGetLastError();
 }
 
