@@ -18,6 +18,7 @@
 // descriptor ends with the tile's valid rows; a lane whose contraction index is
 // past the end gets an address past any descriptor), which is what pads ragged
 // rows and contraction tails.
+#include "moe_ep.h"
 #include "moe_expert.h"
 #include "moe_internal.h"
 
@@ -89,16 +90,26 @@ __device__ __forceinline__ int seg_rows(const Segments& s, int lo, int hi) {
 // Tile t of the launch, where expert e has ceil(rows / bq) x ni of them; e = -1 past the last.
 // Every wavefront of the block scans the offsets by itself (E <= 1024: at most 16 per lane).
 __device__ __forceinline__ Tile find_tile(const Segments& s, int64_t t, int bq, int ni) {
+    constexpr int kPer = (MOE_MAX_EXPERTS + 63) / 64;
     const int lane = threadIdx.x & 63;
     const int per = (s.E + 63) / 64;
-    const int e0 = min(lane * per, s.E), e1 = min(e0 + per, s.E);
-    int own = 0;
-    for (int e = e0; e < e1; ++e) own += (seg_rows(s, s.eoff[e], s.eoff[e + 1]) + bq - 1) / bq;
+    const int e0 = lane * per;
+    int off[kPer + 1], own = 0;
+#pragma unroll
+    for (int u = 0; u <= kPer; ++u)
+        if (u <= per) off[u] = s.eoff[min(e0 + u, s.E)];
+    int rows[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        if (u >= per) break;
+        rows[u] = seg_rows(s, off[u], off[u + 1]);   // past the last expert: none
+        own += (rows[u] + bq - 1) / bq;
+    }
     int incl = own;
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int u = __shfl_up(incl, off, 64);
-        if (lane >= off) incl += u;
+    for (int step = 1; step < 64; step <<= 1) {
+        const int u = __shfl_up(incl, step, 64);
+        if (lane >= step) incl += u;
     }
     const int band = (int)(t / ni);   // row tiles before t's expert are at most this many
     Tile r;
@@ -107,13 +118,15 @@ __device__ __forceinline__ Tile find_tile(const Segments& s, int64_t t, int bq, 
     if (here == 0) return r;
     const int owner = __ffsll((unsigned long long)here) - 1;
     int before = incl - own, fe = -1, fbefore = 0, fn = 0, flo = 0;
-    for (int e = e0; e < e1; ++e) {
-        const int lo = s.eoff[e], n = seg_rows(s, lo, s.eoff[e + 1]), m = (n + bq - 1) / bq;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        if (u >= per) break;
+        const int m = (rows[u] + bq - 1) / bq;
         if (fe < 0 && band < before + m) {
-            fe = e;
+            fe = e0 + u;
             fbefore = before;
-            fn = n;
-            flo = lo;
+            fn = rows[u];
+            flo = off[u];
         }
         before += m;
     }
@@ -128,21 +141,9 @@ __device__ __forceinline__ Tile find_tile(const Segments& s, int64_t t, int bq, 
 }
 
 // ---------------------------------------------------------------- operands
-// KC operand: `rows` rows of 128 contraction bytes a stage.  Row r, 16-byte
-// chunk c sits at r * 128 + ((c ^ key(r)) << 4).  P's key pairs with the row
-// order of its fragments (see frag_row), Q's with consecutive rows: in both,
-// the eight lanes that read together meet eight different keys.
-template <bool ISP>
-__device__ __forceinline__ int kc_key(int r) {
-    return ISP ? ((r & 3) | ((r >> 1) & 4)) : (r & 7);
-}
-
-// Fragment rows of P: row i of the 16-row subtile s stands for tile row
-// 32 (s / 2) + 8 (i / 4) + 4 (s % 2) + i % 4, so that a lane's four values of
-// subtiles s and s + 1 are eight consecutive outputs (one 16-byte store).
-__device__ __forceinline__ int p_frag_row(int s, int i) { return 32 * (s >> 1) + 8 * (i >> 2) + 4 * (s & 1) + (i & 3); }
-
-template <int ROWS, bool ISP, int NW>
+// KC operand: ROWS rows of 128 contraction bytes a stage.  Row r, 16-byte chunk c sits at
+// r * 128 + ((c ^ (r & 7)) << 4): the eight lanes that read together meet eight different chunks.
+template <int ROWS, int NW>
 struct LoadKC {
     static constexpr int kBytes = ROWS * kStepBytes;
     static constexpr int kInstr = kBytes / 1024 >= NW ? kBytes / 1024 / NW : 1;
@@ -155,13 +156,12 @@ struct LoadKC {
         base = static_cast<const char*>(b);
         bytes = (int64_t)valid * ld;
         kbytes = kb;
-        lds = (w * kInstr * 1024) & (kBytes - 1);   // a small tile's loads are repeated by several waves
+        chunk = ((lane & 7) ^ (lane >> 3)) * 16;   // an instruction covers eight rows
+        lds = (w * kInstr * 1024) % kBytes;   // a small tile's loads are repeated by several waves
 #pragma unroll
         for (int i = 0; i < kInstr; ++i) {
             const int r = (lds >> 7) + i * 8 + (lane >> 3);
-            const int c = (lane & 7) ^ kc_key<ISP>(r);
-            if (i == 0) chunk = c * 16;
-            voff[i] = (uint32_t)(r * ld) + c * 16;
+            voff[i] = (uint32_t)(r * ld) + chunk;
         }
     }
     // The descriptor moves along the rows, so a lane's offsets stay the same.  What it would read past
@@ -171,22 +171,20 @@ struct LoadKC {
         int left;
     };
     __device__ __forceinline__ Step step_of(int step) const {
-        const int64_t at = (int64_t)step * kStepBytes;
-        return Step{descriptor(base + at, at < kbytes ? bytes - at : 0), kbytes - step * kStepBytes};
+        const int at = step * kStepBytes;
+        return Step{descriptor(base + at, at < kbytes ? bytes - at : 0), kbytes - at};
     }
     __device__ __forceinline__ void issue(char* stage, const Step& st, int i) const {
-        // P's key, and so the column, depends on r & 8, which is the instruction's parity
-        const uint32_t col = ISP ? chunk ^ ((i & 1) << 6) : chunk;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rsrc, LDS_PTR(void, stage + (lds + i * 1024)), 16,
-                                                 (int)col < st.left ? voff[i] : kOob, 0, 0, 0);
+                                                 (int)chunk < st.left ? voff[i] : kOob, 0, 0, 0);
     }
     __device__ __forceinline__ static bf16x8 frag(const char* stage, int row, int c) {
-        return *reinterpret_cast<const bf16x8*>(stage + (row * kStepBytes + ((c ^ kc_key<ISP>(row)) << 4)));
+        return *reinterpret_cast<const bf16x8*>(stage + (row * kStepBytes + ((c ^ (row & 7)) << 4)));
     }
     // fp8: a lane group's 32 of the 128 channels are chunks g and g + 4 (both operands agree, so the
     // order within the contraction is free): with chunks 2 g and 2 g + 1 half the LDS cycles are conflicts
     __device__ __forceinline__ static i32x8 frag8(const char* stage, int row, int g) {
-        const int at = row * kStepBytes, key = kc_key<ISP>(row);
+        const int at = row * kStepBytes, key = row & 7;
         const i32x4 lo = *reinterpret_cast<const i32x4*>(stage + (at + ((g ^ key) << 4)));
         const i32x4 hi = *reinterpret_cast<const i32x4*>(stage + (at + (((g + 4) ^ key) << 4)));
         return i32x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -268,6 +266,18 @@ struct LoadScales {
     }
 };
 
+// The steps of a tile in the order they are taken: from `start` to the end, then from 0.  Rows of
+// matrices whose length is a power of two lie on few memory channels at one column; tiles that start
+// at different columns spread over all of them.
+struct Steps {
+    int n, start;
+    // step of the s-th turn; past the end a step that reads nothing
+    __device__ __forceinline__ int at(int s) const {
+        const int k = s + start;
+        return s < n ? (k < n ? k : k - n) : n;
+    }
+};
+
 // s_waitcnt vmcnt(N) only
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -282,9 +292,9 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// One stage: P's tile, Q's tile, fp8's scales.
+// One stage: P's tile, Q's tile, fp8's scales; and the epilogue's 2 KB for each wavefront.
 struct Stage {
-    char *p, *q, *scales;
+    char *p, *q, *scales, *scratch;
 };
 
 // ---------------------------------------------------------------- tile body
@@ -302,10 +312,10 @@ struct TileBody {
     static_assert(WP <= NW, "");
     static constexpr int WQ = NW / WP;
     static constexpr int PS = kTileP / WP / 16, QS = BQ / WQ / 16;
-    static_assert(PS % 2 == 0 && QS >= 1, "");
+    static_assert((PS == 2 || PS % 4 == 0) && QS >= 1, "");
 
-    using LP = LoadKC<kTileP, true, NW>;
-    using LQ = LoadKC<BQ, false, NW>;
+    using LP = LoadKC<kTileP, NW>;
+    using LQ = LoadKC<BQ, NW>;
     using MC = LoadMC<NW>;
     using Frag = typename std::conditional<FP8, i32x8, bf16x8>::type;
 
@@ -317,9 +327,9 @@ struct TileBody {
 
     __device__ __forceinline__ static Frag read_p(const Stage& st, int i, int w, int lane) {
         const int wp = w % WP, g = lane >> 4, t = lane & 15, h = i / PS, p = i % PS;
-        if constexpr (FP8) return LP::frag8(st.p, wp * PS * 16 + p_frag_row(p, t), g);
+        if constexpr (FP8) return LP::frag8(st.p, wp * PS * 16 + p * 16 + t, g);
         else if constexpr (PMC) return MC::frag(st.p, wp * PS + p, h * 32, lane);
-        else return LP::frag(st.p, wp * PS * 16 + p_frag_row(p, t), h * 4 + g);
+        else return LP::frag(st.p, wp * PS * 16 + p * 16 + t, h * 4 + g);
     }
     __device__ __forceinline__ static Frag read_q(const Stage& st, int h, int q, int w, int lane) {
         const int wq = w / WP, g = lane >> 4, t = lane & 15;
@@ -333,16 +343,17 @@ struct TileBody {
                *reinterpret_cast<const float*>(st.scales + (1024 + (w % WP) * (kTileP / WP) / 128 * 4));
     }
 
-    // qc: Q fragments of this step's first half, read already, and at the end the next step's.
+    // next: the step that refills this one's stage.  qc: Q fragments of this step's first half, read
+    // already, and at the end the next step's.
     template <class OpP, class OpQ>
-    __device__ __forceinline__ static void step_of(const Stage& cur, const Stage& nxt, int step, const OpP& lp, const OpQ& lq,
+    __device__ __forceinline__ static void step_of(const Stage& cur, const Stage& nxt, int next, const OpP& lp, const OpQ& lq,
                                                    const LoadScales& ls, Frag (&pr)[kRing], Frag (&qc)[QS], float (&sc)[QS],
                                                    f32x4 (&acc)[PS][QS], int w, int lane) {
         constexpr int kLoadsP = OpP::kInstr, kLoads = OpP::kInstr + OpQ::kInstr + (FP8 ? 1 : 0);
         constexpr int kBefore = kGroups - kAhead;                  // groups before the barrier
         constexpr int kQGroups = PS < kBefore ? PS : kBefore;      // they read the second half's Q
-        const auto sp = lp.step_of(step + 2);
-        const auto sq = lq.step_of(step + 2);
+        const auto sp = lp.step_of(next);
+        const auto sq = lq.step_of(next);
         Frag qn[QS];
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
@@ -368,7 +379,7 @@ struct TileBody {
                 for (int l = j * kLoads / kAhead; l < (j + 1) * kLoads / kAhead; ++l) {
                     if (l < kLoadsP) lp.issue(cur.p, sp, l);
                     else if (l < kLoadsP + OpQ::kInstr) lq.issue(cur.q, sq, l - kLoadsP);
-                    else ls.issue(cur.scales, step + 2);
+                    else ls.issue(cur.scales, next);
                 }
             }
             const int p = i % PS;
@@ -393,11 +404,10 @@ struct TileBody {
     }
 
     // The stages are distinct LDS arrays: so the compiler knows that reads of one do not wait for loads
-    // into the other.
+    // into the other.  begin() starts the loads of a tile's first two steps, run() does the rest.
     template <class OpP, class OpQ>
-    __device__ __forceinline__ static void run(const Stage& s0, const Stage& s1, const OpP& lp, const OpQ& lq,
-                                               const LoadScales& ls, int steps, f32x4 (&acc)[PS][QS], int w, int lane) {
-        constexpr int kLoads = OpP::kInstr + OpQ::kInstr + (FP8 ? 1 : 0);
+    __device__ __forceinline__ static void begin(const Stage& s0, const Stage& s1, const OpP& lp, const OpQ& lq,
+                                                 const LoadScales& ls, const Steps& order) {
         auto fill = [&](const Stage& st, int step) {
             const auto sp = lp.step_of(step);
             const auto sq = lq.step_of(step);
@@ -407,15 +417,21 @@ struct TileBody {
             for (int l = 0; l < OpQ::kInstr; ++l) lq.issue(st.q, sq, l);
             if constexpr (FP8) ls.issue(st.scales, step);
         };
-        fill(s0, 0);
-        fill(s1, 1);
+        fill(s0, order.at(0));
+        fill(s1, order.at(1));
+    }
+    // kBehind: loads and stores issued after the second step's loads
+    template <int kBehind, class OpP, class OpQ>
+    __device__ __forceinline__ static void run(const Stage& s0, const Stage& s1, const OpP& lp, const OpQ& lq,
+                                               const LoadScales& ls, const Steps& order, f32x4 (&acc)[PS][QS], int w, int lane) {
+        constexpr int kLoads = OpP::kInstr + OpQ::kInstr + (FP8 ? 1 : 0);
 #pragma unroll
         for (int p = 0; p < PS; ++p)
 #pragma unroll
             for (int q = 0; q < QS; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
         Frag pr[kRing], qc[QS];
         float sc[QS];
-        wait_loads<kLoads>();
+        wait_loads<kLoads + kBehind>();
         lds_barrier();
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) pr[i] = read_p(s0, i, w, lane);
@@ -425,37 +441,45 @@ struct TileBody {
             if constexpr (FP8) sc[q] = read_scale(s0, q, w, lane);
         }
         int step = 0;
-        for (; step + 1 < steps; step += 2) {
-            step_of(s0, s1, step, lp, lq, ls, pr, qc, sc, acc, w, lane);
-            step_of(s1, s0, step + 1, lp, lq, ls, pr, qc, sc, acc, w, lane);
+        for (; step + 1 < order.n; step += 2) {
+            step_of(s0, s1, order.at(step + 2), lp, lq, ls, pr, qc, sc, acc, w, lane);
+            step_of(s1, s0, order.at(step + 3), lp, lq, ls, pr, qc, sc, acc, w, lane);
         }
-        if (step < steps) step_of(s0, s1, step, lp, lq, ls, pr, qc, sc, acc, w, lane);
+        if (step < order.n) step_of(s0, s1, order.n, lp, lq, ls, pr, qc, sc, acc, w, lane);
         wait_loads<0>();   // nothing may be on its way into LDS when the workgroup ends
     }
 
-    // bf16 stores of the tile: out points at the tile's first output, ld its row length; i < ni, j < nj
+    // bf16 stores of the tile: out points at its first output, ld is its row length; i < ni, j < nj.  A
+    // lane holds four columns of one row: 16 rows of kCols columns at a time go through LDS, so that a
+    // store writes whole 128-byte lines (direct 8-byte stores reach them in four parts).  A row's
+    // 16-byte chunk c sits at c ^ row.
+    static constexpr int kCols = PS >= 4 ? 64 : PS * 16, kChunks = kCols / 8;
+    static constexpr int kStores = QS * (PS * 16 / kCols) * (kCols / 32);   // of one wavefront
     __device__ __forceinline__ static void store(uint16_t* out, int64_t ld, int ni, int nj, const f32x4 (&acc)[PS][QS],
-                                                 int w, int lane) {
+                                                 char* scratch, int w, int lane) {
         const int wp = w % WP, wq = w / WP, g = lane >> 4, t = lane & 15;
+        char* mine = scratch + w * 2048;
 #pragma unroll
         for (int q = 0; q < QS; ++q) {
-            const int j = wq * QS * 16 + q * 16 + t;
-            if (j >= nj) continue;
-            uint16_t* row = out + (int64_t)j * ld;
 #pragma unroll
-            for (int p = 0; p < PS; p += 2) {
-                const f32x4 x = acc[p][q], y = acc[p + 1][q];
-                auto pk = [](float lo, float hi) { return (uint32_t)bf16_bits(lo) | ((uint32_t)bf16_bits(hi) << 16); };
-                if constexpr (!PMC) {
-                    const int i = wp * PS * 16 + 16 * p + 8 * g;
-                    if (i < ni)
-                        *reinterpret_cast<i32x4*>(row + i) =
-                            i32x4{(int)pk(x[0], x[1]), (int)pk(x[2], x[3]), (int)pk(y[0], y[1]), (int)pk(y[2], y[3])};
-                } else {
-                    const int i = wp * PS * 16 + 16 * p + 4 * g;
-                    if (i < ni) *reinterpret_cast<u32x2*>(row + i) = u32x2{pk(x[0], x[1]), pk(x[2], x[3])};
-                    if (i + 16 < ni) *reinterpret_cast<u32x2*>(row + i + 16) = u32x2{pk(y[0], y[1]), pk(y[2], y[3])};
+            for (int p0 = 0; p0 < PS; p0 += kCols / 16) {
+#pragma unroll
+                for (int p = 0; p < kCols / 16; ++p) {
+                    const f32x4 v = acc[p0 + p][q];
+                    const int c = 2 * p + (g >> 1);
+                    *reinterpret_cast<u32x2*>(mine + t * kCols * 2 + (((c ^ t) & (kChunks - 1)) << 4) + (g & 1) * 8) =
+                        u32x2{(uint32_t)bf16_bits(v[0]) | ((uint32_t)bf16_bits(v[1]) << 16),
+                              (uint32_t)bf16_bits(v[2]) | ((uint32_t)bf16_bits(v[3]) << 16)};
                 }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+#pragma unroll
+                for (int k = 0; k < kCols / 32; ++k) {
+                    const int r = k * (64 / kChunks) + lane / kChunks, c = lane % kChunks;
+                    const i32x4 v = *reinterpret_cast<const i32x4*>(mine + r * kCols * 2 + (((c ^ r) & (kChunks - 1)) << 4));
+                    const int j = wq * QS * 16 + q * 16 + r, i = (wp * PS + p0) * 16 + c * 8;
+                    if (j < nj && i < ni) *reinterpret_cast<i32x4*>(out + (int64_t)j * ld + i) = v;
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
             }
         }
     }
@@ -480,7 +504,9 @@ __device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& t
     lq.init(static_cast<const char*>(a.q) + qrow * qld, qld, tl.rows, (int)qld, w, lane);
     LoadScales ls;
     f32x4 acc[B::PS][B::QS];
-    const int steps = (cdim * kSize + kStepBytes - 1) / kStepBytes;
+    // Tiles with many rows share panels in L2 and start together; those with few share little.
+    const int n = (cdim * kSize + kStepBytes - 1) / kStepBytes;
+    const Steps steps = {n, !PMC && BQ <= 64 ? (int)(blockIdx.x & 31) * n / 32 : 0};
     if constexpr (FP8) {
         const int kb = a.K / 128, nb = (a.N + 127) / 128;
         ls.init(a.q_scales + qrow * kb, tl.rows, a.p_scales + ((int64_t)tl.e * nb + i0 / 128) * kb, nb - i0 / 128, kb, w,
@@ -489,29 +515,163 @@ __device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& t
     if constexpr (PMC) {
         LoadMC<NW> lp;
         lp.init(wmat, (int64_t)a.K * 2, a.N, i0, w, lane);
-        B::run(s0, s1, lp, lq, ls, steps, acc, w, lane);
+        B::begin(s0, s1, lp, lq, ls, steps);
+        B::template run<0>(s0, s1, lp, lq, ls, steps, acc, w, lane);
     } else {
         typename B::LP lp;
         lp.init(wmat + i0 * qld, qld, ni, (int)qld, w, lane);
-        B::run(s0, s1, lp, lq, ls, steps, acc, w, lane);
+        B::begin(s0, s1, lp, lq, ls, steps);
+        B::template run<0>(s0, s1, lp, lq, ls, steps, acc, w, lane);
     }
-    B::store(static_cast<uint16_t*>(a.out) + orow * idim + i0, idim, ni, tl.rows, acc, w, lane);
+    B::store(static_cast<uint16_t*>(a.out) + orow * idim + i0, idim, ni, tl.rows, acc, s0.scratch, w, lane);
+}
+
+// ---------------------------------------------------------------- few rows
+// Narrow tiles for products with too few 256-column tiles to occupy the chip (a token or a few): 64
+// columns x 32 rows, four wavefronts, two workgroups a compute unit.  What counts here is the bytes
+// on their way from memory, so the ring has kSmallStages stages, and the matrix instructions are
+// not scheduled by hand.
+constexpr int kSmallP = 64, kSmallQ = 32, kSmallWaves = 4, kSmallStages = 6;
+
+template <bool FP8>
+struct SmallBody {
+    using LP = LoadKC<kSmallP, kSmallWaves>;
+    using LQ = LoadKC<kSmallQ, kSmallWaves>;
+    static constexpr int kScales = FP8 ? 512 : 0;
+    static constexpr int kStage = (kSmallP + kSmallQ) * kStepBytes + kScales;
+    static constexpr int kLds = kStage * kSmallStages;
+
+    // Scales of one stage: 32 rows', and the one of the tile's 128-column block at byte 256.
+    struct Scales {
+        __amdgpu_buffer_rsrc_t rsrc;
+        uint32_t voff;
+        int kb, lds;
+        __device__ __forceinline__ void init(const float* rows, int valid, const float* mat, int kblocks, int w, int lane) {
+            kb = kblocks;
+            const bool r = (w & 1) == 0;
+            rsrc = r ? descriptor(rows, (int64_t)valid * kb * 4) : descriptor(mat, (int64_t)kb * 4);
+            voff = lane < (r ? kSmallQ : 1) ? (uint32_t)(lane * kb) * 4 : kOob;
+            lds = r ? 0 : 256;
+        }
+        __device__ __forceinline__ void issue(char* stage, int step) const {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, LDS_PTR(void, stage + lds), 4, step < kb ? voff + step * 4 : kOob, 0,
+                                                     0, 0);
+        }
+    };
+
+    // Wavefront w: columns 32 (w % 2) .. +31, rows 16 (w / 2) .. +15.
+    __device__ __forceinline__ static void run(char* lds, const LP& lp, const LQ& lq, const Scales& ls, const Steps& order, int rows,
+                                               f32x4 (&acc)[2], int w, int lane) {
+        constexpr int kLoads = LP::kInstr + LQ::kInstr + (FP8 ? 1 : 0);
+        const int g = lane >> 4, t = lane & 15, wp = w & 1, wq = w >> 1;
+        auto fill = [&](int step, int slot) {
+            char* st = lds + slot * kStage;
+            const auto sp = lp.step_of(step);
+            const auto sq = lq.step_of(step);
+#pragma unroll
+            for (int l = 0; l < LP::kInstr; ++l) lp.issue(st, sp, l);
+#pragma unroll
+            for (int l = 0; l < LQ::kInstr; ++l) lq.issue(st + kSmallP * kStepBytes, sq, l);
+            if constexpr (FP8) ls.issue(st + (kSmallP + kSmallQ) * kStepBytes, step);
+        };
+        acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < kSmallStages - 1; ++s) fill(order.at(s), s);
+        int cur = 0, nxt = kSmallStages - 1;
+        for (int step = 0; step < order.n; ++step) {
+            wait_loads<(kSmallStages - 2) * kLoads>();
+            lds_barrier();   // this step has arrived, and everyone is done with the one before
+            fill(order.at(step + kSmallStages - 1), nxt);
+            const char* sp = lds + cur * kStage;
+            const char* sq = sp + kSmallP * kStepBytes;
+            if (wq * 16 < rows) {
+                if constexpr (FP8) {
+                    const char* sc = sq + kSmallQ * kStepBytes;
+                    const i32x8 q = LQ::frag8(sq, wq * 16 + t, g);
+                    const float s = *reinterpret_cast<const float*>(sc + (wq * 16 + t) * 4) *
+                                    *reinterpret_cast<const float*>(sc + 256);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            LP::frag8(sp, wp * 32 + p * 16 + t, g), q, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[p][r] = __builtin_fmaf(d[r], s, acc[p][r]);
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const bf16x8 q = LQ::frag(sq, wq * 16 + t, h * 4 + g);
+#pragma unroll
+                        for (int p = 0; p < 2; ++p)
+                            acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                LP::frag(sp, wp * 32 + p * 16 + t, h * 4 + g), q, acc[p], 0, 0, 0);
+                    }
+                }
+            }
+            cur = cur == kSmallStages - 1 ? 0 : cur + 1;
+            nxt = nxt == kSmallStages - 1 ? 0 : nxt + 1;
+        }
+        wait_loads<0>();   // nothing may be on its way into LDS when the workgroup ends
+    }
+};
+
+template <bool FP8>
+__global__ __launch_bounds__(64 * kSmallWaves) void k_expert_rows_small(ExpertGemmArgs a) {
+    using B = SmallBody<FP8>;
+    __shared__ __align__(1024) char lds[B::kLds];
+    constexpr int kSize = FP8 ? 1 : 2;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int ntiles = (a.N + kSmallP - 1) / kSmallP;
+    const Tile tl = find_tile(a.seg, blockIdx.x, kSmallQ, ntiles);
+    if (tl.e < 0) return;
+    const int i0 = tl.col * kSmallP, ni = min(kSmallP, a.N - i0);
+    const int64_t qrow = seg_base(a.seg, tl.e, tl.start, a.q_padded) + tl.row;
+    const int64_t orow = seg_base(a.seg, tl.e, tl.start, a.out_padded) + tl.row;
+    const int64_t ld = (int64_t)a.K * kSize;
+    typename B::LP lp;
+    typename B::LQ lq;
+    typename B::Scales ls;
+    lp.init(static_cast<const char*>(a.p) + ((int64_t)tl.e * a.N + i0) * ld, ld, ni, (int)ld, w, lane);
+    lq.init(static_cast<const char*>(a.q) + qrow * ld, ld, tl.rows, (int)ld, w, lane);
+    if constexpr (FP8) {
+        const int kb = a.K / 128, nb = (a.N + 127) / 128;
+        ls.init(a.q_scales + qrow * kb, tl.rows, a.p_scales + ((int64_t)tl.e * nb + i0 / 128) * kb, kb, w, lane);
+    }
+    f32x4 acc[2];
+    const int n = (int)((ld + kStepBytes - 1) / kStepBytes);
+    B::run(lds, lp, lq, ls, Steps{n, 0}, tl.rows, acc, w, lane);
+    const int j = (w >> 1) * 16 + (lane & 15);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int i = (w & 1) * 32 + p * 16 + 4 * (lane >> 4);
+        if (j < tl.rows && i < ni)
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + (orow + j) * a.N + i0 + i) =
+                u32x2{(uint32_t)bf16_bits(acc[p][0]) | ((uint32_t)bf16_bits(acc[p][1]) << 16),
+                      (uint32_t)bf16_bits(acc[p][2]) | ((uint32_t)bf16_bits(acc[p][3]) << 16)};
+    }
 }
 
 constexpr int kTileBytes = 256 * kStepBytes;   // of one operand's stage
+#ifndef KSB
+#define KSB 129
+#endif
+constexpr int64_t kSmallBelow = KSB;
+
 constexpr int kWaves = 8;   // of a workgroup (one workgroup a compute unit)
 
 template <bool FP8, bool PMC>
 __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_rows(ExpertGemmArgs a) {
     __shared__ __align__(1024) char p0[kTileBytes], p1[kTileBytes], q0[kTileBytes], q1[kTileBytes];
     __shared__ __align__(1024) char c0[FP8 ? kScaleBytes : 16], c1[FP8 ? kScaleBytes : 16];
-    const Stage s0 = {p0, q0, c0}, s1 = {p1, q1, c1};
+    __shared__ __align__(1024) char scratch[kWaves * 2048];
+    const Stage s0 = {p0, q0, c0, scratch}, s1 = {p1, q1, c1, scratch};
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int ntiles = ((PMC ? a.K : a.N) + kTileP - 1) / kTileP;
     const Tile tl = find_tile(a.seg, xcd_tile(blockIdx.x), 256, ntiles);
     if (tl.e < 0) return;
     const int i0 = tl.col * kTileP;
-    if (tl.rows > 128) rows_tile<kWaves, 256, 2, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
+    if (tl.rows > 192) rows_tile<kWaves, 256, 2, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
+    else if (tl.rows > 128) rows_tile<kWaves, 192, 2, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
     else if (tl.rows > 64) rows_tile<kWaves, 128, 4, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
     else if (tl.rows > 32) rows_tile<kWaves, 64, 4, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
     else rows_tile<kWaves, 32, 8, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
@@ -521,31 +681,48 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_rows(ExpertG
 __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad(ExpertGemmArgs a) {
     using B = TileBody<kWaves, 256, 2, false, true, true>;
     __shared__ __align__(1024) char p0[kTileBytes], p1[kTileBytes], q0[kTileBytes], q1[kTileBytes];
-    const Stage s0 = {p0, q0, nullptr}, s1 = {p1, q1, nullptr};
+    __shared__ __align__(1024) char scratch[kWaves * 2048];
+    const Stage s0 = {p0, q0, nullptr, scratch}, s1 = {p1, q1, nullptr, scratch};
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int kt = (a.K + kTileP - 1) / kTileP, nt = (a.N + 255) / 256;
-    const int64_t t0 = xcd_tile(blockIdx.x);
-    const int e = (int)(t0 / (kt * nt));
-    if (e >= a.seg.E) return;
-    int ti, tj;
-    band_order((int)(t0 - (int64_t)e * kt * nt), nt, kt, &tj, &ti);
-    const int i0 = ti * kTileP, j0 = tj * 256;
-    const int lo = a.seg.eoff[e];
-    const int rows = seg_rows(a.seg, lo, a.seg.eoff[e + 1]);
-    const int64_t prow = seg_base(a.seg, e, lo, a.p_padded), qrow = seg_base(a.seg, e, lo, a.q_padded);
+    const int64_t tiles = (int64_t)a.seg.E * kt * nt;
     LoadMC<kWaves> lp, lq;
     LoadScales ls;
-    lp.init(static_cast<const char*>(a.p) + (rows ? prow * a.K * 2 : 0), (int64_t)a.K * 2, rows, i0, w, lane);
-    lq.init(static_cast<const char*>(a.q) + (rows ? qrow * a.N * 2 : 0), (int64_t)a.N * 2, rows, j0, w, lane);
+    Steps steps;
+    int e, i0, j0;
+    auto start = [&](int64_t t) {
+        e = (int)(t / (kt * nt));
+        int ti, tj;
+        band_order((int)(t - (int64_t)e * kt * nt), nt, kt, &tj, &ti);
+        i0 = ti * kTileP;
+        j0 = tj * 256;
+        const int lo = a.seg.eoff[e];
+        const int rows = seg_rows(a.seg, lo, a.seg.eoff[e + 1]);
+        const int64_t prow = seg_base(a.seg, e, lo, a.p_padded), qrow = seg_base(a.seg, e, lo, a.q_padded);
+        lp.init(static_cast<const char*>(a.p) + (rows ? prow * a.K * 2 : 0), (int64_t)a.K * 2, rows, i0, w, lane);
+        lq.init(static_cast<const char*>(a.q) + (rows ? qrow * a.N * 2 : 0), (int64_t)a.N * 2, rows, j0, w, lane);
+        steps = Steps{(rows + kStepC - 1) / kStepC, 0};
+        B::begin(s0, s1, lp, lq, ls, steps);
+    };
+    // Each workgroup takes every 256th tile, and starts the next one's loads before it stores.
+    int64_t t = xcd_tile(blockIdx.x);
+    if (t >= tiles) return;
+    start(t);
+    for (;;) {
     f32x4 acc[B::PS][B::QS];
-    B::run(s0, s1, lp, lq, ls, (rows + kStepC - 1) / kStepC, acc, w, lane);
-    const int ni = min(kTileP, a.K - i0), nj = min(256, a.N - j0);
+    B::template run<0>(s0, s1, lp, lq, ls, steps, acc, w, lane);
     const int64_t at = ((int64_t)e * a.N + j0) * a.K + i0;
-    const int wp = w % 2, wq = w / 2, g = lane >> 4, t = lane & 15;
+    const int ni = min(kTileP, a.K - i0), nj = min(256, a.N - j0);
+    t += 256;
+    if (t < tiles) {
+        lds_barrier();   // everyone is done with the stages
+        start(t);
+    }
+    const int wp = w % 2, wq = w / 2, g = lane >> 4, tt = lane & 15;
     if (a.accumulate || a.out_f32) {
 #pragma unroll
         for (int q = 0; q < B::QS; ++q) {
-            const int j = wq * B::QS * 16 + q * 16 + t;
+            const int j = wq * B::QS * 16 + q * 16 + tt;
 #pragma unroll
             for (int p = 0; p < B::PS; ++p) {
                 const int i = wp * B::PS * 16 + 16 * p + 4 * g;
@@ -568,15 +745,34 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad
             }
         }
     } else {
-        B::store(static_cast<uint16_t*>(a.out) + at, a.K, ni, nj, acc, w, lane);
+        B::store(static_cast<uint16_t*>(a.out) + at, a.K, ni, nj, acc, s0.scratch, w, lane);
+    }
+    if (t >= tiles) return;
     }
 }
+
+// Upper bound on the tiles of a launch: every `bq` rows, and one ragged end for each expert with rows.
+int64_t tile_bound(const ExpertGemmArgs& a, int64_t pairs, int bq, int64_t ni) {
+    return (pairs / bq + (pairs < a.seg.E ? pairs : a.seg.E)) * ni;
+}
+
+// A grid holds under 2^32 threads.
+bool grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }
 
 template <bool FP8, bool PMC>
 hipError_t launch_rows(const ExpertGemmArgs& a, int64_t pairs, hipStream_t s) {
     const int64_t ntiles = ((PMC ? a.K : a.N) + kTileP - 1) / kTileP;
-    const int64_t mtiles = pairs / 256 + (pairs < a.seg.E ? pairs : a.seg.E);   // at least one expert per ragged end
-    const int64_t blocks = (mtiles * ntiles + 255) / 256 * 256;
+    const int64_t tiles = tile_bound(a, pairs, 256, ntiles);
+    if constexpr (!PMC) {
+        if (tiles < kSmallBelow) {
+            const int64_t blocks = tile_bound(a, pairs, kSmallQ, (a.N + kSmallP - 1) / kSmallP);
+            if (!grid_fits(blocks, 64 * kSmallWaves)) return hipErrorInvalidConfiguration;
+            k_expert_rows_small<FP8><<<dim3((unsigned)blocks), dim3(64 * kSmallWaves), 0, s>>>(a);
+            return hipGetLastError();
+        }
+    }
+    const int64_t blocks = (tiles + 255) / 256 * 256;
+    if (!grid_fits(blocks, 64 * kWaves)) return hipErrorInvalidConfiguration;
     k_expert_rows<FP8, PMC><<<dim3((unsigned)blocks), dim3(64 * kWaves), 0, s>>>(a);
     return hipGetLastError();
 }
@@ -592,8 +788,7 @@ hipError_t launch_expert_gemm_bwd_rows(const ExpertGemmArgs& a, int64_t pairs, h
 }
 
 hipError_t launch_expert_gemm_bwd_weights(const ExpertGemmArgs& a, hipStream_t s) {
-    const int64_t tiles = (int64_t)a.seg.E * ((a.K + kTileP - 1) / kTileP) * ((a.N + 255) / 256);
-    const int64_t blocks = (tiles + 255) / 256 * 256;
+    const int blocks = 256;   // each takes every 256th tile
     k_expert_weights_grad<<<dim3((unsigned)blocks), dim3(64 * kWaves), 0, s>>>(a);
     return hipGetLastError();
 }
