@@ -56,6 +56,7 @@ struct Tile {
     int e, row, rows;   // expert, first row within its segment, rows of the tile
     int64_t start;      // packed row of the segment's first row
     int col;            // column tile
+    bool alone;         // the expert's only row tile
 };
 
 // Block b runs on XCD b % 8, and about 256 blocks (32 for each XCD) run together: blocks of one
@@ -136,6 +137,7 @@ __device__ __forceinline__ Tile find_tile(const Segments& s, int64_t t, int bq, 
     int j;
     band_order((int)(t - (int64_t)__builtin_amdgcn_readlane(fbefore, owner) * ni), (n + bq - 1) / bq, ni, &j, &r.col);
     r.row = j * bq;
+    r.alone = n <= bq;
     r.rows = min(bq, n - r.row);
     return r;
 }
@@ -143,25 +145,26 @@ __device__ __forceinline__ Tile find_tile(const Segments& s, int64_t t, int bq, 
 // ---------------------------------------------------------------- operands
 // KC operand: ROWS rows of 128 contraction bytes a stage.  Row r, 16-byte chunk c sits at
 // r * 128 + ((c ^ (r & 7)) << 4): the eight lanes that read together meet eight different chunks.
-template <int ROWS, int NW>
+// TAIL: rows need not be whole steps.
+template <int ROWS, int NW, bool TAIL>
 struct LoadKC {
     static constexpr int kBytes = ROWS * kStepBytes;
-    static constexpr int kInstr = kBytes / 1024 >= NW ? kBytes / 1024 / NW : 1;
+    static constexpr int kInstr = (kBytes / 1024 + NW - 1) / NW;
     const char* base;
     int64_t bytes;    // of the valid rows
     uint32_t voff[kInstr];
     uint32_t chunk;   // byte offset of the lane's chunk within a stage row
-    int kbytes, lds;
+    int kbytes, lds[kInstr];
     __device__ __forceinline__ void init(const void* b, int64_t ld, int valid, int kb, int w, int lane) {
         base = static_cast<const char*>(b);
         bytes = (int64_t)valid * ld;
         kbytes = kb;
         chunk = ((lane & 7) ^ (lane >> 3)) * 16;   // an instruction covers eight rows
-        lds = (w * kInstr * 1024) % kBytes;   // a small tile's loads are repeated by several waves
 #pragma unroll
         for (int i = 0; i < kInstr; ++i) {
-            const int r = (lds >> 7) + i * 8 + (lane >> 3);
-            voff[i] = (uint32_t)(r * ld) + chunk;
+            // where the wavefronts' loads do not divide the tile, some are made twice
+            lds[i] = (w * kInstr + i) % (kBytes / 1024) * 1024;
+            voff[i] = (uint32_t)((lds[i] / kStepBytes + (lane >> 3)) * ld) + chunk;
         }
     }
     // The descriptor moves along the rows, so a lane's offsets stay the same.  What it would read past
@@ -175,8 +178,8 @@ struct LoadKC {
         return Step{descriptor(base + at, at < kbytes ? bytes - at : 0), kbytes - at};
     }
     __device__ __forceinline__ void issue(char* stage, const Step& st, int i) const {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rsrc, LDS_PTR(void, stage + (lds + i * 1024)), 16,
-                                                 (int)chunk < st.left ? voff[i] : kOob, 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rsrc, LDS_PTR(void, stage + lds[i]), 16,
+                                                 !TAIL || (int)chunk < st.left ? voff[i] : kOob, 0, 0, 0);
     }
     __device__ __forceinline__ static bf16x8 frag(const char* stage, int row, int c) {
         return *reinterpret_cast<const bf16x8*>(stage + (row * kStepBytes + ((c ^ (row & 7)) << 4)));
@@ -292,9 +295,9 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// One stage: P's tile, Q's tile, fp8's scales; and the epilogue's 2 KB for each wavefront.
+// One stage: P's tile, Q's tile, fp8's scales.
 struct Stage {
-    char *p, *q, *scales, *scratch;
+    char *p, *q, *scales;
 };
 
 // ---------------------------------------------------------------- tile body
@@ -307,15 +310,15 @@ struct Stage {
 // every wavefront is done with it and that the other stage has arrived; the remaining groups issue
 // the loads that refill the freed stage, for two steps on, and read the first fragments of the other.
 // So nothing is waited for but loads that had a step's time to arrive.
-template <int NW, int BQ, int WP, bool FP8, bool PMC, bool QMC>
+template <int NW, int BQ, int WP, int STAGES, bool FP8, bool PMC, bool QMC>
 struct TileBody {
     static_assert(WP <= NW, "");
     static constexpr int WQ = NW / WP;
     static constexpr int PS = kTileP / WP / 16, QS = BQ / WQ / 16;
     static_assert((PS == 2 || PS % 4 == 0) && QS >= 1, "");
 
-    using LP = LoadKC<kTileP, NW>;
-    using LQ = LoadKC<BQ, NW>;
+    using LP = LoadKC<kTileP, NW, !FP8>;
+    using LQ = LoadKC<BQ, NW, !FP8>;
     using MC = LoadMC<NW>;
     using Frag = typename std::conditional<FP8, i32x8, bf16x8>::type;
 
@@ -358,7 +361,7 @@ struct TileBody {
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             if (i == kBefore) {
-                wait_loads<0>();
+                wait_loads<(STAGES - 2) * kLoads>();
                 lds_barrier();
             }
             if (i < kBefore) {
@@ -403,27 +406,26 @@ struct TileBody {
         }
     }
 
-    // The stages are distinct LDS arrays: so the compiler knows that reads of one do not wait for loads
-    // into the other.  begin() starts the loads of a tile's first two steps, run() does the rest.
+    // The stages' P tiles are distinct LDS arrays: so the compiler knows that reads of one do not wait for
+    // loads into another.  begin() starts the loads of a tile's first steps, run() does the rest.
     template <class OpP, class OpQ>
-    __device__ __forceinline__ static void begin(const Stage& s0, const Stage& s1, const OpP& lp, const OpQ& lq,
+    __device__ __forceinline__ static void begin(const Stage (&st)[STAGES], const OpP& lp, const OpQ& lq,
                                                  const LoadScales& ls, const Steps& order) {
-        auto fill = [&](const Stage& st, int step) {
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s) {
+            const int step = order.at(s);
             const auto sp = lp.step_of(step);
             const auto sq = lq.step_of(step);
 #pragma unroll
-            for (int l = 0; l < OpP::kInstr; ++l) lp.issue(st.p, sp, l);
+            for (int l = 0; l < OpP::kInstr; ++l) lp.issue(st[s].p, sp, l);
 #pragma unroll
-            for (int l = 0; l < OpQ::kInstr; ++l) lq.issue(st.q, sq, l);
-            if constexpr (FP8) ls.issue(st.scales, step);
-        };
-        fill(s0, order.at(0));
-        fill(s1, order.at(1));
+            for (int l = 0; l < OpQ::kInstr; ++l) lq.issue(st[s].q, sq, l);
+            if constexpr (FP8) ls.issue(st[s].scales, step);
+        }
     }
-    // kBehind: loads and stores issued after the second step's loads
-    template <int kBehind, class OpP, class OpQ>
-    __device__ __forceinline__ static void run(const Stage& s0, const Stage& s1, const OpP& lp, const OpQ& lq,
-                                               const LoadScales& ls, const Steps& order, f32x4 (&acc)[PS][QS], int w, int lane) {
+    template <class OpP, class OpQ>
+    __device__ __forceinline__ static void run(const Stage (&st)[STAGES], const OpP& lp, const OpQ& lq, const LoadScales& ls,
+                                               const Steps& order, f32x4 (&acc)[PS][QS], int w, int lane) {
         constexpr int kLoads = OpP::kInstr + OpQ::kInstr + (FP8 ? 1 : 0);
 #pragma unroll
         for (int p = 0; p < PS; ++p)
@@ -431,22 +433,27 @@ struct TileBody {
             for (int q = 0; q < QS; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
         Frag pr[kRing], qc[QS];
         float sc[QS];
-        wait_loads<kLoads + kBehind>();
+        wait_loads<(STAGES - 1) * kLoads>();
         lds_barrier();
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) pr[i] = read_p(s0, i, w, lane);
+        for (int i = 0; i < kAhead; ++i) pr[i] = read_p(st[0], i, w, lane);
 #pragma unroll
         for (int q = 0; q < QS; ++q) {
-            qc[q] = read_q(s0, 0, q, w, lane);
-            if constexpr (FP8) sc[q] = read_scale(s0, q, w, lane);
+            qc[q] = read_q(st[0], 0, q, w, lane);
+            if constexpr (FP8) sc[q] = read_scale(st[0], q, w, lane);
         }
+        // A stage is known at compile time, so the loop takes STAGES steps a turn; leaving it in the
+        // middle would give the accumulators two sets of registers.
         int step = 0;
-        for (; step + 1 < order.n; step += 2) {
-            step_of(s0, s1, order.at(step + 2), lp, lq, ls, pr, qc, sc, acc, w, lane);
-            step_of(s1, s0, order.at(step + 3), lp, lq, ls, pr, qc, sc, acc, w, lane);
+        for (; step + STAGES - 1 < order.n; step += STAGES) {
+#pragma unroll
+            for (int s = 0; s < STAGES; ++s)
+                step_of(st[s], st[(s + 1) % STAGES], order.at(step + s + STAGES), lp, lq, ls, pr, qc, sc, acc, w, lane);
         }
-        if (step < order.n) step_of(s0, s1, order.n, lp, lq, ls, pr, qc, sc, acc, w, lane);
-        wait_loads<0>();   // nothing may be on its way into LDS when the workgroup ends
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s)
+            if (step + s < order.n) step_of(st[s], st[s + 1], order.n, lp, lq, ls, pr, qc, sc, acc, w, lane);
+        wait_loads<0>();   // nothing may be on its way into LDS when the stages are used again
     }
 
     // bf16 stores of the tile: out points at its first output, ld is its row length; i < ni, j < nj.  A
@@ -477,7 +484,7 @@ struct TileBody {
                     const int r = k * (64 / kChunks) + lane / kChunks, c = lane % kChunks;
                     const i32x4 v = *reinterpret_cast<const i32x4*>(mine + r * kCols * 2 + (((c ^ r) & (kChunks - 1)) << 4));
                     const int j = wq * QS * 16 + q * 16 + r, i = (wp * PS + p0) * 16 + c * 8;
-                    if (j < nj && i < ni) *reinterpret_cast<i32x4*>(out + (int64_t)j * ld + i) = v;
+                    if (j < nj && i < ni) __builtin_nontemporal_store(v, reinterpret_cast<i32x4*>(out + (int64_t)j * ld + i));
                 }
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
             }
@@ -488,11 +495,10 @@ struct TileBody {
 // ---------------------------------------------------------------- rows products
 // A tile of the forward or the rows gradient: rows [row, row + rows) of expert
 // e against output columns [i0, i0 + 256).
-template <int NW, int BQ, int WP, bool FP8, bool PMC>
-__device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& tl, int i0, const Stage& s0,
-                                          const Stage& s1, int w,
-                                          int lane) {
-    using B = TileBody<NW, BQ, WP, FP8, PMC, false>;
+template <int NW, int BQ, int WP, int STAGES, bool FP8, bool PMC>
+__device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& tl, int i0, const Stage (&st)[STAGES],
+                                          char* scratch, int w, int lane) {
+    using B = TileBody<NW, BQ, WP, STAGES, FP8, PMC, false>;
     constexpr int kSize = FP8 ? 1 : 2;
     const int cdim = PMC ? a.N : a.K, idim = PMC ? a.K : a.N;
     const int64_t qrow = seg_base(a.seg, tl.e, tl.start, a.q_padded) + tl.row;
@@ -504,9 +510,9 @@ __device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& t
     lq.init(static_cast<const char*>(a.q) + qrow * qld, qld, tl.rows, (int)qld, w, lane);
     LoadScales ls;
     f32x4 acc[B::PS][B::QS];
-    // Tiles with many rows share panels in L2 and start together; those with few share little.
+    // Tiles that share a matrix panel in L2 start together.
     const int n = (cdim * kSize + kStepBytes - 1) / kStepBytes;
-    const Steps steps = {n, !PMC && BQ <= 64 ? (int)(blockIdx.x & 31) * n / 32 : 0};
+    const Steps steps = {n, !PMC && tl.alone ? (int)(blockIdx.x & 31) * n / 32 : 0};
     if constexpr (FP8) {
         const int kb = a.K / 128, nb = (a.N + 127) / 128;
         ls.init(a.q_scales + qrow * kb, tl.rows, a.p_scales + ((int64_t)tl.e * nb + i0 / 128) * kb, nb - i0 / 128, kb, w,
@@ -515,15 +521,16 @@ __device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& t
     if constexpr (PMC) {
         LoadMC<NW> lp;
         lp.init(wmat, (int64_t)a.K * 2, a.N, i0, w, lane);
-        B::begin(s0, s1, lp, lq, ls, steps);
-        B::template run<0>(s0, s1, lp, lq, ls, steps, acc, w, lane);
+        B::begin(st, lp, lq, ls, steps);
+        B::run(st, lp, lq, ls, steps, acc, w, lane);
     } else {
         typename B::LP lp;
         lp.init(wmat + i0 * qld, qld, ni, (int)qld, w, lane);
-        B::begin(s0, s1, lp, lq, ls, steps);
-        B::template run<0>(s0, s1, lp, lq, ls, steps, acc, w, lane);
+        B::begin(st, lp, lq, ls, steps);
+        B::run(st, lp, lq, ls, steps, acc, w, lane);
     }
-    B::store(static_cast<uint16_t*>(a.out) + orow * idim + i0, idim, ni, tl.rows, acc, s0.scratch, w, lane);
+    lds_barrier();   // the epilogue's LDS was a stage
+    B::store(static_cast<uint16_t*>(a.out) + orow * idim + i0, idim, ni, tl.rows, acc, scratch, w, lane);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -535,8 +542,8 @@ constexpr int kSmallP = 64, kSmallQ = 32, kSmallWaves = 4, kSmallStages = 6;
 
 template <bool FP8>
 struct SmallBody {
-    using LP = LoadKC<kSmallP, kSmallWaves>;
-    using LQ = LoadKC<kSmallQ, kSmallWaves>;
+    using LP = LoadKC<kSmallP, kSmallWaves, !FP8>;
+    using LQ = LoadKC<kSmallQ, kSmallWaves, !FP8>;
     static constexpr int kScales = FP8 ? 512 : 0;
     static constexpr int kStage = (kSmallP + kSmallQ) * kStepBytes + kScales;
     static constexpr int kLds = kStage * kSmallStages;
@@ -661,28 +668,53 @@ constexpr int kWaves = 8;   // of a workgroup (one workgroup a compute unit)
 
 template <bool FP8, bool PMC>
 __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_rows(ExpertGemmArgs a) {
-    __shared__ __align__(1024) char p0[kTileBytes], p1[kTileBytes], q0[kTileBytes], q1[kTileBytes];
-    __shared__ __align__(1024) char c0[FP8 ? kScaleBytes : 16], c1[FP8 ? kScaleBytes : 16];
-    __shared__ __align__(1024) char scratch[kWaves * 2048];
-    const Stage s0 = {p0, q0, c0, scratch}, s1 = {p1, q1, c1, scratch};
+    // Two stages of up to 256 rows, or three of up to kThree; the epilogue uses a part.  The compiler
+    // orders LDS reads after the loads into LDS that it takes to reach them: plain reads where it knows
+    // one array for both, transposing reads also where it knows none.  Which loads have arrived is what
+    // the waits in step_of() say; to keep it from waiting for more, plain reads see one unnamed block
+    // and transposing ones an array for each stage and operand.
+    constexpr int kThree = PMC ? 64 : 160, kQ = kThree * kStepBytes;
+    Stage two[2], three[3];
+    if constexpr (PMC) {
+        __shared__ __align__(1024) char p0[kTileBytes], p1[kTileBytes], r0[kTileBytes], r1[kTileBytes], q0[kQ], q1[kQ], q2[kQ];
+        two[0] = {p0, r0, nullptr};
+        two[1] = {p1, r1, nullptr};
+        three[0] = {p0, q0, nullptr};
+        three[1] = {p1, q1, nullptr};
+        three[2] = {r0, q2, nullptr};
+    } else {
+        constexpr int kC = FP8 ? kScaleBytes : 0;
+        __shared__ __align__(1024) char lds[3 * (kTileBytes + kQ + kC)];
+        static_assert(3 * kQ >= kTileBytes, "");
+        char *q = lds + 3 * kTileBytes, *c = q + 3 * kQ;
+        two[0] = {lds, lds + 2 * kTileBytes, c};
+        two[1] = {lds + kTileBytes, q, c + kC};
+        three[0] = {lds, q, c};
+        three[1] = {lds + kTileBytes, q + kQ, c + kC};
+        three[2] = {lds + 2 * kTileBytes, q + 2 * kQ, c + 2 * kC};
+    }
+    static_assert(kTileBytes >= kWaves * 2048, "");
+    char* scratch = two[0].p;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int ntiles = ((PMC ? a.K : a.N) + kTileP - 1) / kTileP;
     const Tile tl = find_tile(a.seg, xcd_tile(blockIdx.x), 256, ntiles);
     if (tl.e < 0) return;
     const int i0 = tl.col * kTileP;
-    if (tl.rows > 192) rows_tile<kWaves, 256, 2, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
-    else if (tl.rows > 128) rows_tile<kWaves, 192, 2, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
-    else if (tl.rows > 64) rows_tile<kWaves, 128, 4, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
-    else if (tl.rows > 32) rows_tile<kWaves, 64, 4, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
-    else rows_tile<kWaves, 32, 8, FP8, PMC>(a, tl, i0, s0, s1, w, lane);
+    if (tl.rows > 192) rows_tile<kWaves, 256, 2, 2, FP8, PMC>(a, tl, i0, two, scratch, w, lane);
+    else if (tl.rows > (PMC ? 128 : 160)) rows_tile<kWaves, 192, 2, 2, FP8, PMC>(a, tl, i0, two, scratch, w, lane);
+    else if (!PMC && tl.rows > 128) rows_tile<kWaves, PMC ? 64 : 160, 4, 3, FP8, PMC>(a, tl, i0, three, scratch, w, lane);
+    else if (PMC && tl.rows > 64) rows_tile<kWaves, 128, 4, 2, FP8, PMC>(a, tl, i0, two, scratch, w, lane);
+    else if (tl.rows > 64) rows_tile<kWaves, PMC ? 64 : 128, 4, 3, FP8, PMC>(a, tl, i0, three, scratch, w, lane);
+    else if (tl.rows > 32) rows_tile<kWaves, 64, 4, 3, FP8, PMC>(a, tl, i0, three, scratch, w, lane);
+    else rows_tile<kWaves, 32, 8, 3, FP8, PMC>(a, tl, i0, three, scratch, w, lane);
 }
 
 // ---------------------------------------------------------------- weights gradient
 __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad(ExpertGemmArgs a) {
-    using B = TileBody<kWaves, 256, 2, false, true, true>;
+    using B = TileBody<kWaves, 256, 2, 2, false, true, true>;
     __shared__ __align__(1024) char p0[kTileBytes], p1[kTileBytes], q0[kTileBytes], q1[kTileBytes];
     __shared__ __align__(1024) char scratch[kWaves * 2048];
-    const Stage s0 = {p0, q0, nullptr, scratch}, s1 = {p1, q1, nullptr, scratch};
+    const Stage st[2] = {{p0, q0, nullptr}, {p1, q1, nullptr}};
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int kt = (a.K + kTileP - 1) / kTileP, nt = (a.N + 255) / 256;
     const int64_t tiles = (int64_t)a.seg.E * kt * nt;
@@ -690,7 +722,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad
     LoadScales ls;
     Steps steps;
     int e, i0, j0;
-    auto start = [&](int64_t t) {
+    auto start = [&](int64_t t, int ln) {
         e = (int)(t / (kt * nt));
         int ti, tj;
         band_order((int)(t - (int64_t)e * kt * nt), nt, kt, &tj, &ti);
@@ -699,26 +731,28 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad
         const int lo = a.seg.eoff[e];
         const int rows = seg_rows(a.seg, lo, a.seg.eoff[e + 1]);
         const int64_t prow = seg_base(a.seg, e, lo, a.p_padded), qrow = seg_base(a.seg, e, lo, a.q_padded);
-        lp.init(static_cast<const char*>(a.p) + (rows ? prow * a.K * 2 : 0), (int64_t)a.K * 2, rows, i0, w, lane);
-        lq.init(static_cast<const char*>(a.q) + (rows ? qrow * a.N * 2 : 0), (int64_t)a.N * 2, rows, j0, w, lane);
+        lp.init(static_cast<const char*>(a.p) + (rows ? prow * a.K * 2 : 0), (int64_t)a.K * 2, rows, i0, w, ln);
+        lq.init(static_cast<const char*>(a.q) + (rows ? qrow * a.N * 2 : 0), (int64_t)a.N * 2, rows, j0, w, ln);
         steps = Steps{(rows + kStepC - 1) / kStepC, 0};
-        B::begin(s0, s1, lp, lq, ls, steps);
+        B::begin(st, lp, lq, ls, steps);
     };
     // Each workgroup takes every 256th tile, and starts the next one's loads before it stores.
     int64_t t = xcd_tile(blockIdx.x);
     if (t >= tiles) return;
-    start(t);
+    start(t, lane);
     for (;;) {
     f32x4 acc[B::PS][B::QS];
-    B::template run<0>(s0, s1, lp, lq, ls, steps, acc, w, lane);
+    B::run(st, lp, lq, ls, steps, acc, w, lane);
     const int64_t at = ((int64_t)e * a.N + j0) * a.K + i0;
     const int ni = min(kTileP, a.K - i0), nj = min(256, a.N - j0);
     t += 256;
+    int ln = lane;
+    asm volatile("" : "+v"(ln));   // what depends on the lane is computed anew: kept over the loop it would spill
     if (t < tiles) {
         lds_barrier();   // everyone is done with the stages
-        start(t);
+        start(t, ln);
     }
-    const int wp = w % 2, wq = w / 2, g = lane >> 4, tt = lane & 15;
+    const int wp = w % 2, wq = w / 2, g = ln >> 4, tt = ln & 15;
     if (a.accumulate || a.out_f32) {
 #pragma unroll
         for (int q = 0; q < B::QS; ++q) {
@@ -745,7 +779,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad
             }
         }
     } else {
-        B::store(static_cast<uint16_t*>(a.out) + at, a.K, ni, nj, acc, s0.scratch, w, lane);
+        B::store(static_cast<uint16_t*>(a.out) + at, a.K, ni, nj, acc, scratch, w, ln);
     }
     if (t >= tiles) return;
     }
