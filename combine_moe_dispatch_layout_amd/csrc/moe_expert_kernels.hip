@@ -46,9 +46,10 @@ __device__ __forceinline__ uint16_t bf16_bits(float f) {
     return __builtin_bit_cast(uint16_t, (__bf16)f);   // round to nearest even
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const void* p, int64_t bytes) {
-    const int64_t n = bytes < 0 ? 0 : (bytes > 0x7fffffff ? 0x7fffffff : bytes);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)n, 0x00020000);
+// Every descriptor covers one stage of one tile, at most 256 rows of 2 * MOE_MAX_FEATURES bytes.
+static_assert(256ll * 2 * MOE_MAX_FEATURES < kOob, "");
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const void* p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, max(bytes, 0), 0x00020000);
 }
 
 // ---------------------------------------------------------------- segments
@@ -151,20 +152,20 @@ struct LoadKC {
     static constexpr int kBytes = ROWS * kStepBytes;
     static constexpr int kInstr = (kBytes / 1024 + NW - 1) / NW;
     const char* base;
-    int64_t bytes;    // of the valid rows
+    int bytes;        // of the valid rows
     uint32_t voff[kInstr];
     uint32_t chunk;   // byte offset of the lane's chunk within a stage row
     int kbytes, lds[kInstr];
-    __device__ __forceinline__ void init(const void* b, int64_t ld, int valid, int kb, int w, int lane) {
+    __device__ __forceinline__ void init(const void* b, int ld, int valid, int kb, int w, int lane) {
         base = static_cast<const char*>(b);
-        bytes = (int64_t)valid * ld;
+        bytes = valid * ld;
         kbytes = kb;
         chunk = ((lane & 7) ^ (lane >> 3)) * 16;   // an instruction covers eight rows
 #pragma unroll
         for (int i = 0; i < kInstr; ++i) {
             // where the wavefronts' loads do not divide the tile, some are made twice
             lds[i] = (w * kInstr + i) % (kBytes / 1024) * 1024;
-            voff[i] = (uint32_t)((lds[i] / kStepBytes + (lane >> 3)) * ld) + chunk;
+            voff[i] = (lds[i] / kStepBytes + (lane >> 3)) * ld + chunk;
         }
     }
     // The descriptor moves along the rows, so a lane's offsets stay the same.  What it would read past
@@ -205,28 +206,28 @@ struct LoadMC {
     static constexpr int kBytes = kStepC * 512;
     static constexpr int kInstr = kBytes / 1024 / NW;
     const char* base;
-    int64_t ld, left;   // bytes of a contraction row; bytes from base to the operand's end
+    int ld, crows, before;   // bytes of a contraction row, contraction rows, bytes of a row before the tile
     uint32_t voff[kInstr];
     int lds;
-    // base: first contraction row, at the tile's first column; cols: columns from there to the row's end
-    __device__ __forceinline__ void init(const void* b, int64_t row_bytes, int64_t crows, int64_t col0, int w, int lane) {
-        base = static_cast<const char*>(b) + col0 * 2;
+    __device__ __forceinline__ void init(const void* b, int row_bytes, int n, int col0, int w, int lane) {
+        before = col0 * 2;
+        base = static_cast<const char*>(b) + before;
         ld = row_bytes;
-        left = crows * row_bytes - col0 * 2;
+        crows = n;
         lds = w * kInstr * 1024;
 #pragma unroll
         for (int i = 0; i < kInstr; ++i) {
             const int c = (w * kInstr + i) * 2 + (lane >> 5), p = lane & 31;
             const int chunk = (((p >> 1) ^ mc_key(c)) << 1) | (p & 1);
-            voff[i] = col0 * 2 + chunk * 16 < row_bytes ? (uint32_t)(c * row_bytes) + chunk * 16 : kOob;
+            voff[i] = before + chunk * 16 < row_bytes ? (uint32_t)(c * row_bytes) + chunk * 16 : kOob;
         }
     }
     struct Step {
         __amdgpu_buffer_rsrc_t rsrc;
     };
     __device__ __forceinline__ Step step_of(int step) const {
-        const int64_t at = (int64_t)step * kStepC * ld;
-        return Step{descriptor(base + at, left - at)};
+        const int c0 = step * kStepC;
+        return Step{descriptor(base + (int64_t)c0 * ld, min(crows - c0, kStepC) * ld - before)};
     }
     __device__ __forceinline__ void issue(char* stage, const Step& st, int i) const {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rsrc, LDS_PTR(void, stage + (lds + i * 1024)), 16, voff[i], 0, 0,
@@ -254,11 +255,11 @@ struct LoadScales {
                                          int w, int lane) {
         kb = kblocks;
         if (w < 4) {
-            rsrc = descriptor(rows, (int64_t)valid * kb * 4);
+            rsrc = descriptor(rows, valid * kb * 4);
             voff = (uint32_t)((w * 64 + lane) * kb) * 4;
             lds = w * 256;
         } else {
-            rsrc = descriptor(mats, (int64_t)min(nblocks, 2) * kb * 4);
+            rsrc = descriptor(mats, min(nblocks, 2) * kb * 4);
             voff = lane < 2 ? (uint32_t)(lane * kb) * 4 : kOob;
             lds = 1024;
         }
@@ -386,21 +387,28 @@ struct TileBody {
                 }
             }
             const int p = i % PS;
+            if constexpr (FP8) {
+                f32x4 d[QS];
 #pragma unroll
-            for (int q = 0; q < QS; ++q) {
-                if constexpr (FP8) {
-                    const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        pr[i % kRing], qc[q], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[p][q][r] = __builtin_fmaf(d[r], sc[q], acc[p][q][r]);
+                for (int q = 0; q < QS; ++q) {
+                    d[q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pr[i % kRing], qc[q], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0,
+                                                                            0, 0, 0, 0);
                     if (i == kGroups - 1) {   // this fragment was used for the last time
+                        __builtin_amdgcn_sched_barrier(0);
                         qc[q] = read_q(nxt, 0, q, w, lane);
-                        sc[q] = read_scale(nxt, q, w, lane);
                     }
-                } else {
+                }
+#pragma unroll
+                for (int q = 0; q < QS; ++q) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[p][q][r] = __builtin_fmaf(d[q][r], sc[q], acc[p][q][r]);
+                    if (i == kGroups - 1) sc[q] = read_scale(nxt, q, w, lane);
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < QS; ++q)
                     acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pr[i % kRing], i < PS ? qc[q] : qn[q], acc[p][q],
                                                                        0, 0, 0);
-                }
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -450,9 +458,11 @@ struct TileBody {
             for (int s = 0; s < STAGES; ++s)
                 step_of(st[s], st[(s + 1) % STAGES], order.at(step + s + STAGES), lp, lq, ls, pr, qc, sc, acc, w, lane);
         }
-#pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s)
-            if (step + s < order.n) step_of(st[s], st[s + 1], order.n, lp, lq, ls, pr, qc, sc, acc, w, lane);
+        if (step < order.n) {
+            step_of(st[0], st[1], order.n, lp, lq, ls, pr, qc, sc, acc, w, lane);
+            if (STAGES > 2 && step + 1 < order.n)
+                step_of(st[1], st[2 % STAGES], order.n, lp, lq, ls, pr, qc, sc, acc, w, lane);
+        }
         wait_loads<0>();   // nothing may be on its way into LDS when the stages are used again
     }
 
@@ -507,7 +517,7 @@ __device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& t
     const char* wmat = static_cast<const char*>(a.p) + (int64_t)tl.e * a.N * a.K * kSize;
     const int64_t qld = (int64_t)cdim * kSize;
     typename B::LQ lq;
-    lq.init(static_cast<const char*>(a.q) + qrow * qld, qld, tl.rows, (int)qld, w, lane);
+    lq.init(static_cast<const char*>(a.q) + qrow * qld, (int)qld, tl.rows, (int)qld, w, lane);
     LoadScales ls;
     f32x4 acc[B::PS][B::QS];
     // Tiles that share a matrix panel in L2 start together.
@@ -520,12 +530,12 @@ __device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& t
     }
     if constexpr (PMC) {
         LoadMC<NW> lp;
-        lp.init(wmat, (int64_t)a.K * 2, a.N, i0, w, lane);
+        lp.init(wmat, a.K * 2, a.N, i0, w, lane);
         B::begin(st, lp, lq, ls, steps);
         B::run(st, lp, lq, ls, steps, acc, w, lane);
     } else {
         typename B::LP lp;
-        lp.init(wmat + i0 * qld, qld, ni, (int)qld, w, lane);
+        lp.init(wmat + i0 * qld, (int)qld, ni, (int)qld, w, lane);
         B::begin(st, lp, lq, ls, steps);
         B::run(st, lp, lq, ls, steps, acc, w, lane);
     }
@@ -556,7 +566,7 @@ struct SmallBody {
         __device__ __forceinline__ void init(const float* rows, int valid, const float* mat, int kblocks, int w, int lane) {
             kb = kblocks;
             const bool r = (w & 1) == 0;
-            rsrc = r ? descriptor(rows, (int64_t)valid * kb * 4) : descriptor(mat, (int64_t)kb * 4);
+            rsrc = r ? descriptor(rows, valid * kb * 4) : descriptor(mat, kb * 4);
             voff = lane < (r ? kSmallQ : 1) ? (uint32_t)(lane * kb) * 4 : kOob;
             lds = r ? 0 : 256;
         }
@@ -638,8 +648,8 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_expert_rows_small(ExpertGe
     typename B::LP lp;
     typename B::LQ lq;
     typename B::Scales ls;
-    lp.init(static_cast<const char*>(a.p) + ((int64_t)tl.e * a.N + i0) * ld, ld, ni, (int)ld, w, lane);
-    lq.init(static_cast<const char*>(a.q) + qrow * ld, ld, tl.rows, (int)ld, w, lane);
+    lp.init(static_cast<const char*>(a.p) + ((int64_t)tl.e * a.N + i0) * ld, (int)ld, ni, (int)ld, w, lane);
+    lq.init(static_cast<const char*>(a.q) + qrow * ld, (int)ld, tl.rows, (int)ld, w, lane);
     if constexpr (FP8) {
         const int kb = a.K / 128, nb = (a.N + 127) / 128;
         ls.init(a.q_scales + qrow * kb, tl.rows, a.p_scales + ((int64_t)tl.e * nb + i0 / 128) * kb, kb, w, lane);
@@ -731,8 +741,8 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad
         const int lo = a.seg.eoff[e];
         const int rows = seg_rows(a.seg, lo, a.seg.eoff[e + 1]);
         const int64_t prow = seg_base(a.seg, e, lo, a.p_padded), qrow = seg_base(a.seg, e, lo, a.q_padded);
-        lp.init(static_cast<const char*>(a.p) + (rows ? prow * a.K * 2 : 0), (int64_t)a.K * 2, rows, i0, w, ln);
-        lq.init(static_cast<const char*>(a.q) + (rows ? qrow * a.N * 2 : 0), (int64_t)a.N * 2, rows, j0, w, ln);
+        lp.init(static_cast<const char*>(a.p) + (rows ? prow * a.K * 2 : 0), a.K * 2, rows, i0, w, ln);
+        lq.init(static_cast<const char*>(a.q) + (rows ? qrow * a.N * 2 : 0), a.N * 2, rows, j0, w, ln);
         steps = Steps{(rows + kStepC - 1) / kStepC, 0};
         B::begin(st, lp, lq, ls, steps);
     };
