@@ -40,7 +40,6 @@ constexpr int kStepBytes = 128;          // contraction bytes of a KC stage row:
 constexpr int kStepC = 64;               // contraction elements of a bf16 stage
 constexpr int kTileP = 256;              // i extent of a tile
 constexpr uint32_t kOob = 0x80000000u;   // past the end of every descriptor (they hold under 2^31 bytes)
-constexpr int kScaleBytes = 1024 + 256;  // fp8: 256 row scales and the tile's weight scales, per stage
 
 __device__ __forceinline__ uint16_t bf16_bits(float f) {
     return __builtin_bit_cast(uint16_t, (__bf16)f);   // round to nearest even
@@ -244,41 +243,59 @@ struct LoadMC {
     }
 };
 
-// fp8: one row scale for each of 256 rows and the weight scales of the tile's
-// two 128-column blocks, for one 128-channel stage.  Waves 0-3 (and again 4-7,
-// with the weight scales) issue one 4-byte load per lane.
-struct LoadScales {
-    __amdgpu_buffer_rsrc_t rsrc;
-    uint32_t voff;
-    int kb, lds;
-    __device__ __forceinline__ void init(const float* rows, int valid, const float* mats, int nblocks, int kblocks,
-                                         int w, int lane) {
-        kb = kblocks;
-        if (w < 4) {
-            rsrc = descriptor(rows, valid * kb * 4);
-            voff = (uint32_t)((w * 64 + lane) * kb) * 4;
-            lds = w * 256;
-        } else {
-            rsrc = descriptor(mats, min(nblocks, 2) * kb * 4);
-            voff = lane < 2 ? (uint32_t)(lane * kb) * 4 : kOob;
-            lds = 1024;
-        }
-    }
-    __device__ __forceinline__ void issue(char* stage, int step) const {
-        const uint32_t v = step < kb ? voff + step * 4 : kOob;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, LDS_PTR(void, stage + lds), 4, v, 0, 0, 0);
-    }
-};
-
 // The steps of a tile in the order they are taken: from `start` to the end, then from 0.  Rows of
 // matrices whose length is a power of two lie on few memory channels at one column; tiles that start
 // at different columns spread over all of them.
 struct Steps {
     int n, start;
+    // Arithmetic instead of conditions: for those the compiler branches, and moves the matrix results'
+    // scaling past the branch, into more registers than there are.
+    __device__ __forceinline__ static int not_below(int a, int b) { return (b - 1 - a) >> 31; }   // a >= b ? -1 : 0
+    __device__ __forceinline__ static int select(int mask, int yes, int no) { return no ^ ((no ^ yes) & mask); }
     // step of the s-th turn; past the end a step that reads nothing
     __device__ __forceinline__ int at(int s) const {
         const int k = s + start;
-        return s < n ? (k < n ? k : k - n) : n;
+        return select(not_below(s, n), n, k - (n & not_below(k, n)));
+    }
+    // turn s's run of four steps 4 i .. 4 i + 3, counted in the order they are taken (start % 4 == 0)
+    __device__ __forceinline__ int four(int s) const {
+        return select(not_below(s + start, n), ((n - start + 3) >> 2) + ((s + start - n) >> 2), s >> 2);
+    }
+};
+
+// fp8: the scales of the tile's rows and of its two 128-column blocks, for four steps at a time (one
+// load a lane and step costs 9% of the prefill product).  Two runs of four are held: row r's at
+// (run % 2) * 4096 + r * 16, the blocks' at 8192 + (run % 2) * 1024.  A run that passes a row's end
+// reads the next row's, which no step uses; past the last row the loads return zeros, dword by dword.
+struct LoadScales {
+    static constexpr int kBytes = 2 * 4096 + 2 * 1024;
+    __amdgpu_buffer_rsrc_t rsrc;
+    char* lds;
+    uint32_t voff;
+    int at, slot, dump;
+    // wavefronts 0-3 load the rows', 4-7 all the blocks'; dump: where 1 KB relative to `to` is free
+    __device__ __forceinline__ void init(const float* rows, int valid, const float* mats, int nblocks, int kblocks, char* to,
+                                         int unused, int w, int lane) {
+        lds = to;
+        dump = unused;
+        rsrc = w < 4 ? descriptor(rows, valid * kblocks * 4) : descriptor(mats, min(nblocks, 2) * kblocks * 4);
+        voff = (uint32_t)((w < 4 ? w * 64 + lane : lane) * kblocks * 4);
+        at = w < 4 ? w * 1024 : 8192;
+        slot = w < 4 ? 4096 : 1024;
+    }
+    // The loads of turn s where it begins a run; else loads that read nothing.
+    __device__ __forceinline__ void issue(const Steps& order, int s) const {
+        const int k = order.at(s);
+        const int begins = ~Steps::not_below(s, order.n) & (((k & 3) - 1) >> 31);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rsrc, LDS_PTR(void, lds + Steps::select(begins, at + (order.four(s) & 1) * slot, dump)), 16,
+            (voff + k * 4) | (kOob & ~begins), 0, 0, 0);
+    }
+    // turn s's scale of a row times that of a column block
+    __device__ __forceinline__ float read(const Steps& order, int s, int row, int block) const {
+        const int run = order.four(s) & 1, k = (order.at(s) & 3) * 4;
+        return *reinterpret_cast<const float*>(lds + (run * 4096 + k + row * 16)) *
+               *reinterpret_cast<const float*>(lds + (8192 + run * 1024 + k + block * 16));
     }
 };
 
@@ -296,9 +313,9 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// One stage: P's tile, Q's tile, fp8's scales.
+// One stage: P's tile and Q's.
 struct Stage {
-    char *p, *q, *scales;
+    char *p, *q;
 };
 
 // ---------------------------------------------------------------- tile body
@@ -341,21 +358,21 @@ struct TileBody {
         else if constexpr (QMC) return MC::frag(st.q, wq * QS + q, h * 32, lane);
         else return LQ::frag(st.q, wq * QS * 16 + q * 16 + t, h * 4 + g);
     }
-    // fp8: the product of the scales of Q's row and of P's 128-column block
-    __device__ __forceinline__ static float read_scale(const Stage& st, int q, int w, int lane) {
-        return *reinterpret_cast<const float*>(st.scales + ((w / WP) * QS * 16 + q * 16 + (lane & 15)) * 4) *
-               *reinterpret_cast<const float*>(st.scales + (1024 + (w % WP) * (kTileP / WP) / 128 * 4));
+    __device__ __forceinline__ static float read_scale(const LoadScales& ls, const Steps& order, int turn, int q, int w,
+                                                       int lane) {
+        return ls.read(order, turn, (w / WP) * QS * 16 + q * 16 + (lane & 15), (w % WP) * (kTileP / WP) / 128);
     }
 
-    // next: the step that refills this one's stage.  qc: Q fragments of this step's first half, read
-    // already, and at the end the next step's.
+    // One turn, in stage `cur`.  qc: Q fragments of its first half, read already, and at the end the
+    // next turn's; sc: fp8's scales, likewise.
     template <class OpP, class OpQ>
-    __device__ __forceinline__ static void step_of(const Stage& cur, const Stage& nxt, int next, const OpP& lp, const OpQ& lq,
-                                                   const LoadScales& ls, Frag (&pr)[kRing], Frag (&qc)[QS], float (&sc)[QS],
+    __device__ __forceinline__ static void step_of(const Stage& cur, const Stage& nxt, int turn, const Steps& order,
+                                                   const OpP& lp, const OpQ& lq, const LoadScales& ls, Frag (&pr)[kRing], Frag (&qc)[QS], float (&sc)[QS],
                                                    f32x4 (&acc)[PS][QS], int w, int lane) {
         constexpr int kLoadsP = OpP::kInstr, kLoads = OpP::kInstr + OpQ::kInstr + (FP8 ? 1 : 0);
         constexpr int kBefore = kGroups - kAhead;                  // groups before the barrier
         constexpr int kQGroups = PS < kBefore ? PS : kBefore;      // they read the second half's Q
+        const int next = order.at(turn + STAGES);   // past the end it reads nothing and writes zeros
         const auto sp = lp.step_of(next);
         const auto sq = lq.step_of(next);
         Frag qn[QS];
@@ -378,31 +395,35 @@ struct TileBody {
 #pragma unroll
                     for (int q = j * QS / kAhead; q < (j + 1) * QS / kAhead; ++q) qc[q] = read_q(nxt, 0, q, w, lane);
                 }
-                // past the end these read nothing and write zeros
 #pragma unroll
                 for (int l = j * kLoads / kAhead; l < (j + 1) * kLoads / kAhead; ++l) {
                     if (l < kLoadsP) lp.issue(cur.p, sp, l);
                     else if (l < kLoadsP + OpQ::kInstr) lq.issue(cur.q, sq, l - kLoadsP);
-                    else ls.issue(cur.scales, next);
+                    else ls.issue(order, turn + STAGES);
                 }
             }
             const int p = i % PS;
             if constexpr (FP8) {
-                f32x4 d[QS];
+                constexpr int kAtOnce = 5;   // unscaled results held
 #pragma unroll
-                for (int q = 0; q < QS; ++q) {
-                    d[q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pr[i % kRing], qc[q], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0,
-                                                                            0, 0, 0, 0);
-                    if (i == kGroups - 1) {   // this fragment was used for the last time
-                        __builtin_amdgcn_sched_barrier(0);
-                        qc[q] = read_q(nxt, 0, q, w, lane);
+                for (int q0 = 0; q0 < QS; q0 += kAtOnce) {
+                    f32x4 d[kAtOnce];
+#pragma unroll
+                    for (int q = q0; q < QS && q < q0 + kAtOnce; ++q) {
+                        d[q - q0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pr[i % kRing], qc[q], f32x4{0.f, 0.f, 0.f, 0.f},
+                                                                                     0, 0, 0, 0, 0, 0);
+                        if (i == kGroups - 1) {   // this fragment was used for the last time
+                            __builtin_amdgcn_sched_barrier(0);
+                            qc[q] = read_q(nxt, 0, q, w, lane);
+                        }
                     }
-                }
 #pragma unroll
-                for (int q = 0; q < QS; ++q) {
+                    for (int q = q0; q < QS && q < q0 + kAtOnce; ++q) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[p][q][r] = __builtin_fmaf(d[q][r], sc[q], acc[p][q][r]);
-                    if (i == kGroups - 1) sc[q] = read_scale(nxt, q, w, lane);
+                        for (int r = 0; r < 4; ++r) acc[p][q][r] = __builtin_fmaf(d[q - q0][r], sc[q], acc[p][q][r]);
+                        if (i == kGroups - 1) sc[q] = read_scale(ls, order, turn + 1, q, w, lane);
+                    }
+                    if (q0 + kAtOnce < QS) __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
 #pragma unroll
@@ -428,7 +449,7 @@ struct TileBody {
             for (int l = 0; l < OpP::kInstr; ++l) lp.issue(st[s].p, sp, l);
 #pragma unroll
             for (int l = 0; l < OpQ::kInstr; ++l) lq.issue(st[s].q, sq, l);
-            if constexpr (FP8) ls.issue(st[s].scales, step);
+            if constexpr (FP8) ls.issue(order, s);
         }
     }
     template <class OpP, class OpQ>
@@ -448,7 +469,7 @@ struct TileBody {
 #pragma unroll
         for (int q = 0; q < QS; ++q) {
             qc[q] = read_q(st[0], 0, q, w, lane);
-            if constexpr (FP8) sc[q] = read_scale(st[0], q, w, lane);
+            if constexpr (FP8) sc[q] = read_scale(ls, order, 0, q, w, lane);
         }
         // A stage is known at compile time, so the loop takes STAGES steps a turn; leaving it in the
         // middle would give the accumulators two sets of registers.
@@ -456,12 +477,12 @@ struct TileBody {
         for (; step + STAGES - 1 < order.n; step += STAGES) {
 #pragma unroll
             for (int s = 0; s < STAGES; ++s)
-                step_of(st[s], st[(s + 1) % STAGES], order.at(step + s + STAGES), lp, lq, ls, pr, qc, sc, acc, w, lane);
+                step_of(st[s], st[(s + 1) % STAGES], step + s, order, lp, lq, ls, pr, qc, sc, acc, w, lane);
         }
         if (step < order.n) {
-            step_of(st[0], st[1], order.n, lp, lq, ls, pr, qc, sc, acc, w, lane);
+            step_of(st[0], st[1], step, order, lp, lq, ls, pr, qc, sc, acc, w, lane);
             if (STAGES > 2 && step + 1 < order.n)
-                step_of(st[1], st[2 % STAGES], order.n, lp, lq, ls, pr, qc, sc, acc, w, lane);
+                step_of(st[1], st[2 % STAGES], step + 1, order, lp, lq, ls, pr, qc, sc, acc, w, lane);
         }
         wait_loads<0>();   // nothing may be on its way into LDS when the stages are used again
     }
@@ -503,11 +524,13 @@ struct TileBody {
 };
 
 // ---------------------------------------------------------------- rows products
+constexpr int kThreeFp8 = 128;   // rows of the largest fp8 tile with three stages
+
 // A tile of the forward or the rows gradient: rows [row, row + rows) of expert
 // e against output columns [i0, i0 + 256).
 template <int NW, int BQ, int WP, int STAGES, bool FP8, bool PMC>
 __device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& tl, int i0, const Stage (&st)[STAGES],
-                                          char* scratch, int w, int lane) {
+                                          char* scratch, char* scales, int w, int lane) {
     using B = TileBody<NW, BQ, WP, STAGES, FP8, PMC, false>;
     constexpr int kSize = FP8 ? 1 : 2;
     const int cdim = PMC ? a.N : a.K, idim = PMC ? a.K : a.N;
@@ -522,11 +545,11 @@ __device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& t
     f32x4 acc[B::PS][B::QS];
     // Tiles that share a matrix panel in L2 start together.
     const int n = (cdim * kSize + kStepBytes - 1) / kStepBytes;
-    const Steps steps = {n, !PMC && tl.alone ? (int)(blockIdx.x & 31) * n / 32 : 0};
+    const Steps steps = {n, !PMC && tl.alone ? ((int)(blockIdx.x & 31) * n / 32) & ~3 : 0};
     if constexpr (FP8) {
         const int kb = a.K / 128, nb = (a.N + 127) / 128;
-        ls.init(a.q_scales + qrow * kb, tl.rows, a.p_scales + ((int64_t)tl.e * nb + i0 / 128) * kb, nb - i0 / 128, kb, w,
-                lane);
+        ls.init(a.q_scales + qrow * kb, tl.rows, a.p_scales + ((int64_t)tl.e * nb + i0 / 128) * kb, nb - i0 / 128, kb,
+                scales, BQ > kThreeFp8 ? -1024 : kThreeFp8 * 16, w, lane);
     }
     if constexpr (PMC) {
         LoadMC<NW> lp;
@@ -676,6 +699,8 @@ constexpr int64_t kSmallBelow = KSB;
 
 constexpr int kWaves = 8;   // of a workgroup (one workgroup a compute unit)
 
+constexpr int max_of(int a, int b) { return a > b ? a : b; }
+
 template <bool FP8, bool PMC>
 __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_rows(ExpertGemmArgs a) {
     // Two stages of up to 256 rows, or three of up to kThree; the epilogue uses a part.  The compiler
@@ -683,25 +708,28 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_rows(ExpertG
     // one array for both, transposing reads also where it knows none.  Which loads have arrived is what
     // the waits in step_of() say; to keep it from waiting for more, plain reads see one unnamed block
     // and transposing ones an array for each stage and operand.
-    constexpr int kThree = PMC ? 64 : 160, kQ = kThree * kStepBytes;
+    constexpr int kThree = PMC ? 64 : FP8 ? kThreeFp8 : 160, kQ = kThree * kStepBytes;
     Stage two[2], three[3];
+    char* scales = nullptr;
     if constexpr (PMC) {
         __shared__ __align__(1024) char p0[kTileBytes], p1[kTileBytes], r0[kTileBytes], r1[kTileBytes], q0[kQ], q1[kQ], q2[kQ];
-        two[0] = {p0, r0, nullptr};
-        two[1] = {p1, r1, nullptr};
-        three[0] = {p0, q0, nullptr};
-        three[1] = {p1, q1, nullptr};
-        three[2] = {r0, q2, nullptr};
+        two[0] = {p0, r0};
+        two[1] = {p1, r1};
+        three[0] = {p0, q0};
+        three[1] = {p1, q1};
+        three[2] = {r0, q2};
     } else {
-        constexpr int kC = FP8 ? kScaleBytes : 0;
-        __shared__ __align__(1024) char lds[3 * (kTileBytes + kQ + kC)];
-        static_assert(3 * kQ >= kTileBytes, "");
-        char *q = lds + 3 * kTileBytes, *c = q + 3 * kQ;
-        two[0] = {lds, lds + 2 * kTileBytes, c};
-        two[1] = {lds + kTileBytes, q, c + kC};
-        three[0] = {lds, q, c};
-        three[1] = {lds + kTileBytes, q + kQ, c + kC};
-        three[2] = {lds + 2 * kTileBytes, q + 2 * kQ, c + 2 * kC};
+        constexpr int kTiles = max_of(4 * kTileBytes, 3 * (kTileBytes + kQ));
+        __shared__ __align__(1024) char lds[kTiles + (FP8 ? LoadScales::kBytes : 0)];
+        char* q = lds + 3 * kTileBytes;
+        two[0] = {lds, lds + 2 * kTileBytes};
+        two[1] = {lds + kTileBytes, q};
+        three[0] = {lds, q};
+        three[1] = {lds + kTileBytes, q + kQ};
+        three[2] = {lds + 2 * kTileBytes, q + 2 * kQ};
+        scales = lds + kTiles;
+        // LoadScales's unused kilobyte: before the scales of two stages, behind the rows of three
+        static_assert(!FP8 || (kTiles >= 4 * kTileBytes + 1024 && kThreeFp8 * 16 + 1024 <= 4096), "");
     }
     static_assert(kTileBytes >= kWaves * 2048, "");
     char* scratch = two[0].p;
@@ -710,13 +738,14 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_rows(ExpertG
     const Tile tl = find_tile(a.seg, xcd_tile(blockIdx.x), 256, ntiles);
     if (tl.e < 0) return;
     const int i0 = tl.col * kTileP;
-    if (tl.rows > 192) rows_tile<kWaves, 256, 2, 2, FP8, PMC>(a, tl, i0, two, scratch, w, lane);
-    else if (tl.rows > (PMC ? 128 : 160)) rows_tile<kWaves, 192, 2, 2, FP8, PMC>(a, tl, i0, two, scratch, w, lane);
-    else if (!PMC && tl.rows > 128) rows_tile<kWaves, PMC ? 64 : 160, 4, 3, FP8, PMC>(a, tl, i0, three, scratch, w, lane);
-    else if (PMC && tl.rows > 64) rows_tile<kWaves, 128, 4, 2, FP8, PMC>(a, tl, i0, two, scratch, w, lane);
-    else if (tl.rows > 64) rows_tile<kWaves, PMC ? 64 : 128, 4, 3, FP8, PMC>(a, tl, i0, three, scratch, w, lane);
-    else if (tl.rows > 32) rows_tile<kWaves, 64, 4, 3, FP8, PMC>(a, tl, i0, three, scratch, w, lane);
-    else rows_tile<kWaves, 32, 8, 3, FP8, PMC>(a, tl, i0, three, scratch, w, lane);
+    if (tl.rows > 192) rows_tile<kWaves, 256, 2, 2, FP8, PMC>(a, tl, i0, two, scratch, scales, w, lane);
+    else if (tl.rows > (PMC ? 128 : 160)) rows_tile<kWaves, 192, 2, 2, FP8, PMC>(a, tl, i0, two, scratch, scales, w, lane);
+    else if (!PMC && !FP8 && tl.rows > 128) rows_tile<kWaves, kThree, 4, 3, FP8, PMC>(a, tl, i0, three, scratch, scales, w, lane);
+    else if (FP8 && tl.rows > 128) rows_tile<kWaves, 160, 4, 2, FP8, PMC>(a, tl, i0, two, scratch, scales, w, lane);
+    else if (PMC && tl.rows > 64) rows_tile<kWaves, 128, 4, 2, FP8, PMC>(a, tl, i0, two, scratch, scales, w, lane);
+    else if (tl.rows > 64) rows_tile<kWaves, PMC ? 64 : 128, 4, 3, FP8, PMC>(a, tl, i0, three, scratch, scales, w, lane);
+    else if (tl.rows > 32) rows_tile<kWaves, 64, 4, 3, FP8, PMC>(a, tl, i0, three, scratch, scales, w, lane);
+    else rows_tile<kWaves, 32, 8, 3, FP8, PMC>(a, tl, i0, three, scratch, scales, w, lane);
 }
 
 // ---------------------------------------------------------------- weights gradient
@@ -724,12 +753,12 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad
     using B = TileBody<kWaves, 256, 2, 2, false, true, true>;
     __shared__ __align__(1024) char p0[kTileBytes], p1[kTileBytes], q0[kTileBytes], q1[kTileBytes];
     __shared__ __align__(1024) char scratch[kWaves * 2048];
-    const Stage st[2] = {{p0, q0, nullptr}, {p1, q1, nullptr}};
+    const Stage st[2] = {{p0, q0}, {p1, q1}};
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int kt = (a.K + kTileP - 1) / kTileP, nt = (a.N + 255) / 256;
     const int64_t tiles = (int64_t)a.seg.E * kt * nt;
     LoadMC<kWaves> lp, lq;
-    LoadScales ls;
+    LoadScales ls;   // none
     Steps steps;
     int e, i0, j0;
     auto start = [&](int64_t t, int ln) {
