@@ -507,44 +507,53 @@ def moe_combine_backward(ctx, grad_out, topk_weights, expert_out, handle, grad_e
 
 
 # ---------------------------------------------------------------- expert products
+def _rows_capacity(ctx):
+    """Rows of a buffer in each order: [MOE_ROWS_RECV, MOE_ROWS_PACKED] (fixed per context, so cached)."""
+    cap = ctx.__dict__.get("_rows_cap")
+    if cap is None:
+        c = ctx.cfg
+        packed = c.max_tokens * c.topk
+        recv = c.num_experts * c.max_tokens * c.num_ranks if c.layout == MOE_LAYOUT_PADDED_LL else packed
+        cap = ctx.__dict__["_rows_cap"] = (recv, packed)
+    return cap
+
+
 def _expert_rows(ctx, t, dtype, width, order, name):
     """A row buffer of an expert product: [rows, width] of the dtype on the
     context's device, with every row that its order can address."""
-    _as_dev(t, dtype, name)
-    c = ctx.cfg
-    if t.device.index != ctx.device:
+    if not (t.is_cuda and t.dtype is dtype and t.is_contiguous()):
+        raise TypeError("%s must be a contiguous %s CUDA tensor" % (name, dtype))
+    if t.get_device() != ctx.device:
         raise ValueError("%s is on %s, the context on cuda:%d" % (name, t.device, ctx.device))
-    if order == MOE_ROWS_PACKED or c.layout == MOE_LAYOUT_CONTIGUOUS:
-        need = c.max_tokens * c.topk
-    elif order == MOE_ROWS_RECV:
-        need = c.num_experts * c.max_tokens * c.num_ranks
-    else:
+    if order != MOE_ROWS_RECV and order != MOE_ROWS_PACKED:
         raise ValueError("row order must be MOE_ROWS_RECV or MOE_ROWS_PACKED")
-    if t.dim() != 2 or t.shape[1] != width or t.shape[0] < need:
-        raise ValueError("%s must be [%d, %d], is %s" % (name, need, width, tuple(t.shape)))
+    shape, need = t.shape, _rows_capacity(ctx)[order]
+    if len(shape) != 2 or shape[1] != width or shape[0] < need:
+        raise ValueError("%s must be [%d, %d], is %s" % (name, need, width, tuple(shape)))
     return t
 
 
 def _expert_out(ctx, width, dtype, order):
-    c = ctx.cfg
-    n = (c.num_experts * c.max_tokens * c.num_ranks
-         if order == MOE_ROWS_RECV and c.layout == MOE_LAYOUT_PADDED_LL else c.max_tokens * c.topk)
-    return torch.empty((n, width), dtype=dtype, device=torch.device("cuda", ctx.device))
+    if order != MOE_ROWS_RECV and order != MOE_ROWS_PACKED:
+        raise ValueError("row order must be MOE_ROWS_RECV or MOE_ROWS_PACKED")
+    return torch.empty((_rows_capacity(ctx)[order], width), dtype=dtype, device=torch.device("cuda", ctx.device))
 
 
 def _expert_mats(ctx, t, dtype, shape, name):
-    _as_dev(t, dtype, name)
-    if t.device.index != ctx.device:
+    if not (t.is_cuda and t.dtype is dtype and t.is_contiguous()):
+        raise TypeError("%s must be a contiguous %s CUDA tensor" % (name, dtype))
+    if t.get_device() != ctx.device:
         raise ValueError("%s is on %s, the context on cuda:%d" % (name, t.device, ctx.device))
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError("%s must be %s, is %s" % (name, shape, tuple(t.shape)))
     return t
 
 
 def _mats_shape(ctx, weights):
-    if weights.dim() != 3 or weights.shape[0] != ctx.cfg.num_experts:
+    shape = weights.shape
+    if len(shape) != 3 or shape[0] != ctx.cfg.num_experts:
         raise ValueError("weights must be [%d, out_features, in_features]" % ctx.cfg.num_experts)
-    return weights.shape[1], weights.shape[2]
+    return shape[1], shape[2]
 
 
 def moe_expert_gemm(ctx, rows, weights, handle, out=None, rows_order=MOE_ROWS_RECV, out_order=MOE_ROWS_RECV):
@@ -626,9 +635,10 @@ def moe_expert_gemm_backward_weights(ctx, grad_out, rows, handle, grad_weights=N
 
 
 def _gate_up_features(gate_up):
-    if gate_up.dim() != 2 or gate_up.shape[1] % 2:
+    shape = gate_up.shape
+    if len(shape) != 2 or shape[1] % 2:
         raise ValueError("gate_up must be [rows, 2 * features]")
-    return gate_up.shape[1] // 2
+    return shape[1] // 2
 
 
 def moe_swiglu(ctx, gate_up, handle, out=None, order=MOE_ROWS_RECV):
