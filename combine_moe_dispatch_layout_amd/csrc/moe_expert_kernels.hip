@@ -12,12 +12,27 @@
 // a lane ends up with four consecutive i of one j.
 //
 // Tiles travel from memory to LDS without passing through registers (buffer
-// loads with an LDS destination), in a ring of stages of 128 contraction bytes.
-// Those loads write LDS in lane order, so the bank swizzle is applied to the
-// address each lane reads from.  Out-of-range lanes read zeros (the buffer
+// loads with an LDS destination), in two or three stages of 128 contraction
+// bytes.  Those loads write LDS in lane order, so the bank swizzle is applied to
+// the address each lane reads from.  Out-of-range lanes read zeros (the buffer
 // descriptor ends with the tile's valid rows; a lane whose contraction index is
 // past the end gets an address past any descriptor), which is what pads ragged
 // rows and contraction tails.
+//
+// What bounds them (MI355X; a large copy moves 4.76 TB/s, a large library
+// product does 1.39 PFLOP/s NT, 1.21 NN, 1.08 TN in bf16 and 3.05 in plain fp8):
+//   many rows an expert   the matrix cores and the power they may draw: 8192^3
+//                         takes 0.78 ms forward (1.41 PFLOP/s, 67-70% of the cycles on the
+//                         matrix cores at a clock that falls to 1.5-1.9 GHz), 1.52 ms for both
+//                         gradients (1.45 PFLOP/s), 0.50 ms in fp8 with block scales (2.18)
+//   few rows an expert    reading the matrices: 1 row an expert 6.2 TB/s, 64 rows 5.6, 128
+//                         rows 5.2, 256 rows 4.0 of matrix bytes; what is lost there is the time
+//                         of flight of a stage, so smaller tiles get a third stage
+// Tried and dropped: reading the next steps' lines into L2 ahead (sq 8192 0.90 ms
+// against 0.83: the address unit is busy), raised wave priority around the
+// matrix instructions (1-3% slower), bands of 2, 8 or 16 row tiles (0-3%
+// slower), four wavefronts of 128 x 128 (the compiler moves accumulators
+// about), staggered workgroups in the weights gradient (no change).
 #include "moe_ep.h"
 #include "moe_expert.h"
 #include "moe_internal.h"
@@ -41,8 +56,11 @@ constexpr int kStepC = 64;               // contraction elements of a bf16 stage
 constexpr int kTileP = 256;              // i extent of a tile
 constexpr uint32_t kOob = 0x80000000u;   // past the end of every descriptor (they hold under 2^31 bytes)
 
-__device__ __forceinline__ uint16_t bf16_bits(float f) {
+__device__ __forceinline__ uint32_t bf16_bits(float f) {
     return __builtin_bit_cast(uint16_t, (__bf16)f);   // round to nearest even
+}
+__device__ __forceinline__ u32x2 bf16_pack(f32x4 v) {
+    return u32x2{bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16)};
 }
 
 // Every descriptor covers one stage of one tile, at most 256 rows of 2 * MOE_MAX_FEATURES bytes.
@@ -248,8 +266,8 @@ struct LoadMC {
 // at different columns spread over all of them.
 struct Steps {
     int n, start;
-    // Arithmetic instead of conditions: for those the compiler branches, and moves the matrix results'
-    // scaling past the branch, into more registers than there are.
+    // Arithmetic instead of conditions: for those the compiler branches, and moves the scaling of the
+    // matrix results past the branch, into more registers than there are.
     __device__ __forceinline__ static int not_below(int a, int b) { return (b - 1 - a) >> 31; }   // a >= b ? -1 : 0
     __device__ __forceinline__ static int select(int mask, int yes, int no) { return no ^ ((no ^ yes) & mask); }
     // step of the s-th turn; past the end a step that reads nothing
@@ -257,10 +275,9 @@ struct Steps {
         const int k = s + start;
         return select(not_below(s, n), n, k - (n & not_below(k, n)));
     }
-    // turn s's run of four steps 4 i .. 4 i + 3, counted in the order they are taken (start % 4 == 0)
-    __device__ __forceinline__ int four(int s) const {
-        return select(not_below(s + start, n), ((n - start + 3) >> 2) + ((s + start - n) >> 2), s >> 2);
-    }
+    // turn s's run of four steps 4 i .. 4 i + 3, counted in the order they are taken (start is 0, or
+    // both start and n are multiples of 4)
+    __device__ __forceinline__ int four(int s) const { return s >> 2; }
 };
 
 // fp8: the scales of the tile's rows and of its two 128-column blocks, for four steps at a time (one
@@ -322,12 +339,14 @@ struct Stage {
 // One tile of kTileP x BQ outputs.  WP x WQ wavefronts; each owns
 // (kTileP / WP) x (BQ / WQ) outputs as PS x QS subtiles of 16 x 16.
 //
-// Two stages in LDS.  A step's matrix instructions are issued in groups, one P fragment times the QS
-// Q fragments each; P fragments are read kAhead groups before they are used, Q fragments a whole
-// half step before.  After the group whose reads are the last from the stage, one barrier says that
-// every wavefront is done with it and that the other stage has arrived; the remaining groups issue
-// the loads that refill the freed stage, for two steps on, and read the first fragments of the other.
-// So nothing is waited for but loads that had a step's time to arrive.
+// A step's matrix instructions are issued in groups, one P fragment times the QS Q fragments each; P
+// fragments are read kAhead groups before they are used, bf16's Q fragments half a step before.  After
+// the group whose reads are the last from the stage, one barrier says that every wavefront is done
+// with it and that the next stage has arrived; the remaining groups issue the loads that refill the
+// freed stage, for STAGES steps on, and read the first fragments of the next.  So nothing is waited
+// for but loads that had STAGES - 1 steps' time to arrive.  Groups are kept in this order (the
+// scheduler is fenced off between them): with all loads right behind the barrier the wavefronts
+// queue for the address unit while the matrix cores are idle.
 template <int NW, int BQ, int WP, int STAGES, bool FP8, bool PMC, bool QMC>
 struct TileBody {
     static_assert(WP <= NW, "");
@@ -367,8 +386,8 @@ struct TileBody {
     // next turn's; sc: fp8's scales, likewise.
     template <class OpP, class OpQ>
     __device__ __forceinline__ static void step_of(const Stage& cur, const Stage& nxt, int turn, const Steps& order,
-                                                   const OpP& lp, const OpQ& lq, const LoadScales& ls, Frag (&pr)[kRing], Frag (&qc)[QS], float (&sc)[QS],
-                                                   f32x4 (&acc)[PS][QS], int w, int lane) {
+                                                   const OpP& lp, const OpQ& lq, const LoadScales& ls, Frag (&pr)[kRing],
+                                                   Frag (&qc)[QS], float (&sc)[QS], f32x4 (&acc)[PS][QS], int w, int lane) {
         constexpr int kLoadsP = OpP::kInstr, kLoads = OpP::kInstr + OpQ::kInstr + (FP8 ? 1 : 0);
         constexpr int kBefore = kGroups - kAhead;                  // groups before the barrier
         constexpr int kQGroups = PS < kBefore ? PS : kBefore;      // they read the second half's Q
@@ -435,8 +454,7 @@ struct TileBody {
         }
     }
 
-    // The stages' P tiles are distinct LDS arrays: so the compiler knows that reads of one do not wait for
-    // loads into another.  begin() starts the loads of a tile's first steps, run() does the rest.
+    // begin() starts the loads of a tile's first steps, run() does the rest.
     template <class OpP, class OpQ>
     __device__ __forceinline__ static void begin(const Stage (&st)[STAGES], const OpP& lp, const OpQ& lq,
                                                  const LoadScales& ls, const Steps& order) {
@@ -492,7 +510,6 @@ struct TileBody {
     // store writes whole 128-byte lines (direct 8-byte stores reach them in four parts).  A row's
     // 16-byte chunk c sits at c ^ row.
     static constexpr int kCols = PS >= 4 ? 64 : PS * 16, kChunks = kCols / 8;
-    static constexpr int kStores = QS * (PS * 16 / kCols) * (kCols / 32);   // of one wavefront
     __device__ __forceinline__ static void store(uint16_t* out, int64_t ld, int ni, int nj, const f32x4 (&acc)[PS][QS],
                                                  char* scratch, int w, int lane) {
         const int wp = w % WP, wq = w / WP, g = lane >> 4, t = lane & 15;
@@ -506,8 +523,7 @@ struct TileBody {
                     const f32x4 v = acc[p0 + p][q];
                     const int c = 2 * p + (g >> 1);
                     *reinterpret_cast<u32x2*>(mine + t * kCols * 2 + (((c ^ t) & (kChunks - 1)) << 4) + (g & 1) * 8) =
-                        u32x2{(uint32_t)bf16_bits(v[0]) | ((uint32_t)bf16_bits(v[1]) << 16),
-                              (uint32_t)bf16_bits(v[2]) | ((uint32_t)bf16_bits(v[3]) << 16)};
+                        bf16_pack(v);
                 }
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
 #pragma unroll
@@ -543,9 +559,12 @@ __device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& t
     lq.init(static_cast<const char*>(a.q) + qrow * qld, (int)qld, tl.rows, (int)qld, w, lane);
     LoadScales ls;
     f32x4 acc[B::PS][B::QS];
-    // Tiles that share a matrix panel in L2 start together.
+    // Tiles that share a matrix panel in L2 start together.  Only lengths of whole runs of four steps
+    // are started elsewhere: others spread over the channels by themselves, and no run is cut short, so
+    // that LoadScales never needs a third.  (64 experts x 4 rows, 4096 x 4096 bf16: 371 us, 437 us
+    // without.)
     const int n = (cdim * kSize + kStepBytes - 1) / kStepBytes;
-    const Steps steps = {n, !PMC && tl.alone ? ((int)(blockIdx.x & 31) * n / 32) & ~3 : 0};
+    const Steps steps = {n, !PMC && tl.alone && n % 4 == 0 ? ((int)(blockIdx.x & 31) * n / 32) & ~3 : 0};
     if constexpr (FP8) {
         const int kb = a.K / 128, nb = (a.N + 127) / 128;
         ls.init(a.q_scales + qrow * kb, tl.rows, a.p_scales + ((int64_t)tl.e * nb + i0 / 128) * kb, nb - i0 / 128, kb,
@@ -570,7 +589,8 @@ __device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& t
 // Narrow tiles for products with too few 256-column tiles to occupy the chip (a token or a few): 64
 // columns x 32 rows, four wavefronts, two workgroups a compute unit.  What counts here is the bytes
 // on their way from memory, so the ring has kSmallStages stages, and the matrix instructions are
-// not scheduled by hand.
+// not scheduled by hand.  A token with 6 experts of 4096 x 4096 bf16 takes 51 us (3.9 TB/s; 32-column
+// tiles 48.7, but 8 experts with 8 rows each then 90 instead of 66; other starts than 0 no better).
 constexpr int kSmallP = 64, kSmallQ = 32, kSmallWaves = 4, kSmallStages = 6;
 
 template <bool FP8>
@@ -600,7 +620,7 @@ struct SmallBody {
     };
 
     // Wavefront w: columns 32 (w % 2) .. +31, rows 16 (w / 2) .. +15.
-    __device__ __forceinline__ static void run(char* lds, const LP& lp, const LQ& lq, const Scales& ls, const Steps& order, int rows,
+    __device__ __forceinline__ static void run(char* lds, const LP& lp, const LQ& lq, const Scales& ls, int steps, int rows,
                                                f32x4 (&acc)[2], int w, int lane) {
         constexpr int kLoads = LP::kInstr + LQ::kInstr + (FP8 ? 1 : 0);
         const int g = lane >> 4, t = lane & 15, wp = w & 1, wq = w >> 1;
@@ -616,12 +636,12 @@ struct SmallBody {
         };
         acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < kSmallStages - 1; ++s) fill(order.at(s), s);
+        for (int s = 0; s < kSmallStages - 1; ++s) fill(s, s);
         int cur = 0, nxt = kSmallStages - 1;
-        for (int step = 0; step < order.n; ++step) {
+        for (int step = 0; step < steps; ++step) {
             wait_loads<(kSmallStages - 2) * kLoads>();
             lds_barrier();   // this step has arrived, and everyone is done with the one before
-            fill(order.at(step + kSmallStages - 1), nxt);
+            fill(step + kSmallStages - 1, nxt);   // past the end it reads nothing
             const char* sp = lds + cur * kStage;
             const char* sq = sp + kSmallP * kStepBytes;
             if (wq * 16 < rows) {
@@ -678,26 +698,24 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_expert_rows_small(ExpertGe
         ls.init(a.q_scales + qrow * kb, tl.rows, a.p_scales + ((int64_t)tl.e * nb + i0 / 128) * kb, kb, w, lane);
     }
     f32x4 acc[2];
-    const int n = (int)((ld + kStepBytes - 1) / kStepBytes);
-    B::run(lds, lp, lq, ls, Steps{n, 0}, tl.rows, acc, w, lane);
+    B::run(lds, lp, lq, ls, (int)((ld + kStepBytes - 1) / kStepBytes), tl.rows, acc, w, lane);
     const int j = (w >> 1) * 16 + (lane & 15);
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
         const int i = (w & 1) * 32 + p * 16 + 4 * (lane >> 4);
         if (j < tl.rows && i < ni)
-            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + (orow + j) * a.N + i0 + i) =
-                u32x2{(uint32_t)bf16_bits(acc[p][0]) | ((uint32_t)bf16_bits(acc[p][1]) << 16),
-                      (uint32_t)bf16_bits(acc[p][2]) | ((uint32_t)bf16_bits(acc[p][3]) << 16)};
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + (orow + j) * a.N + i0 + i) = bf16_pack(acc[p]);
     }
 }
 
 constexpr int kTileBytes = 256 * kStepBytes;   // of one operand's stage
-#ifndef KSB
-#define KSB 129
-#endif
-constexpr int64_t kSmallBelow = KSB;
+constexpr int kWaves = 8;                      // of a workgroup (one workgroup a compute unit)
 
-constexpr int kWaves = 8;   // of a workgroup (one workgroup a compute unit)
+// Products of at most this many wide tiles, half of the chip's compute units, run as narrow ones.
+// Wide against narrow, measured: 96 tiles (a token, 6 experts, 4096 x 4096 bf16) 70 and 51 us, 128 tiles (8
+// experts, 8 rows each) 90 and 66 us; 144 tiles (32 rows each) 88 and 150 us, 224 tiles (fp8, 7168 x
+// 2048) 23 and 32 us, 243 tiles (2056 x 1000) 24 and 38 us.
+constexpr int64_t kSmallTiles = 128;
 
 constexpr int max_of(int a, int b) { return a > b ? a : b; }
 
@@ -738,6 +756,10 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_rows(ExpertG
     const Tile tl = find_tile(a.seg, xcd_tile(blockIdx.x), 256, ntiles);
     if (tl.e < 0) return;
     const int i0 = tl.col * kTileP;
+    // The smallest tile that holds the rows.  A third stage pays where reading the matrix is the bound
+    // (forward, 64 experts of 4096 x 4096: 128 rows 413 us, with two stages 524; 160 rows 447, as 192 rows
+    // with two 495); fp8's scales leave it room up to 128 rows, the transposed operand's separate
+    // arrays up to 64.
     if (tl.rows > 192) rows_tile<kWaves, 256, 2, 2, FP8, PMC>(a, tl, i0, two, scratch, scales, w, lane);
     else if (tl.rows > (PMC ? 128 : 160)) rows_tile<kWaves, 192, 2, 2, FP8, PMC>(a, tl, i0, two, scratch, scales, w, lane);
     else if (!PMC && !FP8 && tl.rows > 128) rows_tile<kWaves, kThree, 4, 3, FP8, PMC>(a, tl, i0, three, scratch, scales, w, lane);
@@ -749,6 +771,11 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_rows(ExpertG
 }
 
 // ---------------------------------------------------------------- weights gradient
+// Tiles of 256 x 256 over every matrix, also of experts without rows (they get zeros).  With few rows an
+// expert it is bound by writing the gradients: 64 matrices of 4096 x 4096 take 0.42 ms at 16 rows each (5.1
+// TB/s written), 0.54 at 128, 1.7 at 768 (0.98 PFLOP/s), 3.6 at 2048 (1.21).
+constexpr int kWeightsGradBlocks = 256;
+
 __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad(ExpertGemmArgs a) {
     using B = TileBody<kWaves, 256, 2, 2, false, true, true>;
     __shared__ __align__(1024) char p0[kTileBytes], p1[kTileBytes], q0[kTileBytes], q1[kTileBytes];
@@ -775,52 +802,50 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad
         steps = Steps{(rows + kStepC - 1) / kStepC, 0};
         B::begin(st, lp, lq, ls, steps);
     };
-    // Each workgroup takes every 256th tile, and starts the next one's loads before it stores.
+    // Each workgroup takes every kWeightsGradBlocks-th tile, and starts the next one's loads before it
+    // stores.
     int64_t t = xcd_tile(blockIdx.x);
     if (t >= tiles) return;
     start(t, lane);
     for (;;) {
-    f32x4 acc[B::PS][B::QS];
-    B::run(st, lp, lq, ls, steps, acc, w, lane);
-    const int64_t at = ((int64_t)e * a.N + j0) * a.K + i0;
-    const int ni = min(kTileP, a.K - i0), nj = min(256, a.N - j0);
-    t += 256;
-    int ln = lane;
-    asm volatile("" : "+v"(ln));   // what depends on the lane is computed anew: kept over the loop it would spill
-    if (t < tiles) {
-        lds_barrier();   // everyone is done with the stages
-        start(t, ln);
-    }
-    const int wp = w % 2, wq = w / 2, g = ln >> 4, tt = ln & 15;
-    if (a.accumulate || a.out_f32) {
+        f32x4 acc[B::PS][B::QS];
+        B::run(st, lp, lq, ls, steps, acc, w, lane);
+        const int64_t at = ((int64_t)e * a.N + j0) * a.K + i0;
+        const int ni = min(kTileP, a.K - i0), nj = min(256, a.N - j0);
+        t += kWeightsGradBlocks;
+        int ln = lane;
+        asm volatile("" : "+v"(ln));   // what depends on the lane is computed anew: kept over the loop it would spill
+        if (t < tiles) {
+            lds_barrier();   // everyone is done with the stages
+            start(t, ln);
+        }
+        if (a.accumulate || a.out_f32) {
+            const int wp = w % 2, wq = w / 2, g = ln >> 4, tt = ln & 15;
 #pragma unroll
-        for (int q = 0; q < B::QS; ++q) {
-            const int j = wq * B::QS * 16 + q * 16 + tt;
+            for (int q = 0; q < B::QS; ++q) {
+                const int j = wq * B::QS * 16 + q * 16 + tt;
 #pragma unroll
-            for (int p = 0; p < B::PS; ++p) {
-                const int i = wp * B::PS * 16 + 16 * p + 4 * g;
-                if (j >= nj || i >= ni) continue;
-                const int64_t o = at + (int64_t)j * a.K + i;
-                if (a.out_f32) {
-                    f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o);
-                    *d = a.accumulate ? *d + acc[p][q] : acc[p][q];
-                } else {
-                    u32x2* d = reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + o);
-                    const u32x2 old = *d;
+                for (int p = 0; p < B::PS; ++p) {
+                    const int i = wp * B::PS * 16 + 16 * p + 4 * g;
+                    if (j >= nj || i >= ni) continue;
+                    const int64_t o = at + (int64_t)j * a.K + i;
                     f32x4 v = acc[p][q];
-                    v[0] += __uint_as_float(old.x << 16);
-                    v[1] += __uint_as_float(old.x & 0xffff0000u);
-                    v[2] += __uint_as_float(old.y << 16);
-                    v[3] += __uint_as_float(old.y & 0xffff0000u);
-                    *d = u32x2{(uint32_t)bf16_bits(v[0]) | ((uint32_t)bf16_bits(v[1]) << 16),
-                               (uint32_t)bf16_bits(v[2]) | ((uint32_t)bf16_bits(v[3]) << 16)};
+                    if (a.out_f32) {
+                        f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o);
+                        *d = a.accumulate ? *d + v : v;
+                    } else {
+                        u32x2* d = reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + o);
+                        const u32x2 old = *d;
+                        v += f32x4{__uint_as_float(old.x << 16), __uint_as_float(old.x & 0xffff0000u),
+                                   __uint_as_float(old.y << 16), __uint_as_float(old.y & 0xffff0000u)};
+                        *d = bf16_pack(v);
+                    }
                 }
             }
+        } else {
+            B::store(static_cast<uint16_t*>(a.out) + at, a.K, ni, nj, acc, scratch, w, ln);
         }
-    } else {
-        B::store(static_cast<uint16_t*>(a.out) + at, a.K, ni, nj, acc, scratch, w, ln);
-    }
-    if (t >= tiles) return;
+        if (t >= tiles) return;
     }
 }
 
@@ -837,7 +862,7 @@ hipError_t launch_rows(const ExpertGemmArgs& a, int64_t pairs, hipStream_t s) {
     const int64_t ntiles = ((PMC ? a.K : a.N) + kTileP - 1) / kTileP;
     const int64_t tiles = tile_bound(a, pairs, 256, ntiles);
     if constexpr (!PMC) {
-        if (tiles < kSmallBelow) {
+        if (tiles <= kSmallTiles) {
             const int64_t blocks = tile_bound(a, pairs, kSmallQ, (a.N + kSmallP - 1) / kSmallP);
             if (!grid_fits(blocks, 64 * kSmallWaves)) return hipErrorInvalidConfiguration;
             k_expert_rows_small<FP8><<<dim3((unsigned)blocks), dim3(64 * kSmallWaves), 0, s>>>(a);
@@ -861,8 +886,7 @@ hipError_t launch_expert_gemm_bwd_rows(const ExpertGemmArgs& a, int64_t pairs, h
 }
 
 hipError_t launch_expert_gemm_bwd_weights(const ExpertGemmArgs& a, hipStream_t s) {
-    const int blocks = 256;   // each takes every 256th tile
-    k_expert_weights_grad<<<dim3((unsigned)blocks), dim3(64 * kWaves), 0, s>>>(a);
+    k_expert_weights_grad<<<dim3(kWeightsGradBlocks), dim3(64 * kWaves), 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -1,0 +1,229 @@
+"""The expert products with many tiles: segments of every length around the tile
+sizes, contractions of every number of steps, the largest features, buffers past
+4 GB, other streams, and captured graphs whose inputs change."""
+import pytest
+import torch
+
+import expert_ref as X
+
+RECV, PACKED = 0, 1
+pytestmark = pytest.mark.gpu
+
+# rows of the experts, in turn: on both sides of every tile size
+LENGTHS = [0, 1, 16, 17, 32, 33, 64, 65, 96, 128, 129, 144, 145, 160, 161, 192, 193, 255, 256, 257, 300, 517]
+EXPERTS = 6 * len(LENGTHS)
+
+
+@pytest.fixture(scope="module")
+def case(gpu):
+    e = torch.arange(EXPERTS).repeat_interleave(torch.tensor(LENGTHS * 6))
+    idx = e[torch.randperm(e.numel(), generator=torch.Generator().manual_seed(5))].reshape(-1, 1)
+    c = X.Case(gpu, T=e.numel(), k=1, E=EXPERTS, R=4, idx=idx)
+    yield c
+    c.close()
+
+
+@pytest.mark.parametrize("K,N", [(8, 264), (64, 256), (72, 520), (128, 40), (192, 264), (256, 264), (320, 264), (512, 136),
+                                 (576, 264), (1000, 8)])
+def test_gemm(gpu, case, K, N):
+    c = case
+    w, x = c.randn(EXPERTS, N, K, scale=K ** -0.5), c.randn(c.n, K)
+    ref, mag = X.per_expert(c, x, w), X.per_expert(c, x.abs(), w.abs())
+    out = torch.full((c.n, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    gpu.moe_expert_gemm(c.ctx, c.buffer(RECV, x, float("nan")), w.cuda(), c.handle, out=out)
+    X.check(c.rows_of(out, RECV)[0], ref, X.sum_bound(ref, mag, K, X.BF16_HALF), "out")
+
+
+@pytest.mark.parametrize("blocks,N", [(1, 264), (2, 256), (3, 136), (4, 264), (5, 8), (6, 264), (7, 264), (8, 264), (9, 136),
+                                      (12, 264)])
+def test_gemm_fp8(gpu, case, blocks, N):
+    c, K = case, 128 * blocks
+    wq = (c.randn(EXPERTS, N, K, scale=112.0).float().clamp(-448, 448)).to(torch.float8_e4m3fn).view(torch.uint8)
+    ws = torch.rand(EXPERTS, -(-N // 128), blocks, generator=c.gen) * 0.01 + 1e-4
+    xq, xs = X.quantise(c.randn(c.n, K).float() * torch.rand(c.n, 1, generator=c.gen) * 10)
+    w = X.e4m3(wq) * X.expand(ws, N, K)
+    x = X.e4m3(xq) * xs.double().repeat_interleave(128, 1)
+    ref, mag = X.per_expert(c, x, w), X.per_expert(c, x.abs(), w.abs())
+    out = gpu.moe_expert_gemm_fp8(c.ctx, c.buffer(RECV, xq, 0x7F), c.buffer(RECV, xs, float("nan")), wq.cuda(), ws.cuda(), c.handle)
+    X.check(c.rows_of(out, RECV)[0], ref, X.sum_bound(ref, mag, K, X.BF16_HALF), "out")
+
+
+@pytest.mark.parametrize("K,N", [(264, 8), (256, 64), (520, 72), (40, 128), (264, 192), (264, 320), (136, 520)])
+def test_backward_rows(gpu, case, K, N):
+    c = case
+    w, dy = c.randn(EXPERTS, N, K, scale=N ** -0.5), c.randn(c.n, N)
+    wt = w.transpose(1, 2).contiguous()
+    ref, mag = X.per_expert(c, dy, wt), X.per_expert(c, dy.abs(), wt.abs())
+    grad = gpu.moe_expert_gemm_backward_rows(c.ctx, c.buffer(RECV, dy, float("nan")), w.cuda(), c.handle)
+    X.check(c.rows_of(grad, RECV)[0], ref, X.sum_bound(ref, mag, N, X.BF16_HALF), "grad_rows")
+
+
+@pytest.mark.parametrize("dtype,accumulate", [(torch.bfloat16, False), (torch.float32, False), (torch.bfloat16, True),
+                                              (torch.float32, True)])
+@pytest.mark.parametrize("K,N", [(264, 520), (8, 8), (256, 256), (72, 264)])
+def test_backward_weights(gpu, case, K, N, dtype, accumulate):
+    c = case
+    x, dy = c.randn(c.n, K), c.randn(c.n, N)
+    before = c.randn(EXPERTS, N, K).to(dtype) if accumulate else torch.full((EXPERTS, N, K), float("nan"), dtype=dtype)
+    ref, mag = X.outer(c, dy, x, EXPERTS), X.outer(c, dy.abs(), x.abs(), EXPERTS)
+    if accumulate:
+        ref, mag = ref + before.double(), mag + before.double().abs()
+    grad = before.cuda()
+    gpu.moe_expert_gemm_backward_weights(c.ctx, c.buffer(RECV, dy, float("nan")), c.buffer(RECV, x, float("nan")), c.handle,
+                                         grad_weights=grad, accumulate=accumulate)
+    half = X.BF16_HALF if dtype is torch.bfloat16 else X.F32_STEP / 2
+    X.check(grad.cpu(), ref, X.sum_bound(ref, mag, max(LENGTHS), half), "grad_weights")
+
+
+@pytest.mark.parametrize("E,T", [(2, 5), (140, 150)])    # narrow tiles, wide tiles
+@pytest.mark.parametrize("K,N", [(65536, 8), (8, 65536)])
+def test_largest_features(gpu, E, T, K, N):
+    c = X.Case(gpu, T=T, k=1, E=E)
+    w, x, dy = c.randn(E, N, K, scale=K ** -0.5), c.randn(c.n, K), c.randn(c.n, N)
+    ref, mag = X.per_expert(c, x, w), X.per_expert(c, x.abs(), w.abs())
+    wd, xd, dyd = w.cuda(), c.buffer(RECV, x, 0.0), c.buffer(RECV, dy, 0.0)
+    out = gpu.moe_expert_gemm(c.ctx, xd, wd, c.handle)
+    X.check(c.rows_of(out, RECV)[0], ref, X.sum_bound(ref, mag, K, X.BF16_HALF), "out")
+    wt = w.transpose(1, 2).contiguous()
+    ref, mag = X.per_expert(c, dy, wt), X.per_expert(c, dy.abs(), wt.abs())
+    grad = gpu.moe_expert_gemm_backward_rows(c.ctx, dyd, wd, c.handle)
+    X.check(c.rows_of(grad, RECV)[0], ref, X.sum_bound(ref, mag, N, X.BF16_HALF), "grad_rows")
+    gw = gpu.moe_expert_gemm_backward_weights(c.ctx, dyd, xd, c.handle)
+    ref, mag = X.outer(c, dy, x, E), X.outer(c, dy.abs(), x.abs(), E)
+    X.check(gw.cpu(), ref, X.sum_bound(ref, mag, T, X.BF16_HALF), "grad_weights")
+    c.close()
+
+
+def test_matrices_past_4_gb(gpu):
+    """40 matrices of 8192 x 8192: the last ones start past 2^32 bytes, in the products and in fp32 gradients."""
+    E, K = 40, 8192
+    c = X.Case(gpu, T=2 * E, k=1, E=E)
+    w = torch.zeros((E, K, K), dtype=torch.bfloat16, device="cuda")
+    last = c.randn(K, K, scale=K ** -0.5)
+    w[E - 1] = last.cuda()
+    x = c.randn(c.n, K)
+    r = c.expert == E - 1
+    assert r.any()
+    out = c.rows_of(gpu.moe_expert_gemm(c.ctx, c.buffer(RECV, x, 0.0), w, c.handle), RECV)[0]
+    ref = x[r].double() @ last.double().t()
+    X.check(out[r], ref, X.sum_bound(ref, x[r].double().abs() @ last.double().abs().t(), K, X.BF16_HALF), "out")
+    assert (out[~r] == 0).all()
+    grad = c.rows_of(gpu.moe_expert_gemm_backward_rows(c.ctx, c.buffer(RECV, x, 0.0), w, c.handle), RECV)[0]
+    ref = x[r].double() @ last.double()
+    X.check(grad[r], ref, X.sum_bound(ref, x[r].double().abs() @ last.double().abs(), K, X.BF16_HALF), "grad_rows")
+    del w
+    gw = torch.empty((E, K, K), dtype=torch.float32, device="cuda")
+    xd = c.buffer(RECV, x, 0.0)
+    gpu.moe_expert_gemm_backward_weights(c.ctx, xd, xd, c.handle, grad_weights=gw)
+    ref = x[r].double().t() @ x[r].double()
+    X.check(gw[E - 1].cpu(), ref, X.sum_bound(ref, x[r].double().abs().t() @ x[r].double().abs(), int(r.sum()), X.F32_STEP / 2),
+            "grad_weights")
+    c.close()
+    del gw
+    torch.cuda.empty_cache()
+
+
+def test_padded_rows_past_4_gb(gpu):
+    """The padded layout's windows of the last experts start past 2^32 bytes."""
+    T, k, E, R, K, N = 64, 4, 256, 32, 8192, 16
+    c = X.Case(gpu, T=T, k=k, E=E, R=R, layout=1, src=31)
+    w, x = c.randn(E, N, K, scale=K ** -0.5), c.randn(c.n, K)
+    assert int(c.at[RECV].max()) * K * 2 > 2 ** 32
+    rows = torch.full((c.size[RECV], K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    rows[c.at[RECV].cuda()] = x.cuda()
+    ref, mag = X.per_expert(c, x, w), X.per_expert(c, x.abs(), w.abs())
+    out = gpu.moe_expert_gemm(c.ctx, rows, w.cuda(), c.handle)
+    X.check(out[c.at[RECV].cuda()].cpu(), ref, X.sum_bound(ref, mag, K, X.BF16_HALF), "out")
+    act = gpu.moe_swiglu(c.ctx, rows, c.handle, out=torch.zeros(c.size[RECV], K // 2, dtype=torch.bfloat16, device="cuda"))
+    ref = X.swiglu64(x)
+    X.check(act[c.at[RECV].cuda()].cpu(), ref, (X.BF16_HALF + 128 * X.F32_STEP) * ref.abs() + 2.0 ** -120, "act")
+    c.close()
+    del rows, out, act
+    torch.cuda.empty_cache()
+
+
+def test_contexts_on_concurrent_streams(gpu):
+    """Two contexts at once on two streams, neither of them the one their tensors were made on."""
+    cases = [X.Case(gpu, T=300, k=2, E=40, seed=s) for s in (1, 2)]
+    data = []
+    for c in cases:
+        w = c.randn(40, 528, 264, scale=0.06).cuda()
+        x, dy = c.buffer(RECV, c.randn(c.n, 264), 0.0), c.buffer(RECV, c.randn(c.n, 528), 0.0)
+
+        def calls(c=c, w=w, x=x, dy=dy):
+            y = gpu.moe_expert_gemm(c.ctx, x, w, c.handle)
+            return (y, gpu.moe_expert_gemm_backward_rows(c.ctx, dy, w, c.handle),
+                    gpu.moe_expert_gemm_backward_weights(c.ctx, dy, x, c.handle), gpu.moe_swiglu(c.ctx, y, c.handle))
+        data.append((calls, calls()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(data[i][0]())
+    torch.cuda.synchronize()
+    for i, c in enumerate(cases):
+        for g in got[i]:
+            for a, b in zip(g, data[i][1]):
+                n = c.n if a.dim() == 2 else a.shape[0]
+                assert torch.equal(a[:n], b[:n])
+        c.close()
+
+
+@pytest.mark.parametrize("T", [1, 24])
+def test_captured_fp8_decode_step_with_new_inputs(gpu, T):
+    """dispatch, product, quantising activation, product and combine as one graph, replayed on new tokens and new
+    routings, with eager work in between: every replay gives the eager bits."""
+    m, k, E, H, I = gpu, 2, 12, 512, 256
+    ctx = m.Context(m.make_config(T, H, E, 2, k, 1, m.MOE_QUANT_FP8_E4M3, m.MOE_LAYOUT_PADDED_LL))
+    g = torch.Generator().manual_seed(T)
+
+    def mats(n, kk):
+        q = (torch.randn(E, n, kk, generator=g) * 112).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        return q.cuda(), ((torch.rand(E, -(-n // 128), kk // 128, generator=g) + 0.5) / 112 * kk ** -0.5).cuda()
+    (q1, s1), (q2, s2) = mats(2 * I, H), mats(H, I)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    idx = torch.empty(T, k, dtype=torch.int64, device="cuda")
+    tw = torch.empty(T, k, device="cuda")
+    bufs, h = m.DispatchBuffers(ctx), m.Handle(ctx)
+    gu = torch.empty(T * k, 2 * I, dtype=torch.bfloat16, device="cuda")
+    a, sa = torch.empty(T * k, I, dtype=torch.uint8, device="cuda"), torch.empty(T * k, I // 128, device="cuda")
+    y = torch.empty(E * T * 2, H, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+
+    def new_inputs():
+        x.copy_(torch.randn(T, H, generator=g))
+        i = torch.rand(T, E, generator=g).topk(k, dim=1).indices
+        i[torch.rand(T, k, generator=g) < 0.2] = -1
+        idx.copy_(i)
+        tw.copy_(torch.rand(T, k, generator=g))
+
+    def step():
+        m.moe_dispatch(ctx, x, idx, bufs=bufs, handle=h)
+        m.moe_expert_gemm_fp8(ctx, bufs.recv_rows, bufs.recv_scales, q1, s1, h, out=gu, out_order=PACKED)
+        m.moe_swiglu_fp8(ctx, gu, h, out=a, scales=sa, order=PACKED)
+        m.moe_expert_gemm_fp8(ctx, a, sa, q2, s2, h, out=y, rows_order=PACKED)
+        m.moe_combine(ctx, y, tw, h, out=out)
+    side = torch.cuda.Stream()
+    new_inputs()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for _ in range(4):
+        new_inputs()
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        out.zero_()
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(got, out) and (T == 1 or out.abs().sum() > 0)
+    assert m.moe_poll_error(ctx)[0] == m.MOE_OK
+    ctx.close()
