@@ -227,3 +227,55 @@ def test_captured_fp8_decode_step_with_new_inputs(gpu, T):
         assert torch.equal(got, out) and (T == 1 or out.abs().sum() > 0)
     assert m.moe_poll_error(ctx)[0] == m.MOE_OK
     ctx.close()
+
+
+def test_handle_of_the_allocation_free_dispatch(gpu):
+    m = gpu
+    c = X.Case(m, T=50, k=2, E=8, empty=0.1)
+    scfg = m.StaticConfig(m.make_config(50, 128, 8, 1, 2))
+    bufs, h = m.DispatchBuffers(scfg), m.Handle(scfg)
+    m.moe_dispatch_noalloc(scfg, c.x, c.idx, bufs, h)
+    w = c.randn(8, 72, 128, scale=0.1).cuda()
+    a, b = m.moe_expert_gemm(c.ctx, bufs.recv_rows, w, h), m.moe_expert_gemm(c.ctx, c.bufs.recv_rows, w, c.handle)
+    assert torch.equal(a[:c.n], b[:c.n])
+    c.close()
+
+
+def test_activation_with_more_items_than_workgroups(gpu):
+    """65536 rows of 32768 channels and more: the kernel's workgroups loop."""
+    T, I = 70001, 32768
+    c = X.Case(gpu, T=T, k=1, E=4, hidden=8)
+    probe = torch.tensor([0, 1, 65535, 65536, 69999, T - 1])
+    v = c.randn(probe.numel(), 2 * I)
+    gu = torch.zeros(T, 2 * I, dtype=torch.bfloat16, device="cuda")
+    gu[probe.cuda()] = v.cuda()
+    out = torch.full((T, I), 7.0, dtype=torch.bfloat16, device="cuda")
+    gpu.moe_swiglu(c.ctx, gu, c.handle, out=out)
+    ref = X.swiglu64(v)
+    X.check(out[probe.cuda()].cpu(), ref, (X.BF16_HALF + 128 * X.F32_STEP) * ref.abs() + 2.0 ** -120, "act")
+    out[probe.cuda()] = 0
+    assert not out.any()
+    c.close()
+    del gu, out
+    torch.cuda.empty_cache()
+
+
+def test_grids_past_the_launch_limit_are_refused(gpu):
+    """More tiles than one launch may have.  (The handle's offsets still describe four tokens.)"""
+    import ctypes
+    m, M, k, N = gpu, 1 << 20, 32, 65536
+    ctx = m.Context(m.make_config(M, 8, 32, 1, k))
+    idx = torch.arange(32, device="cuda").repeat(4, 1)
+    bufs, h = m.moe_dispatch(ctx, torch.zeros(4, 8, dtype=torch.bfloat16, device="cuda"), idx)
+    w = torch.zeros(32, N, 8, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros(128, N, dtype=torch.bfloat16, device="cuda")
+
+    def call():
+        return m.load_library().moe_expert_gemm(ctx.handle, bufs.recv_rows.data_ptr(), 0, w.data_ptr(), 8, N,
+                                                ctypes.byref(h.c), out.data_ptr(), 0, 0)
+    assert call() == m.MOE_OK
+    h.c.num_tokens = M
+    assert call() == m.MOE_ERR_UNSUPPORTED
+    ctx.close()
+    del bufs, h, w, out
+    torch.cuda.empty_cache()
