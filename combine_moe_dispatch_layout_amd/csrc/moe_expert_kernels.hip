@@ -84,6 +84,11 @@ __device__ __forceinline__ int64_t xcd_tile(int b) {
     return ((int64_t)(i >> 5) << 8) + ((b & 7) << 5) + (i & 31);
 }
 
+// The same for many small blocks, four neighbouring tiles on one XCD: of the row tiles of a matrix (4 experts
+// x 64 rows in tiles of 32, 4096 x 4096 bf16: 49 us, 73 with neighbours spread over the XCDs), or of columns
+// that share lines of the output.
+__device__ __forceinline__ int xcd_tile4(int b) { return (b & ~31) | ((b & 7) << 2) | ((b >> 3) & 3); }
+
 // Order of the tiles of one matrix with `nj` row tiles and `ni` column tiles: bands of kBand row
 // tiles, column by column, so that 32 consecutive tiles touch about 4 + 8 panels.
 constexpr int kBand = 4;
@@ -586,11 +591,133 @@ __device__ __forceinline__ void rows_tile(const ExpertGemmArgs& a, const Tile& t
 }
 
 // ---------------------------------------------------------------- few rows
-// Narrow tiles for products with too few 256-column tiles to occupy the chip (a token or a few): 64
-// columns x 32 rows, four wavefronts, two workgroups a compute unit.  What counts here is the bytes
+// A token or a few: one wavefront multiplies 16 or 32 columns with up to 32 rows, and no operand passes
+// through LDS, so nothing is waited for but the wavefront's own loads.  The lanes of a matrix
+// instruction read 64 contiguous bytes of 16 matrix rows; 512 bytes of each row are on their way.
+// What bounds it is reading the matrices (201 MB alone take 35-39 us, 5.2-5.8 TB/s), and from about 16 rows
+// on the loads of the rows, which every wavefront repeats.  A token with 6 experts of 4096 x 4096 bf16 takes
+// 38 us (5.4 TB/s; 51 in the narrow tiles below), with 6 of 2048 x 7168 32 us (76), with 2 of 4096 x 4096 16 us (44).
+
+__device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t rsrc, uint32_t off) {
+    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)off, 0, 0));
+}
+__device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t rsrc, uint32_t off) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rsrc, (int)off, 0, 0));
+}
+
+// PS x QS subtiles of 16 x 16.
+template <bool FP8, int PS, int QS>
+struct FewBody {
+    // contraction bytes of one matrix instruction, and instructions that are loaded for ahead
+    static constexpr int kUnit = FP8 ? 128 : 64, kRing = 512 / kUnit, kChunks = kUnit / 64;
+    struct Unit {
+        i32x4 p[PS][kChunks], q[QS][kChunks];
+        float m, s[QS];   // fp8: scale of the column block, of the rows
+    };
+    __amdgpu_buffer_rsrc_t rp, rq, rm, rs;
+    int ld;   // bytes of a row
+
+    // Unit u of the lane's columns and rows; zeros past the row's end, as past the last row.  fp8 takes
+    // chunks g and g + 4 of 128 channels, for both operands.
+    __device__ __forceinline__ void load(Unit& x, int u, int lane) const {
+        const int at = u * kUnit + (lane >> 4) * 16, t = lane & 15;
+        const bool in = at < ld;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const uint32_t off = in ? (uint32_t)(t * ld + at + c * 64) : kOob, sub = (uint32_t)(16 * ld);
+#pragma unroll
+            for (int p = 0; p < PS; ++p) x.p[p][c] = load16(rp, off + p * sub);
+#pragma unroll
+            for (int q = 0; q < QS; ++q) x.q[q][c] = load16(rq, off + q * sub);
+        }
+        if constexpr (FP8) {
+            x.m = load4(rm, in ? (uint32_t)u * 4 : kOob);
+#pragma unroll
+            for (int q = 0; q < QS; ++q) x.s[q] = load4(rs, in ? (uint32_t)((t + 16 * q) * (ld / 128) + u) * 4 : kOob);
+        }
+    }
+    __device__ __forceinline__ static i32x8 join(const i32x4 (&v)[kChunks]) {
+        return i32x8{v[0].x, v[0].y, v[0].z, v[0].w, v[kChunks - 1].x, v[kChunks - 1].y, v[kChunks - 1].z, v[kChunks - 1].w};
+    }
+    __device__ __forceinline__ void run(f32x4 (&acc)[PS][QS], int lane) const {
+#pragma unroll
+        for (int p = 0; p < PS; ++p)
+#pragma unroll
+            for (int q = 0; q < QS; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // The loads stay in this order (the scheduler is fenced off), so that a use waits for its own only.
+        Unit ring[kRing];
+#pragma unroll
+        for (int u = 0; u < kRing; ++u) {
+            load(ring[u], u, lane);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        for (int first = 0; first * kUnit < ld; first += kRing) {
+#pragma unroll
+            for (int u = 0; u < kRing; ++u) {
+                Unit& x = ring[u];
+#pragma unroll
+                for (int p = 0; p < PS; ++p)
+#pragma unroll
+                    for (int q = 0; q < QS; ++q) {
+                        if constexpr (FP8) {
+                            const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                join(x.p[p]), join(x.q[q]), f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+                            const float sc = x.s[q] * x.m;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) acc[p][q][r] = __builtin_fmaf(d[r], sc, acc[p][q][r]);
+                        } else {
+                            acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(bf16x8, x.p[p][0]), __builtin_bit_cast(bf16x8, x.q[q][0]), acc[p][q], 0, 0, 0);
+                        }
+                    }
+                load(x, first + kRing + u, lane);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+};
+
+template <bool FP8, int PS, int QS>
+__device__ __forceinline__ void few_tile(const ExpertGemmArgs& a, const Tile& tl, int lane) {
+    constexpr int kSize = FP8 ? 1 : 2;
+    const int i0 = tl.col * PS * 16;
+    const int64_t qrow = seg_base(a.seg, tl.e, tl.start, a.q_padded) + tl.row;
+    const int64_t orow = seg_base(a.seg, tl.e, tl.start, a.out_padded) + tl.row;
+    FewBody<FP8, PS, QS> b;
+    b.ld = a.K * kSize;
+    b.rp = descriptor(static_cast<const char*>(a.p) + ((int64_t)tl.e * a.N + i0) * b.ld, min(PS * 16, a.N - i0) * b.ld);
+    b.rq = descriptor(static_cast<const char*>(a.q) + qrow * b.ld, tl.rows * b.ld);
+    if constexpr (FP8) {
+        const int kb = a.K / 128, nb = (a.N + 127) / 128;
+        b.rm = descriptor(a.p_scales + ((int64_t)tl.e * nb + i0 / 128) * kb, kb * 4);
+        b.rs = descriptor(a.q_scales + qrow * kb, tl.rows * kb * 4);
+    }
+    f32x4 acc[PS][QS];
+    b.run(acc, lane);
+#pragma unroll
+    for (int p = 0; p < PS; ++p)
+#pragma unroll
+        for (int q = 0; q < QS; ++q) {
+            const int i = i0 + 16 * p + 4 * (lane >> 4), j = q * 16 + (lane & 15);
+            if (i < a.N && j < tl.rows)
+                *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + (orow + j) * a.N + i) = bf16_pack(acc[p][q]);
+        }
+}
+
+// Tiles of 16 * PS columns and up to 16 * QS rows.
+template <bool FP8, int PS, int QS>
+__global__ __launch_bounds__(64, 2) void k_expert_rows_few(ExpertGemmArgs a) {
+    const Tile tl = find_tile(a.seg, xcd_tile4((int)blockIdx.x), 16 * QS, (a.N + PS * 16 - 1) / (PS * 16));
+    if (tl.e < 0) return;
+    if (QS > 1 && tl.rows > 16) few_tile<FP8, PS, QS>(a, tl, threadIdx.x);
+    else few_tile<FP8, PS, 1>(a, tl, threadIdx.x);
+}
+
+// ---------------------------------------------------------------- few tiles
+// Narrow tiles for products with too few 256-column tiles to occupy the chip but more rows than the above
+// takes: 64 columns x 32 rows, four wavefronts, two workgroups a compute unit.  What counts here is the bytes
 // on their way from memory, so the ring has kSmallStages stages, and the matrix instructions are
-// not scheduled by hand.  A token with 6 experts of 4096 x 4096 bf16 takes 51 us (3.9 TB/s; 32-column
-// tiles 48.7, but 8 experts with 8 rows each then 90 instead of 66; other starts than 0 no better).
+// not scheduled by hand.  8 experts x 16 rows, 4096 x 4096 bf16: 62 us (4.3 TB/s).
 constexpr int kSmallP = 64, kSmallQ = 32, kSmallWaves = 4, kSmallStages = 6;
 
 template <bool FP8>
@@ -682,7 +809,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_expert_rows_small(ExpertGe
     constexpr int kSize = FP8 ? 1 : 2;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int ntiles = (a.N + kSmallP - 1) / kSmallP;
-    const Tile tl = find_tile(a.seg, blockIdx.x, kSmallQ, ntiles);
+    const Tile tl = find_tile(a.seg, xcd_tile4((int)blockIdx.x), kSmallQ, ntiles);
     if (tl.e < 0) return;
     const int i0 = tl.col * kSmallP, ni = min(kSmallP, a.N - i0);
     const int64_t qrow = seg_base(a.seg, tl.e, tl.start, a.q_padded) + tl.row;
@@ -711,11 +838,13 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_expert_rows_small(ExpertGe
 constexpr int kTileBytes = 256 * kStepBytes;   // of one operand's stage
 constexpr int kWaves = 8;                      // of a workgroup (one workgroup a compute unit)
 
-// Products of at most this many wide tiles, half of the chip's compute units, run as narrow ones.
-// Wide against narrow, measured: 96 tiles (a token, 6 experts, 4096 x 4096 bf16) 70 and 51 us, 128 tiles (8
-// experts, 8 rows each) 90 and 66 us; 144 tiles (32 rows each) 88 and 150 us, 224 tiles (fp8, 7168 x
-// 2048) 23 and 32 us, 243 tiles (2056 x 1000) 24 and 38 us.
-constexpr int64_t kSmallTiles = 128;
+// Products of at most kWideTiles wide tiles, half of the chip's compute units, run as narrow tiles if those are at
+// most kSmallTiles.  Wide against narrow, cold matrices, us:
+//   4096 x 4096 bf16    8 experts x 16 rows 77 and 62, 4 x 64 rows 72 and 49, 1 x 512 rows 90 and 67
+//   more narrow tiles   6 x 64 rows 75 and 91, 4 x 256 rows 102 and 165
+//   more wide tiles     4096 x 1024, 40 x 20 rows 82 and 103; 4096 x 512, 100 x 8 rows 83 and 108
+//   fp8                 4096 x 4096, 1 x 512 rows 60 and 36; 2048 x 7168, 1 x 256 rows 33 and 21, 4 x 32 rows 24 and 18
+constexpr int64_t kWideTiles = 128, kSmallTiles = 1100;
 
 constexpr int max_of(int a, int b) { return a > b ? a : b; }
 
@@ -857,15 +986,37 @@ int64_t tile_bound(const ExpertGemmArgs& a, int64_t pairs, int bq, int64_t ni) {
 // A grid holds under 2^32 threads.
 bool grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }
 
+// Which products run on k_expert_rows_few, from the number of its tiles; cold matrices, us, this kernel
+// against the best of the others.
+// Up to a mean of eight rows an expert:
+//   bf16, 16 columns   4096 x 4096, 1 row each, 6 / 8 / 10 / 12 experts: 42 / 58 / 69 / 82 against 52 / 62 / 76 / 78;
+//                      8 rows each, 8 / 10 / 12 experts: 61 / 75 / 91 against 61 / 78 / 80
+//   fp8, 32 columns    7168 x 2048, 1 row each, 6 / 8 / 10 / 12 experts: 20 / 24 / 30 / 35 against 25 / 26 / 45 / 46;
+//                      8 rows each, 6 experts 23 against 25; 4096 x 7168, 16 experts 87 against 84
+// With any mean, 32 columns: 4096 x 4096 bf16, 2 / 4 / 6 experts of 32 rows 19 / 41 / 62 against 45 / 48 / 53, of 16
+// rows 16 / 34 / 54 against 44 / 48 / 52; 1 expert of 64 rows 18 against 42, of 256 rows (K = 2048) 32 against 22.
+constexpr int kFewMean = 8;
+constexpr int64_t kFewBf16 = 1280, kFewFp8 = 2816, kFewTiles = 1024;
+
+template <bool FP8, int PS, int QS>
+hipError_t launch_few(const ExpertGemmArgs& a, int64_t pairs, hipStream_t s) {
+    const int64_t blocks = (tile_bound(a, pairs, 16 * QS, (a.N + PS * 16 - 1) / (PS * 16)) + 31) / 32 * 32;
+    k_expert_rows_few<FP8, PS, QS><<<dim3((unsigned)blocks), dim3(64), 0, s>>>(a);
+    return hipGetLastError();
+}
+
 template <bool FP8, bool PMC>
 hipError_t launch_rows(const ExpertGemmArgs& a, int64_t pairs, hipStream_t s) {
     const int64_t ntiles = ((PMC ? a.K : a.N) + kTileP - 1) / kTileP;
     const int64_t tiles = tile_bound(a, pairs, 256, ntiles);
     if constexpr (!PMC) {
-        if (tiles <= kSmallTiles) {
-            const int64_t blocks = tile_bound(a, pairs, kSmallQ, (a.N + kSmallP - 1) / kSmallP);
-            if (!grid_fits(blocks, 64 * kSmallWaves)) return hipErrorInvalidConfiguration;
-            k_expert_rows_small<FP8><<<dim3((unsigned)blocks), dim3(64 * kSmallWaves), 0, s>>>(a);
+        const int64_t active = pairs < a.seg.E ? pairs : a.seg.E, columns = (a.N + 31) / 32;
+        if (pairs <= kFewMean * active && active * columns <= (FP8 ? kFewFp8 : kFewBf16))
+            return launch_few<FP8, FP8 ? 2 : 1, 1>(a, pairs, s);
+        if (tile_bound(a, pairs, 32, columns) <= kFewTiles) return launch_few<FP8, 2, 2>(a, pairs, s);
+        const int64_t small = tile_bound(a, pairs, kSmallQ, (a.N + kSmallP - 1) / kSmallP);
+        if (tiles <= kWideTiles && small <= kSmallTiles) {
+            k_expert_rows_small<FP8><<<dim3((unsigned)((small + 31) / 32 * 32)), dim3(64 * kSmallWaves), 0, s>>>(a);
             return hipGetLastError();
         }
     }

@@ -279,3 +279,67 @@ def test_grids_past_the_launch_limit_are_refused(gpu):
     ctx.close()
     del bufs, h, w, out
     torch.cuda.empty_cache()
+
+
+# Few tiles.  Lengths of a mean of at most 8 (one wavefront a tile of 16 rows), of more (32 rows), and of enough rows
+# and columns for the narrow tiles of a whole workgroup, each on both sides of its tile sizes.
+FEW = {
+    "mean of 5": ([0, 1, 2, 16, 17, 0, 3, 5, 1, 33, 2, 0, 4, 1, 6, 0], [8, 16, 24, 40, 1000]),
+    "mean of 31": ([0, 1, 15, 16, 17, 31, 32, 33, 64, 100], [8, 24, 40, 72, 1000]),
+    "mean of 65": ([0, 1, 31, 32, 33, 63, 64, 65, 100, 129, 200], [1064, 1096]),
+}
+FEW_CASES = [(name, N) for name in FEW for N in FEW[name][1]]
+
+
+def few_case(gpu, name):
+    lengths = FEW[name][0]
+    idx = torch.arange(len(lengths)).repeat_interleave(torch.tensor(lengths))
+    idx = idx[torch.randperm(idx.numel(), generator=torch.Generator().manual_seed(3))].reshape(-1, 1)
+    return X.Case(gpu, T=idx.numel(), k=1, E=len(lengths), R=1, idx=idx)
+
+
+@pytest.mark.parametrize("K", [8, 40, 64, 248, 256, 264, 520, 1032, 2056])
+@pytest.mark.parametrize("name,N", FEW_CASES)
+def test_gemm_of_few_rows(gpu, name, N, K):
+    c = few_case(gpu, name)
+    w, x = c.randn(c.E, N, K, scale=K ** -0.5), c.randn(c.n, K)
+    ref, mag = X.per_expert(c, x, w), X.per_expert(c, x.abs(), w.abs())
+    out = torch.full((c.n, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    gpu.moe_expert_gemm(c.ctx, c.buffer(RECV, x, float("nan")), w.cuda(), c.handle, out=out)
+    X.check(c.rows_of(out, RECV)[0], ref, X.sum_bound(ref, mag, K, X.BF16_HALF), "out")
+    c.close()
+
+
+@pytest.mark.parametrize("blocks", [1, 2, 3, 4, 5, 8, 9, 17])
+@pytest.mark.parametrize("name,N", FEW_CASES)
+def test_gemm_fp8_of_few_rows(gpu, name, N, blocks):
+    c, K = few_case(gpu, name), 128 * blocks
+    wq = (c.randn(c.E, N, K, scale=112.0).float().clamp(-448, 448)).to(torch.float8_e4m3fn).view(torch.uint8)
+    ws = torch.rand(c.E, -(-N // 128), blocks, generator=c.gen) * 0.01 + 1e-4
+    xq, xs = X.quantise(c.randn(c.n, K).float() * torch.rand(c.n, 1, generator=c.gen) * 10)
+    w = X.e4m3(wq) * X.expand(ws, N, K)
+    x = X.e4m3(xq) * xs.double().repeat_interleave(128, 1)
+    ref, mag = X.per_expert(c, x, w), X.per_expert(c, x.abs(), w.abs())
+    out = gpu.moe_expert_gemm_fp8(c.ctx, c.buffer(RECV, xq, 0x7F), c.buffer(RECV, xs, float("nan")), wq.cuda(), ws.cuda(), c.handle)
+    X.check(c.rows_of(out, RECV)[0], ref, X.sum_bound(ref, mag, K, X.BF16_HALF), "out")
+    c.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_largest_features_of_one_row(gpu, fp8):
+    """The longest contraction and the most columns that a token can have."""
+    for K, N in ((65536, 136), (128, 65536)):
+        c = X.Case(gpu, T=1, k=2, E=3, hidden=128)
+        if fp8:
+            wq = (c.randn(c.E, N, K, scale=112.0).float().clamp(-448, 448)).to(torch.float8_e4m3fn).view(torch.uint8)
+            ws = torch.rand(c.E, -(-N // 128), K // 128, generator=c.gen) * 0.01 + 1e-4
+            xq, xs = X.quantise(c.randn(c.n, K).float())
+            w, x = X.e4m3(wq) * X.expand(ws, N, K), X.e4m3(xq) * xs.double().repeat_interleave(128, 1)
+            out = gpu.moe_expert_gemm_fp8(c.ctx, c.buffer(RECV, xq, 0x7F), c.buffer(RECV, xs, float("nan")), wq.cuda(),
+                                          ws.cuda(), c.handle)
+        else:
+            w, x = c.randn(c.E, N, K, scale=K ** -0.5), c.randn(c.n, K)
+            out = gpu.moe_expert_gemm(c.ctx, c.buffer(RECV, x, float("nan")), w.cuda(), c.handle)
+        ref, mag = X.per_expert(c, x, w), X.per_expert(c, x.abs(), w.abs())
+        X.check(c.rows_of(out, RECV)[0], ref, X.sum_bound(ref, mag, K, X.BF16_HALF), "out")
+        c.close()
