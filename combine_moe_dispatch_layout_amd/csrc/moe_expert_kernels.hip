@@ -713,32 +713,34 @@ __global__ __launch_bounds__(64, 2) void k_expert_rows_few(ExpertGemmArgs a) {
     else few_tile<FP8, PS, 1>(a, tl, threadIdx.x);
 }
 
-// ---------------------------------------------------------------- few tiles
-// Narrow tiles for products with too few 256-column tiles to occupy the chip but more rows than the above
-// takes: 64 columns x 32 rows, four wavefronts, two workgroups a compute unit.  What counts here is the bytes
-// on their way from memory, so the ring has kSmallStages stages, and the matrix instructions are
-// not scheduled by hand.  8 experts x 16 rows, 4096 x 4096 bf16: 62 us (4.3 TB/s).
-constexpr int kSmallP = 64, kSmallQ = 32, kSmallWaves = 4, kSmallStages = 6;
+// ---------------------------------------------------------------- narrow tiles
+// Narrow tiles for products with too few 256-column tiles to occupy the chip: 64 x 64 or 128 x 128, two
+// workgroups a compute unit (64 KB of stages each), so that one computes while the other waits. Steps are not
+// scheduled by hand.  4096 x 4096 bf16, 1 expert: 512 rows 46 us (0.38 PFLOP/s, 64 x 64), 2048 rows
+// 76 us (0.90, 128 x 128); bound by the latency of a step, of which LDS holds one (128 x 128) or three ahead.
+template <bool FP8, int P, int Q, int NW, int STAGES>
+struct NarrowBody {
+    using LP = LoadKC<P, NW, !FP8>;
+    using LQ = LoadKC<Q, NW, !FP8>;
+    static constexpr int WP = P / 32, WQ = NW / WP, QS = Q / 16 / WQ;   // a wavefront owns 32 columns x 16 QS rows
+    static_assert(WP * WQ == NW && QS * WQ * 16 == Q && NW >= 4, "");
+    static constexpr int kRowScales = (Q + 63) / 64 * 256;              // bytes; then the column block's
+    static constexpr int kScales = FP8 ? kRowScales + 256 : 0;
+    static constexpr int kStage = (P + Q) * kStepBytes + kScales;
+    static constexpr int kLds = kStage * STAGES;
 
-template <bool FP8>
-struct SmallBody {
-    using LP = LoadKC<kSmallP, kSmallWaves, !FP8>;
-    using LQ = LoadKC<kSmallQ, kSmallWaves, !FP8>;
-    static constexpr int kScales = FP8 ? 512 : 0;
-    static constexpr int kStage = (kSmallP + kSmallQ) * kStepBytes + kScales;
-    static constexpr int kLds = kStage * kSmallStages;
-
-    // Scales of one stage: 32 rows', and the one of the tile's 128-column block at byte 256.
+    // Scales of one stage: the rows', and the one of the tile's 128-column block.
     struct Scales {
         __amdgpu_buffer_rsrc_t rsrc;
         uint32_t voff;
         int kb, lds;
         __device__ __forceinline__ void init(const float* rows, int valid, const float* mat, int kblocks, int w, int lane) {
             kb = kblocks;
-            const bool r = (w & 1) == 0;
+            const int part = w & 3;   // wavefront 0 loads 64 rows', 1 the next 64's, if there are, 2 and 3 the block's
+            const bool r = part * 256 < kRowScales;
             rsrc = r ? descriptor(rows, valid * kb * 4) : descriptor(mat, kb * 4);
-            voff = lane < (r ? kSmallQ : 1) ? (uint32_t)(lane * kb) * 4 : kOob;
-            lds = r ? 0 : 256;
+            voff = r ? (uint32_t)((part * 64 + lane) * kb) * 4 : lane == 0 ? 0 : kOob;
+            lds = r ? part * 256 : kRowScales;
         }
         __device__ __forceinline__ void issue(char* stage, int step) const {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, LDS_PTR(void, stage + lds), 4, step < kb ? voff + step * 4 : kOob, 0,
@@ -746,11 +748,10 @@ struct SmallBody {
         }
     };
 
-    // Wavefront w: columns 32 (w % 2) .. +31, rows 16 (w / 2) .. +15.
     __device__ __forceinline__ static void run(char* lds, const LP& lp, const LQ& lq, const Scales& ls, int steps, int rows,
-                                               f32x4 (&acc)[2], int w, int lane) {
+                                               f32x4 (&acc)[2][QS], int w, int lane) {
         constexpr int kLoads = LP::kInstr + LQ::kInstr + (FP8 ? 1 : 0);
-        const int g = lane >> 4, t = lane & 15, wp = w & 1, wq = w >> 1;
+        const int g = lane >> 4, t = lane & 15, wp = w % WP, wq = w / WP;
         auto fill = [&](int step, int slot) {
             char* st = lds + slot * kStage;
             const auto sp = lp.step_of(step);
@@ -758,60 +759,72 @@ struct SmallBody {
 #pragma unroll
             for (int l = 0; l < LP::kInstr; ++l) lp.issue(st, sp, l);
 #pragma unroll
-            for (int l = 0; l < LQ::kInstr; ++l) lq.issue(st + kSmallP * kStepBytes, sq, l);
-            if constexpr (FP8) ls.issue(st + (kSmallP + kSmallQ) * kStepBytes, step);
+            for (int l = 0; l < LQ::kInstr; ++l) lq.issue(st + P * kStepBytes, sq, l);
+            if constexpr (FP8) ls.issue(st + (P + Q) * kStepBytes, step);
         };
-        acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < kSmallStages - 1; ++s) fill(s, s);
-        int cur = 0, nxt = kSmallStages - 1;
+        for (int q = 0; q < QS; ++q) acc[0][q] = acc[1][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s) fill(s, s);
+        int cur = 0, nxt = STAGES - 1;
         for (int step = 0; step < steps; ++step) {
-            wait_loads<(kSmallStages - 2) * kLoads>();
+            wait_loads<(STAGES - 2) * kLoads>();
             lds_barrier();   // this step has arrived, and everyone is done with the one before
-            fill(step + kSmallStages - 1, nxt);   // past the end it reads nothing
+            fill(step + STAGES - 1, nxt);   // past the end it reads nothing
             const char* sp = lds + cur * kStage;
-            const char* sq = sp + kSmallP * kStepBytes;
-            if (wq * 16 < rows) {
+            const char* sq = sp + P * kStepBytes;
+            if (wq * QS * 16 < rows) {
                 if constexpr (FP8) {
-                    const char* sc = sq + kSmallQ * kStepBytes;
-                    const i32x8 q = LQ::frag8(sq, wq * 16 + t, g);
-                    const float s = *reinterpret_cast<const float*>(sc + (wq * 16 + t) * 4) *
-                                    *reinterpret_cast<const float*>(sc + 256);
+                    const char* sc = sq + Q * kStepBytes;
+                    i32x8 pf[2];
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            LP::frag8(sp, wp * 32 + p * 16 + t, g), q, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+                    for (int p = 0; p < 2; ++p) pf[p] = LP::frag8(sp, wp * 32 + p * 16 + t, g);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[p][r] = __builtin_fmaf(d[r], s, acc[p][r]);
+                    for (int q = 0; q < QS; ++q) {
+                        const int row = (wq * QS + q) * 16 + t;
+                        const i32x8 qf = LQ::frag8(sq, row, g);
+                        const float s =
+                            *reinterpret_cast<const float*>(sc + row * 4) * *reinterpret_cast<const float*>(sc + kRowScales);
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                pf[p], qf, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) acc[p][q][r] = __builtin_fmaf(d[r], s, acc[p][q][r]);
+                        }
                     }
                 } else {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const bf16x8 q = LQ::frag(sq, wq * 16 + t, h * 4 + g);
+                        bf16x8 pf[2];
 #pragma unroll
-                        for (int p = 0; p < 2; ++p)
-                            acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                LP::frag(sp, wp * 32 + p * 16 + t, h * 4 + g), q, acc[p], 0, 0, 0);
+                        for (int p = 0; p < 2; ++p) pf[p] = LP::frag(sp, wp * 32 + p * 16 + t, h * 4 + g);
+#pragma unroll
+                        for (int q = 0; q < QS; ++q) {
+                            const bf16x8 qf = LQ::frag(sq, (wq * QS + q) * 16 + t, h * 4 + g);
+#pragma unroll
+                            for (int p = 0; p < 2; ++p)
+                                acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[p], qf, acc[p][q], 0, 0, 0);
+                        }
                     }
                 }
             }
-            cur = cur == kSmallStages - 1 ? 0 : cur + 1;
-            nxt = nxt == kSmallStages - 1 ? 0 : nxt + 1;
+            cur = cur == STAGES - 1 ? 0 : cur + 1;
+            nxt = nxt == STAGES - 1 ? 0 : nxt + 1;
         }
         wait_loads<0>();   // nothing may be on its way into LDS when the workgroup ends
     }
 };
 
-template <bool FP8>
-__global__ __launch_bounds__(64 * kSmallWaves) void k_expert_rows_small(ExpertGemmArgs a) {
-    using B = SmallBody<FP8>;
+template <bool FP8, int P, int Q, int NW, int STAGES>
+__global__ __launch_bounds__(64 * NW) void k_expert_rows_narrow(ExpertGemmArgs a) {
+    using B = NarrowBody<FP8, P, Q, NW, STAGES>;
     __shared__ __align__(1024) char lds[B::kLds];
     constexpr int kSize = FP8 ? 1 : 2;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int ntiles = (a.N + kSmallP - 1) / kSmallP;
-    const Tile tl = find_tile(a.seg, xcd_tile4((int)blockIdx.x), kSmallQ, ntiles);
+    const Tile tl = find_tile(a.seg, xcd_tile4((int)blockIdx.x), Q, (a.N + P - 1) / P);
     if (tl.e < 0) return;
-    const int i0 = tl.col * kSmallP, ni = min(kSmallP, a.N - i0);
+    const int i0 = tl.col * P, ni = min(P, a.N - i0);
     const int64_t qrow = seg_base(a.seg, tl.e, tl.start, a.q_padded) + tl.row;
     const int64_t orow = seg_base(a.seg, tl.e, tl.start, a.out_padded) + tl.row;
     const int64_t ld = (int64_t)a.K * kSize;
@@ -824,27 +837,22 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_expert_rows_small(ExpertGe
         const int kb = a.K / 128, nb = (a.N + 127) / 128;
         ls.init(a.q_scales + qrow * kb, tl.rows, a.p_scales + ((int64_t)tl.e * nb + i0 / 128) * kb, kb, w, lane);
     }
-    f32x4 acc[2];
+    f32x4 acc[2][B::QS];
     B::run(lds, lp, lq, ls, (int)((ld + kStepBytes - 1) / kStepBytes), tl.rows, acc, w, lane);
-    const int j = (w >> 1) * 16 + (lane & 15);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        const int i = (w & 1) * 32 + p * 16 + 4 * (lane >> 4);
-        if (j < tl.rows && i < ni)
-            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + (orow + j) * a.N + i0 + i) = bf16_pack(acc[p]);
+    for (int q = 0; q < B::QS; ++q) {
+        const int j = (w / B::WP * B::QS + q) * 16 + (lane & 15);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int i = (w % B::WP) * 32 + p * 16 + 4 * (lane >> 4);
+            if (j < tl.rows && i < ni)
+                *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + (orow + j) * a.N + i0 + i) = bf16_pack(acc[p][q]);
+        }
     }
 }
 
 constexpr int kTileBytes = 256 * kStepBytes;   // of one operand's stage
 constexpr int kWaves = 8;                      // of a workgroup (one workgroup a compute unit)
-
-// Products of at most kWideTiles wide tiles, half of the chip's compute units, run as narrow tiles if those are at
-// most kSmallTiles.  Wide against narrow, cold matrices, us:
-//   4096 x 4096 bf16    8 experts x 16 rows 77 and 62, 4 x 64 rows 72 and 49, 1 x 512 rows 90 and 67
-//   more narrow tiles   6 x 64 rows 75 and 91, 4 x 256 rows 102 and 165
-//   more wide tiles     4096 x 1024, 40 x 20 rows 82 and 103; 4096 x 512, 100 x 8 rows 83 and 108
-//   fp8                 4096 x 4096, 1 x 512 rows 60 and 36; 2048 x 7168, 1 x 256 rows 33 and 21, 4 x 32 rows 24 and 18
-constexpr int64_t kWideTiles = 128, kSmallTiles = 1100;
 
 constexpr int max_of(int a, int b) { return a > b ? a : b; }
 
@@ -986,17 +994,23 @@ int64_t tile_bound(const ExpertGemmArgs& a, int64_t pairs, int bq, int64_t ni) {
 // A grid holds under 2^32 threads.
 bool grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }
 
-// Which products run on k_expert_rows_few, from the number of its tiles; cold matrices, us, this kernel
-// against the best of the others.
-// Up to a mean of eight rows an expert:
-//   bf16, 16 columns   4096 x 4096, 1 row each, 6 / 8 / 10 / 12 experts: 42 / 58 / 69 / 82 against 52 / 62 / 76 / 78;
-//                      8 rows each, 8 / 10 / 12 experts: 61 / 75 / 91 against 61 / 78 / 80
-//   fp8, 32 columns    7168 x 2048, 1 row each, 6 / 8 / 10 / 12 experts: 20 / 24 / 30 / 35 against 25 / 26 / 45 / 46;
-//                      8 rows each, 6 experts 23 against 25; 4096 x 7168, 16 experts 87 against 84
-// With any mean, 32 columns: 4096 x 4096 bf16, 2 / 4 / 6 experts of 32 rows 19 / 41 / 62 against 45 / 48 / 53, of 16
-// rows 16 / 34 / 54 against 44 / 48 / 52; 1 expert of 64 rows 18 against 42, of 256 rows (K = 2048) 32 against 22.
+// Which kernel a forward product runs on, from the numbers of its tiles, were its rows spread evenly over the
+// experts (as many as there are rows, at most): the smallest
+// tiles that still run together.  Cold matrices, us, against the best of the others.
+//   A mean of up to eight rows: one wavefront a tile.
+//     bf16, 16 columns   4096 x 4096, 1 row each, 6 / 8 / 10 / 12 experts: 38 / 57 / 68 / 83 against 52 / 62 / 76 / 78;
+//                        8 rows each, 8 / 10 / 12 experts: 61 / 75 / 91 against 61 / 78 / 80
+//     fp8, 32 columns    2048 x 7168, 1 row each, 6 / 8 / 10 / 12 experts: 20 / 24 / 30 / 35 against 25 / 26 / 44 / 46;
+//                        8 rows each, 6 / 8 experts: 22 / 27 against 25 / 26; 7168 x 4096, 16 x 1 row 87 against 84
+//   Few tiles, any mean, 32 columns: 4096 x 4096 bf16, 2 / 4 / 6 experts of 32 rows 19 / 41 / 62 against 45 / 48 / 53, of
+//     16 rows 16 / 34 / 54 against 44 / 48 / 52; 1 expert of 64 rows 18 against 42.
+//   64 x 64 tiles that run together (two a compute unit): 4096 x 4096 bf16, 8 experts of 16 rows 62, 128 x 128 69,
+//     256 columns 77; 1 x 512 rows 46 / 57 / 90; beyond, 9 x 64 rows 108 / 82 / 83.
+//   128 x 128 tiles that run together, where 256 columns would leave compute units idle: 4096 x 4096 bf16, 4 x 256 rows
+//     64 against 103, 1 x 2048 rows 76 against 102; with more tiles, 12 x 256 rows 171 against 128; where 256 columns
+//     fill the chip, 16 x 64 rows about 130 against 101.  fp8 with half of a tile's rows idle: 9 x 64 rows 57 against 48.
 constexpr int kFewMean = 8;
-constexpr int64_t kFewBf16 = 1280, kFewFp8 = 2816, kFewTiles = 1024;
+constexpr int64_t kFewBf16 = 1280, kFewFp8 = 2816, kFewTiles = 640, kNarrowTiles = 512, kWideTiles = 256;
 
 template <bool FP8, int PS, int QS>
 hipError_t launch_few(const ExpertGemmArgs& a, int64_t pairs, hipStream_t s) {
@@ -1005,20 +1019,26 @@ hipError_t launch_few(const ExpertGemmArgs& a, int64_t pairs, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <bool FP8, int P, int Q, int NW, int STAGES>
+hipError_t launch_narrow(const ExpertGemmArgs& a, int64_t pairs, hipStream_t s) {
+    const int64_t blocks = (tile_bound(a, pairs, Q, (a.N + P - 1) / P) + 31) / 32 * 32;
+    k_expert_rows_narrow<FP8, P, Q, NW, STAGES><<<dim3((unsigned)blocks), dim3(64 * NW), 0, s>>>(a);
+    return hipGetLastError();
+}
+
 template <bool FP8, bool PMC>
 hipError_t launch_rows(const ExpertGemmArgs& a, int64_t pairs, hipStream_t s) {
     const int64_t ntiles = ((PMC ? a.K : a.N) + kTileP - 1) / kTileP;
     const int64_t tiles = tile_bound(a, pairs, 256, ntiles);
     if constexpr (!PMC) {
-        const int64_t active = pairs < a.seg.E ? pairs : a.seg.E, columns = (a.N + 31) / 32;
-        if (pairs <= kFewMean * active && active * columns <= (FP8 ? kFewFp8 : kFewBf16))
-            return launch_few<FP8, FP8 ? 2 : 1, 1>(a, pairs, s);
-        if (tile_bound(a, pairs, 32, columns) <= kFewTiles) return launch_few<FP8, 2, 2>(a, pairs, s);
-        const int64_t small = tile_bound(a, pairs, kSmallQ, (a.N + kSmallP - 1) / kSmallP);
-        if (tiles <= kWideTiles && small <= kSmallTiles) {
-            k_expert_rows_small<FP8><<<dim3((unsigned)((small + 31) / 32 * 32)), dim3(64 * kSmallWaves), 0, s>>>(a);
-            return hipGetLastError();
-        }
+        const int64_t active = pairs < a.seg.E ? pairs : a.seg.E, mean = (pairs + active - 1) / active;
+        // tiles of bq rows x cols columns, were the rows spread evenly
+        auto even = [&](int64_t bq, int64_t cols) { return active * ((mean + bq - 1) / bq) * ((a.N + cols - 1) / cols); };
+        if (mean <= kFewMean && even(32, 32) <= (FP8 ? kFewFp8 : kFewBf16)) return launch_few<FP8, FP8 ? 2 : 1, 1>(a, pairs, s);
+        if (even(32, 32) <= kFewTiles) return launch_few<FP8, 2, 2>(a, pairs, s);
+        if (even(64, 64) <= kNarrowTiles) return launch_narrow<FP8, 64, 64, 4, 4>(a, pairs, s);
+        if (even(128, 128) <= kNarrowTiles && even(256, 256) < kWideTiles && (!FP8 || mean > 64))
+            return launch_narrow<FP8, 128, 128, 8, 2>(a, pairs, s);
     }
     const int64_t blocks = (tiles + 255) / 256 * 256;
     if (!grid_fits(blocks, 64 * kWaves)) return hipErrorInvalidConfiguration;

@@ -282,11 +282,12 @@ def test_grids_past_the_launch_limit_are_refused(gpu):
 
 
 # Few tiles.  Lengths of a mean of at most 8 (one wavefront a tile of 16 rows), of more (32 rows), and of enough rows
-# and columns for the narrow tiles of a whole workgroup, each on both sides of its tile sizes.
+# and columns for the narrow tiles of a whole workgroup (64 x 64, 128 x 128), each on both sides of its tile sizes.
 FEW = {
     "mean of 5": ([0, 1, 2, 16, 17, 0, 3, 5, 1, 33, 2, 0, 4, 1, 6, 0], [8, 16, 24, 40, 1000]),
     "mean of 31": ([0, 1, 15, 16, 17, 31, 32, 33, 64, 100], [8, 24, 40, 72, 1000]),
     "mean of 65": ([0, 1, 31, 32, 33, 63, 64, 65, 100, 129, 200], [1064, 1096]),
+    "mean of 114": ([0, 1, 16, 63, 64, 65, 127, 128, 129, 255, 256, 257], [1608, 2056]),
 }
 FEW_CASES = [(name, N) for name in FEW for N in FEW[name][1]]
 
