@@ -48,12 +48,14 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 #define LDS_PTR(T, p) ((__attribute__((address_space(3))) T*)(p))
 
 constexpr int kStepBytes = 128;          // contraction bytes of a KC stage row: 64 bf16 or 128 fp8
 constexpr int kStepC = 64;               // contraction elements of a bf16 stage
 constexpr int kTileP = 256;              // i extent of a tile
+constexpr int kNonTemporal = 2;          // cache policy of a buffer access
 constexpr uint32_t kOob = 0x80000000u;   // past the end of every descriptor (they hold under 2^31 bytes)
 
 __device__ __forceinline__ uint32_t bf16_bits(float f) {
@@ -513,12 +515,16 @@ struct TileBody {
     // bf16 stores of the tile: out points at its first output, ld is its row length; i < ni, j < nj.  A
     // lane holds four columns of one row: 16 rows of kCols columns at a time go through LDS, so that a
     // store writes whole 128-byte lines (direct 8-byte stores reach them in four parts).  A row's
-    // 16-byte chunk c sits at c ^ row.
+    // 16-byte chunk c sits at c ^ row.  The stores pass the caches (non-temporal) where rows are whole lines; else
+    // two tiles share lines, which meet in L2 (gradients of 64 matrices of 4104 x 4096: 0.55 ms, 1.23 past the
+    // caches; of 4096 x 4096 0.39 past them, 0.44 not).
     static constexpr int kCols = PS >= 4 ? 64 : PS * 16, kChunks = kCols / 8;
     __device__ __forceinline__ static void store(uint16_t* out, int64_t ld, int ni, int nj, const f32x4 (&acc)[PS][QS],
                                                  char* scratch, int w, int lane) {
         const int wp = w % WP, wq = w / WP, g = lane >> 4, t = lane & 15;
         char* mine = scratch + w * 2048;
+        const auto rsrc = descriptor(out, ((nj - 1) * (int)ld + ni) * 2);
+        const bool whole = ld % 64 == 0;
 #pragma unroll
         for (int q = 0; q < QS; ++q) {
 #pragma unroll
@@ -536,7 +542,9 @@ struct TileBody {
                     const int r = k * (64 / kChunks) + lane / kChunks, c = lane % kChunks;
                     const i32x4 v = *reinterpret_cast<const i32x4*>(mine + r * kCols * 2 + (((c ^ r) & (kChunks - 1)) << 4));
                     const int j = wq * QS * 16 + q * 16 + r, i = (wp * PS + p0) * 16 + c * 8;
-                    if (j < nj && i < ni) __builtin_nontemporal_store(v, reinterpret_cast<i32x4*>(out + (int64_t)j * ld + i));
+                    const int at = j < nj && i < ni ? (j * (int)ld + i) * 2 : (int)kOob;   // past the end nothing is stored
+                    if (whole) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, at, 0, kNonTemporal);
+                    else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, at, 0, 0);
                 }
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
             }
@@ -908,10 +916,47 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_rows(ExpertG
 }
 
 // ---------------------------------------------------------------- weights gradient
-// Tiles of 256 x 256 over every matrix, also of experts without rows (they get zeros).  With few rows an
-// expert it is bound by writing the gradients: 64 matrices of 4096 x 4096 take 0.42 ms at 16 rows each (5.1
-// TB/s written), 0.54 at 128, 1.7 at 768 (0.98 PFLOP/s), 3.6 at 2048 (1.21).
+// Experts with rows (or without), by number.  A lane knows min(16, ceil(E / 64)) of them.
+struct ExpertList {
+    uint32_t mask;   // bit u: the lane's expert u is in the list
+    int incl;        // experts in the list up to the lane's last
+    int per;
+    __device__ __forceinline__ void init(const Segments& s, bool with_rows, int lane) {
+        constexpr int kPer = (MOE_MAX_EXPERTS + 63) / 64;
+        per = (s.E + 63) / 64;
+        int off[kPer + 1];
+#pragma unroll
+        for (int u = 0; u <= kPer; ++u)
+            if (u <= per) off[u] = s.eoff[min(lane * per + u, s.E)];
+        mask = 0;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            if (u >= per) break;
+            if (lane * per + u < s.E && (seg_rows(s, off[u], off[u + 1]) > 0) == with_rows) mask |= 1u << u;
+        }
+        incl = __popc(mask);
+#pragma unroll
+        for (int step = 1; step < 64; step <<= 1) {
+            const int u = __shfl_up(incl, step, 64);
+            if (lane >= step) incl += u;
+        }
+    }
+    __device__ __forceinline__ int count() const { return __builtin_amdgcn_readlane(incl, 63); }
+    // The n-th, n < count().
+    __device__ __forceinline__ int at(int n) const {
+        const int owner = __ffsll((unsigned long long)__ballot(n < incl)) - 1;
+        uint32_t m = __builtin_amdgcn_readlane(mask, owner);
+        for (int skip = n - __builtin_amdgcn_readlane(incl, owner) + __popc(m); skip > 0; --skip) m &= m - 1;
+        return owner * per + __ffs(m) - 1;
+    }
+};
+
+// Tiles of 256 x 256 over the matrices of experts with rows; those of the others are zeroed as one run of
+// memory (160 experts of 2320 x 624 with 2 rows in all: 463 MB, 90 us, as tiles of zeros 225).  With few rows an
+// expert it is bound by writing the gradients: 64 matrices of 4096 x 4096 take 0.39 ms at 4 rows each (5.5 TB/s
+// written), 0.54 at 128, 1.64 at 768 (1.01 PFLOP/s), 3.6 at 2048 (1.21).
 constexpr int kWeightsGradBlocks = 256;
+constexpr int kZeroChunk = 64 * 1024;   // bytes of zeros a workgroup writes in turn
 
 __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad(ExpertGemmArgs a) {
     using B = TileBody<kWaves, 256, 2, 2, false, true, true>;
@@ -920,15 +965,34 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad
     const Stage st[2] = {{p0, q0}, {p1, q1}};
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int kt = (a.K + kTileP - 1) / kTileP, nt = (a.N + 255) / 256;
-    const int64_t tiles = (int64_t)a.seg.E * kt * nt;
+    ExpertList list;
+    list.init(a.seg, true, lane);
+    const int64_t tiles = (int64_t)list.count() * kt * nt;
+    auto zero = [&] {
+        if (a.accumulate || list.count() == a.seg.E) return;
+        ExpertList none;
+        none.init(a.seg, false, lane);
+        const int64_t bytes = (int64_t)a.N * a.K * (a.out_f32 ? 4 : 2), chunks = (bytes + kZeroChunk - 1) / kZeroChunk;
+        for (int64_t c = blockIdx.x; c < none.count() * chunks; c += kWeightsGradBlocks) {
+            const int n = (int)(c / chunks);
+            const int64_t from = (c - n * chunks) * kZeroChunk, to = min(from + kZeroChunk, bytes);
+            char* out = static_cast<char*>(a.out) + none.at(n) * bytes;
+            for (int64_t b = from + threadIdx.x * 16; b < to; b += 64 * kWaves * 16)
+                __builtin_nontemporal_store(i32x4{0, 0, 0, 0}, reinterpret_cast<i32x4*>(out + b));
+        }
+    };
+    // half of the workgroups begin with the zeros, so that they are written while the others multiply
+    const bool first = (blockIdx.x >> 3) & 1;
+    if (first) zero();
     LoadMC<kWaves> lp, lq;
     LoadScales ls;   // none
     Steps steps;
     int e, i0, j0;
     auto start = [&](int64_t t, int ln) {
-        e = (int)(t / (kt * nt));
+        const int n = (int)(t / (kt * nt));
+        e = list.at(n);
         int ti, tj;
-        band_order((int)(t - (int64_t)e * kt * nt), nt, kt, &tj, &ti);
+        band_order((int)(t - (int64_t)n * kt * nt), nt, kt, &tj, &ti);
         i0 = ti * kTileP;
         j0 = tj * 256;
         const int lo = a.seg.eoff[e];
@@ -942,9 +1006,8 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad
     // Each workgroup takes every kWeightsGradBlocks-th tile, and starts the next one's loads before it
     // stores.
     int64_t t = xcd_tile(blockIdx.x);
-    if (t >= tiles) return;
-    start(t, lane);
-    for (;;) {
+    if (t < tiles) start(t, lane);
+    while (t < tiles) {
         f32x4 acc[B::PS][B::QS];
         B::run(st, lp, lq, ls, steps, acc, w, lane);
         const int64_t at = ((int64_t)e * a.N + j0) * a.K + i0;
@@ -982,8 +1045,8 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad
         } else {
             B::store(static_cast<uint16_t*>(a.out) + at, a.K, ni, nj, acc, scratch, w, ln);
         }
-        if (t >= tiles) return;
     }
+    if (!first) zero();
 }
 
 // Upper bound on the tiles of a launch: every `bq` rows, and one ragged end for each expert with rows.

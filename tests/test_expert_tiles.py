@@ -344,3 +344,23 @@ def test_largest_features_of_one_row(gpu, fp8):
         ref, mag = X.per_expert(c, x, w), X.per_expert(c, x.abs(), w.abs())
         X.check(c.rows_of(out, RECV)[0], ref, X.sum_bound(ref, mag, K, X.BF16_HALF), "out")
         c.close()
+
+
+@pytest.mark.parametrize("dtype,accumulate", [(torch.bfloat16, False), (torch.float32, False), (torch.bfloat16, True)])
+@pytest.mark.parametrize("E,K,N", [(3, 8, 8), (70, 136, 264), (130, 624, 1000), (1000, 72, 40)])
+def test_weights_gradient_where_most_experts_have_no_rows(gpu, E, K, N, dtype, accumulate):
+    """Runs of experts without rows at the start, between and at the end; matrices of more and less than one run of zeros."""
+    busy = torch.tensor([1, E // 2, E // 2 + 1] if E > 3 else [1])
+    idx = busy.repeat_interleave(torch.tensor([5, 300, 1][:busy.numel()])).reshape(-1, 1)
+    c = X.Case(gpu, T=idx.numel(), k=1, E=E, idx=idx)
+    x, dy = c.randn(c.n, K), c.randn(c.n, N)
+    before = c.randn(E, N, K).to(dtype) if accumulate else torch.full((E, N, K), float("nan"), dtype=dtype)
+    ref, mag = X.outer(c, dy, x, E), X.outer(c, dy.abs(), x.abs(), E)
+    if accumulate:
+        ref, mag = ref + before.double(), mag + before.double().abs()
+    grad = before.cuda()
+    gpu.moe_expert_gemm_backward_weights(c.ctx, c.buffer(RECV, dy, float("nan")), c.buffer(RECV, x, float("nan")), c.handle,
+                                         grad_weights=grad, accumulate=accumulate)
+    half = X.BF16_HALF if dtype is torch.bfloat16 else X.F32_STEP / 2
+    X.check(grad.cpu(), ref, X.sum_bound(ref, mag, 300, half), "grad_weights")
+    c.close()
