@@ -219,15 +219,16 @@ struct LoadKC {
     }
 };
 
-// MC operand: 64 contraction rows of 256 bf16 a stage.  Contraction row c,
-// 32-byte unit u (16 columns) sits at c * 512 + ((u ^ key(c)) << 5).  A
+// MC operand: 64 contraction rows of W bf16 a stage.  Contraction row c,
+// 32-byte unit u (16 columns) sits at c * 2 W + ((u ^ key(c)) << 5).  A
 // transposing load takes, for 16 lanes, four contraction rows of 16 columns;
 // the 32 lanes that read together meet eight different keys.
 __device__ __forceinline__ int mc_key(int c) { return (c & 3) | ((c >> 1) & 4); }
 
-template <int NW>
+template <int NW, int W = 256>
 struct LoadMC {
-    static constexpr int kBytes = kStepC * 512;
+    static constexpr int kRow = W * 2, kLanes = kRow / 16;   // bytes of a stage row, lanes that load it
+    static constexpr int kBytes = kStepC * kRow;
     static constexpr int kInstr = kBytes / 1024 / NW;
     const char* base;
     int ld, crows, before;   // bytes of a contraction row, contraction rows, bytes of a row before the tile
@@ -241,7 +242,7 @@ struct LoadMC {
         lds = w * kInstr * 1024;
 #pragma unroll
         for (int i = 0; i < kInstr; ++i) {
-            const int c = (w * kInstr + i) * 2 + (lane >> 5), p = lane & 31;
+            const int c = (w * kInstr + i) * (64 / kLanes) + lane / kLanes, p = lane % kLanes;
             const int chunk = (((p >> 1) ^ mc_key(c)) << 1) | (p & 1);
             voff[i] = before + chunk * 16 < row_bytes ? (uint32_t)(c * row_bytes) + chunk * 16 : kOob;
         }
@@ -261,9 +262,9 @@ struct LoadMC {
     __device__ __forceinline__ static bf16x8 frag(const char* stage, int sub, int c0, int lane) {
         const int g = lane >> 4, t = lane & 15;
         const int key = (t >> 2) | ((g & 1) << 2);
-        const int at = (c0 + 8 * g + (t >> 2)) * 512 + ((sub ^ key) << 5) + (t & 3) * 8;
+        const int at = (c0 + 8 * g + (t >> 2)) * kRow + ((sub ^ key) << 5) + (t & 3) * 8;
         const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(LDS_PTR(bf16x4, stage + at));
-        const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(LDS_PTR(bf16x4, stage + (at + 4 * 512)));
+        const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(LDS_PTR(bf16x4, stage + (at + 4 * kRow)));
         return bf16x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     }
 };
@@ -916,6 +917,22 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_rows(ExpertG
 }
 
 // ---------------------------------------------------------------- weights gradient
+// Four results at element o of the output, in its type, added to what it holds if asked.
+__device__ __forceinline__ void put(const ExpertGemmArgs& a, int64_t o, f32x4 v) {
+    if (a.out_f32) {
+        f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o);
+        *d = a.accumulate ? *d + v : v;
+        return;
+    }
+    u32x2* d = reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + o);
+    if (a.accumulate) {
+        const u32x2 old = *d;
+        v += f32x4{__uint_as_float(old.x << 16), __uint_as_float(old.x & 0xffff0000u), __uint_as_float(old.y << 16),
+                   __uint_as_float(old.y & 0xffff0000u)};
+    }
+    *d = bf16_pack(v);
+}
+
 // Experts with rows (or without), by number.  A lane knows min(16, ceil(E / 64)) of them.
 struct ExpertList {
     uint32_t mask;   // bit u: the lane's expert u is in the list
@@ -1027,19 +1044,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad
 #pragma unroll
                 for (int p = 0; p < B::PS; ++p) {
                     const int i = wp * B::PS * 16 + 16 * p + 4 * g;
-                    if (j >= nj || i >= ni) continue;
-                    const int64_t o = at + (int64_t)j * a.K + i;
-                    f32x4 v = acc[p][q];
-                    if (a.out_f32) {
-                        f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o);
-                        *d = a.accumulate ? *d + v : v;
-                    } else {
-                        u32x2* d = reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + o);
-                        const u32x2 old = *d;
-                        v += f32x4{__uint_as_float(old.x << 16), __uint_as_float(old.x & 0xffff0000u),
-                                   __uint_as_float(old.y << 16), __uint_as_float(old.y & 0xffff0000u)};
-                        *d = bf16_pack(v);
-                    }
+                    if (j < nj && i < ni) put(a, at + (int64_t)j * a.K + i, acc[p][q]);
                 }
             }
         } else {
@@ -1047,6 +1052,109 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad
         }
     }
     if (!first) zero();
+}
+
+// ---------------------------------------------------------------- gradients of few tiles
+// The gradients in 128 x 128 tiles, two workgroups a compute unit, for the cases that the forward product's
+// narrow tiles are for.  Rows gradient, against 256 columns, us: 4096 x 4096, 1 expert with 512 rows 51 and 87, 4 with
+// 256 55 and 100, 1 with 2048 69 and 101.  Weights gradient: 1 x 4096 rows, 1024 x 1024, 50 and 75; 24 x 580 rows, 168 x
+// 440, 11 and 23; 8 x 300 rows, 1024 x 512, 8.4 and 16.  Up to kNarrowTiles of them, which run together; the rows
+// gradient only where 256 columns leave compute units idle.
+constexpr int kNarrowGrad = 128;
+
+template <bool WEIGHTS>
+__device__ __forceinline__ void grad_narrow(const ExpertGemmArgs& a, const Stage (&st)[2], int w, int lane) {
+    constexpr int T = kNarrowGrad, WP = T / 32, WQ = kWaves / WP, QS = T / 16 / WQ;
+    using LP = LoadMC<kWaves, T>;
+    using LQ = typename std::conditional<WEIGHTS, LP, LoadKC<T, kWaves, true>>::type;
+    static_assert(LP::kBytes == T * kStepBytes && LQ::kBytes == T * kStepBytes, "");
+    const int kt = (a.K + T - 1) / T;
+    LP lp;
+    LQ lq;
+    int steps, i0, ni, nj;
+    int64_t at;   // first output
+    if constexpr (WEIGHTS) {
+        const int nt = (a.N + T - 1) / T, t = xcd_tile4((int)blockIdx.x), e = t / (kt * nt);
+        if (e >= a.seg.E) return;
+        int ti, tj;
+        band_order(t - e * kt * nt, nt, kt, &tj, &ti);
+        i0 = ti * T;
+        const int j0 = tj * T, lo = a.seg.eoff[e];
+        const int rows = seg_rows(a.seg, lo, a.seg.eoff[e + 1]);   // none: the tile is zeroed
+        const int64_t prow = seg_base(a.seg, e, lo, a.p_padded), qrow = seg_base(a.seg, e, lo, a.q_padded);
+        lp.init(static_cast<const char*>(a.p) + (rows ? prow * a.K * 2 : 0), a.K * 2, rows, i0, w, lane);
+        lq.init(static_cast<const char*>(a.q) + (rows ? qrow * a.N * 2 : 0), a.N * 2, rows, j0, w, lane);
+        steps = (rows + kStepC - 1) / kStepC;
+        nj = a.N - j0;
+        at = ((int64_t)e * a.N + j0) * a.K + i0;
+    } else {
+        const Tile tl = find_tile(a.seg, xcd_tile4((int)blockIdx.x), T, kt);
+        if (tl.e < 0) return;
+        i0 = tl.col * T;
+        const int64_t qrow = seg_base(a.seg, tl.e, tl.start, a.q_padded) + tl.row;
+        lp.init(static_cast<const char*>(a.p) + (int64_t)tl.e * a.N * a.K * 2, a.K * 2, a.N, i0, w, lane);
+        lq.init(static_cast<const char*>(a.q) + qrow * a.N * 2, a.N * 2, tl.rows, a.N * 2, w, lane);
+        steps = (a.N + kStepC - 1) / kStepC;
+        nj = tl.rows;
+        at = (seg_base(a.seg, tl.e, tl.start, a.out_padded) + tl.row) * a.K + i0;
+    }
+    ni = a.K - i0;
+    const int g = lane >> 4, t = lane & 15, wp = w % WP, wq = w / WP;
+    f32x4 acc[2][QS];
+#pragma unroll
+    for (int q = 0; q < QS; ++q) acc[0][q] = acc[1][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto fill = [&](const Stage& to, int step) {
+        const auto sp = lp.step_of(step);
+        const auto sq = lq.step_of(step);
+#pragma unroll
+        for (int l = 0; l < LP::kInstr; ++l) lp.issue(to.p, sp, l);
+#pragma unroll
+        for (int l = 0; l < LQ::kInstr; ++l) lq.issue(to.q, sq, l);
+    };
+    auto one = [&](const Stage& cur, const Stage& nxt, int step) {
+        wait_loads<0>();
+        lds_barrier();          // this step has arrived, and everyone is done with the one before
+        fill(nxt, step + 1);    // past the end it reads nothing
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            bf16x8 pf[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) pf[p] = LP::frag(cur.p, wp * 2 + p, h * 32, lane);
+#pragma unroll
+            for (int q = 0; q < QS; ++q) {
+                bf16x8 qf;
+                if constexpr (WEIGHTS) qf = LQ::frag(cur.q, wq * QS + q, h * 32, lane);
+                else qf = LQ::frag(cur.q, (wq * QS + q) * 16 + t, h * 4 + g);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[p], qf, acc[p][q], 0, 0, 0);
+            }
+        }
+    };
+    fill(st[0], 0);
+    int step = 0;
+    for (; step + 1 < steps; step += 2) {
+        one(st[0], st[1], step);
+        one(st[1], st[0], step + 1);
+    }
+    if (step < steps) one(st[0], st[1], step);
+    wait_loads<0>();   // nothing may be on its way into LDS when the workgroup ends
+#pragma unroll
+    for (int q = 0; q < QS; ++q) {
+        const int j = (wq * QS + q) * 16 + t;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int i = wp * 32 + p * 16 + 4 * g;
+            if (j < nj && i < ni) put(a, at + (int64_t)j * a.K + i, acc[p][q]);
+        }
+    }
+}
+
+template <bool WEIGHTS>
+__global__ __launch_bounds__(64 * kWaves, kWaves / 2) void k_expert_grad_narrow(ExpertGemmArgs a) {
+    constexpr int kBytes = kNarrowGrad * kStepBytes;
+    __shared__ __align__(1024) char p0[kBytes], p1[kBytes], q0[kBytes], q1[kBytes];
+    const Stage st[2] = {{p0, q0}, {p1, q1}};
+    grad_narrow<WEIGHTS>(a, st, __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), threadIdx.x & 63);
 }
 
 // Upper bound on the tiles of a launch: every `bq` rows, and one ragged end for each expert with rows.
@@ -1089,19 +1197,29 @@ hipError_t launch_narrow(const ExpertGemmArgs& a, int64_t pairs, hipStream_t s) 
     return hipGetLastError();
 }
 
+template <bool WEIGHTS>
+hipError_t launch_grad_narrow(const ExpertGemmArgs& a, int64_t tiles, hipStream_t s) {
+    k_expert_grad_narrow<WEIGHTS><<<dim3((unsigned)((tiles + 31) / 32 * 32)), dim3(64 * kWaves), 0, s>>>(a);
+    return hipGetLastError();
+}
+
 template <bool FP8, bool PMC>
 hipError_t launch_rows(const ExpertGemmArgs& a, int64_t pairs, hipStream_t s) {
     const int64_t ntiles = ((PMC ? a.K : a.N) + kTileP - 1) / kTileP;
     const int64_t tiles = tile_bound(a, pairs, 256, ntiles);
-    if constexpr (!PMC) {
-        const int64_t active = pairs < a.seg.E ? pairs : a.seg.E, mean = (pairs + active - 1) / active;
-        // tiles of bq rows x cols columns, were the rows spread evenly
-        auto even = [&](int64_t bq, int64_t cols) { return active * ((mean + bq - 1) / bq) * ((a.N + cols - 1) / cols); };
+    const int64_t active = pairs < a.seg.E ? pairs : a.seg.E, mean = (pairs + active - 1) / active;
+    const int64_t idim = PMC ? a.K : a.N;
+    // tiles of bq rows x cols columns, were the rows spread evenly
+    auto even = [&](int64_t bq, int64_t cols) { return active * ((mean + bq - 1) / bq) * ((idim + cols - 1) / cols); };
+    const bool idle = even(128, 128) <= kNarrowTiles && even(256, 256) < kWideTiles;
+    if constexpr (PMC) {
+        constexpr int T = kNarrowGrad;
+        if (idle) return launch_grad_narrow<false>(a, tile_bound(a, pairs, T, (a.K + T - 1) / T), s);
+    } else {
         if (mean <= kFewMean && even(32, 32) <= (FP8 ? kFewFp8 : kFewBf16)) return launch_few<FP8, FP8 ? 2 : 1, 1>(a, pairs, s);
         if (even(32, 32) <= kFewTiles) return launch_few<FP8, 2, 2>(a, pairs, s);
         if (even(64, 64) <= kNarrowTiles) return launch_narrow<FP8, 64, 64, 4, 4>(a, pairs, s);
-        if (even(128, 128) <= kNarrowTiles && even(256, 256) < kWideTiles && (!FP8 || mean > 64))
-            return launch_narrow<FP8, 128, 128, 8, 2>(a, pairs, s);
+        if (idle && (!FP8 || mean > 64)) return launch_narrow<FP8, 128, 128, 8, 2>(a, pairs, s);
     }
     const int64_t blocks = (tiles + 255) / 256 * 256;
     if (!grid_fits(blocks, 64 * kWaves)) return hipErrorInvalidConfiguration;
@@ -1120,6 +1238,9 @@ hipError_t launch_expert_gemm_bwd_rows(const ExpertGemmArgs& a, int64_t pairs, h
 }
 
 hipError_t launch_expert_gemm_bwd_weights(const ExpertGemmArgs& a, hipStream_t s) {
+    constexpr int T = kNarrowGrad;
+    const int64_t tiles = (int64_t)a.seg.E * ((a.K + T - 1) / T) * ((a.N + T - 1) / T);
+    if (tiles <= kNarrowTiles) return launch_grad_narrow<true>(a, tiles, s);
     k_expert_weights_grad<<<dim3(kWeightsGradBlocks), dim3(64 * kWaves), 0, s>>>(a);
     return hipGetLastError();
 }

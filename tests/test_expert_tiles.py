@@ -364,3 +364,37 @@ def test_weights_gradient_where_most_experts_have_no_rows(gpu, E, K, N, dtype, a
     half = X.BF16_HALF if dtype is torch.bfloat16 else X.F32_STEP / 2
     X.check(grad.cpu(), ref, X.sum_bound(ref, mag, 300, half), "grad_weights")
     c.close()
+
+
+@pytest.mark.parametrize("rows_order,out_order", [(RECV, RECV), (RECV, PACKED), (PACKED, RECV), (PACKED, PACKED)])
+def test_padded_windows_with_many_tiles(gpu, rows_order, out_order):
+    """Every product over slot windows where it has too many tiles for the narrow ones."""
+    c = X.Case(gpu, T=70, k=3, E=66, R=2, layout=1, src=1, empty=0.1, max_tokens=72)
+    E, K, N = 66, 1032, 1040
+    orders = dict(rows_order=rows_order, out_order=out_order)
+    w, x, dy = c.randn(E, N, K, scale=K ** -0.5), c.randn(c.n, K), c.randn(c.n, N)
+    wt = w.transpose(1, 2).contiguous()
+    rows, go = c.buffer(rows_order, x, float("nan")), c.buffer(out_order, dy, float("nan"))
+    out = torch.full((c.size[out_order], N), 7.0, dtype=torch.bfloat16, device="cuda")
+    gpu.moe_expert_gemm(c.ctx, rows, w.cuda(), c.handle, out=out, **orders)
+    got, rest = c.rows_of(out, out_order)
+    X.check(got, X.per_expert(c, x, w), X.sum_bound(X.per_expert(c, x, w), X.per_expert(c, x.abs(), w.abs()), K, X.BF16_HALF), "out")
+    assert (rest == 7.0).all()
+    grad = torch.full((c.size[rows_order], K), 7.0, dtype=torch.bfloat16, device="cuda")
+    gpu.moe_expert_gemm_backward_rows(c.ctx, go, w.cuda(), c.handle, grad_rows=grad, **orders)
+    got, rest = c.rows_of(grad, rows_order)
+    X.check(got, X.per_expert(c, dy, wt), X.sum_bound(X.per_expert(c, dy, wt), X.per_expert(c, dy.abs(), wt.abs()), N, X.BF16_HALF),
+            "grad_rows")
+    assert (rest == 7.0).all()
+    gw = gpu.moe_expert_gemm_backward_weights(c.ctx, go, rows, c.handle, **orders)
+    X.check(gw.cpu(), X.outer(c, dy, x, E), X.sum_bound(X.outer(c, dy, x, E), X.outer(c, dy.abs(), x.abs(), E), 70, X.BF16_HALF), "grad_w")
+    K, N = 1024, 2056
+    wq = (c.randn(E, N, K, scale=112.0).float().clamp(-448, 448)).to(torch.float8_e4m3fn).view(torch.uint8)
+    ws = torch.rand(E, -(-N // 128), K // 128, generator=c.gen) * 0.01 + 1e-4
+    xq, xs = X.quantise(c.randn(c.n, K).float())
+    w8, x8 = X.e4m3(wq) * X.expand(ws, N, K), X.e4m3(xq) * xs.double().repeat_interleave(128, 1)
+    out = gpu.moe_expert_gemm_fp8(c.ctx, c.buffer(rows_order, xq, 0x7F), c.buffer(rows_order, xs, float("nan")), wq.cuda(), ws.cuda(),
+                                  c.handle, **orders)
+    X.check(c.rows_of(out, out_order)[0], X.per_expert(c, x8, w8),
+            X.sum_bound(X.per_expert(c, x8, w8), X.per_expert(c, x8.abs(), w8.abs()), K, X.BF16_HALF), "fp8")
+    c.close()
