@@ -6,10 +6,10 @@
 // reads them).  Everything is computed in binary32 and rounded once.
 //
 // Bound by memory: each input is read once and each output written once, 16
-// bytes a lane; one wavefront handles 512 channels of one row.  32,768 rows of 2048
-// channels take 71 us (5.7 TB/s, where a large copy does 4.8), the gradient of
-// 49,152 rows 177 us (5.7 TB/s); 1,024 packed rows as E4M3 take 5 us, a launch's
-// latency.
+// bytes a lane; one wavefront handles 512 channels, of one row or of several.
+// 32,768 rows of 2048 channels take 71 us (5.7 TB/s, where a large copy does 4.8),
+// the gradient of 49,152 rows 176 us (5.7 TB/s); 1,024 packed rows as E4M3 take 5 us,
+// a launch's latency.
 #include "moe_expert.h"
 #include "moe_internal.h"
 
@@ -70,19 +70,32 @@ __device__ __forceinline__ int total_rows(const Segments& s) {
 
 enum Mode { kBf16, kFp8, kBackward };
 
-template <int MODE>
+// FLAT: a wavefront takes 64 consecutive runs of eight channels, also of several rows (every row is where its
+// number says).  Otherwise 512 channels of one row, which is looked up once for the wavefront.
+template <int MODE, bool FLAT>
 __global__ __launch_bounds__(kThreads) void k_swiglu(SwigluArgs a) {
     const int lane = threadIdx.x & 63;
-    const int slices = (a.I + kSlice - 1) / kSlice;
-    const int64_t items = (int64_t)total_rows(a.seg) * slices;
+    const int slices = (a.I + kSlice - 1) / kSlice, runs = a.I / 8;
+    const int rows = total_rows(a.seg);
+    const int64_t items = FLAT ? ((int64_t)rows * runs + 63) / 64 : (int64_t)rows * slices;
     const int64_t step = (int64_t)gridDim.x * (kThreads / 64);
     for (int64_t it = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
          it < items; it += step) {
-        const int r = (int)(it / slices);
-        const int64_t row = row_of(a.seg, r, a.padded);
-        if (row < 0) continue;
-        const int c = (int)(it - (int64_t)r * slices) * kSlice + lane * 8;
-        if (c >= a.I) continue;
+        int64_t row;
+        int c;
+        if constexpr (FLAT) {
+            const int64_t r = it * 64 / runs;
+            const uint32_t run = (uint32_t)(it * 64 - r * runs) + lane, next = run / (uint32_t)runs;
+            row = r + next;
+            c = (int)(run - next * runs) * 8;
+            if (row >= rows) continue;
+        } else {
+            const int r = (int)(it / slices);
+            row = row_of(a.seg, r, a.padded);
+            if (row < 0) continue;
+            c = (int)(it - (int64_t)r * slices) * kSlice + lane * 8;
+            if (c >= a.I) continue;
+        }
         const uint16_t* in = a.gate_up + row * 2 * a.I + c;
         float g[8], u[8], v[8];
         unpack(*reinterpret_cast<const u32x4*>(in), g);
@@ -105,7 +118,7 @@ __global__ __launch_bounds__(kThreads) void k_swiglu(SwigluArgs a) {
             if constexpr (MODE == kBf16) {
                 *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + row * a.I + c) = pack(v);
             } else {
-                // the 16 lanes of a 128-channel block share its maximum; c < I keeps whole blocks together
+                // the 16 lanes of a 128-channel block share its maximum; blocks are whole: I is a multiple of 128
                 float m = 0.0f;
                 bool finite = true;
 #pragma unroll
@@ -132,9 +145,14 @@ __global__ __launch_bounds__(kThreads) void k_swiglu(SwigluArgs a) {
 
 template <int MODE>
 hipError_t launch(const SwigluArgs& a, int64_t pairs, hipStream_t s) {
-    const int64_t items = pairs * ((a.I + kSlice - 1) / kSlice);
+    // Contiguous rows, us, flat and not: 49,152 x 256 forward 16 and 23, backward 22 and 31; 32,768 x 744 27 and 30, 40
+    // and 46; whole slices, 32,768 x 2048 forward 82 and 77, fp8 84 and 79, backward 123 and 125.
+    const bool flat = a.seg.seg_cap == INT32_MAX && (MODE == kBackward || a.I % kSlice != 0);
+    const int64_t items = flat ? (pairs * (a.I / 8) + 63) / 64 : pairs * ((a.I + kSlice - 1) / kSlice);
     const int64_t blocks = (items + kThreads / 64 - 1) / (kThreads / 64);
-    k_swiglu<MODE><<<dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), dim3(kThreads), 0, s>>>(a);
+    const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20));
+    if (flat) k_swiglu<MODE, true><<<grid, dim3(kThreads), 0, s>>>(a);
+    else k_swiglu<MODE, false><<<grid, dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
 }
 

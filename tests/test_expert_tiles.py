@@ -398,3 +398,38 @@ def test_padded_windows_with_many_tiles(gpu, rows_order, out_order):
     X.check(c.rows_of(out, out_order)[0], X.per_expert(c, x8, w8),
             X.sum_bound(X.per_expert(c, x8, w8), X.per_expert(c, x8.abs(), w8.abs()), K, X.BF16_HALF), "fp8")
     c.close()
+
+
+@pytest.mark.parametrize("features", [8, 64, 120, 128, 256, 384, 504, 512, 520, 744, 1408])
+@pytest.mark.parametrize("rows", [1, 7, 64, 1001])
+def test_activation_of_rows_that_share_wavefronts(gpu, rows, features):
+    c = X.Case(gpu, T=rows, k=1, E=3)
+    size = c.size[RECV] + 3   # rows behind the last stay as they were
+    gu, d = c.randn(rows, 2 * features, scale=2.0), c.randn(rows, features)
+    tail = lambda v: torch.cat([c.buffer(RECV, v, 0.0), torch.full((3, v.shape[1]), float("nan"), dtype=v.dtype, device="cuda")])
+    out = torch.full((size, features), 7.0, dtype=torch.bfloat16, device="cuda")
+    gpu.moe_swiglu(c.ctx, tail(gu), c.handle, out=out)
+    ref = X.swiglu64(gu)
+    X.check(out[:rows].cpu(), ref, (X.BF16_HALF + 128 * X.F32_STEP) * ref.abs() + 2.0 ** -120, "act")
+    assert (out[rows:] == 7.0).all()
+    grad = torch.full((size, 2 * features), 7.0, dtype=torch.bfloat16, device="cuda")
+    gpu.moe_swiglu_backward(c.ctx, tail(d), tail(gu), c.handle, grad_gate_up=grad)
+    x = gu.double().requires_grad_()
+    y = torch.nn.functional.silu(x[:, :features]) * x[:, features:]
+    y.backward(d.double())
+    # s (1 + g (1 - s)) cancels near its zero: errors are relative to 1 + |g|
+    scale = torch.cat([(d.double() * x[:, features:]).abs() * (1 + x[:, :features].abs()), x.grad[:, features:].abs()], 1).detach()
+    X.check(grad[:rows].cpu(), x.grad, X.BF16_HALF * x.grad.abs() + 128 * X.F32_STEP * scale + 2.0 ** -120, "grad")
+    assert (grad[rows:] == 7.0).all()
+    if features % 128 == 0:
+        codes = torch.full((size, features), 3, dtype=torch.uint8, device="cuda")
+        scales = torch.full((size, features // 128), 7.0, device="cuda")
+        gpu.moe_swiglu_fp8(c.ctx, tail(gu), c.handle, out=codes, scales=scales)
+        amax = ref.abs().reshape(rows, -1, 128).amax(2).clamp_min(1e-4)
+        X.check(scales[:rows].cpu(), amax / 448, 130 * X.F32_STEP * amax / 448, "scales")
+        v = X.e4m3(codes[:rows].cpu()) * scales[:rows].cpu().double().repeat_interleave(128, 1)
+        # half a step of E4M3, or of its smallest numbers (2^-9), beside the binary32 error
+        step = torch.maximum(ref.abs() * 2.0 ** -4, scales[:rows].cpu().double().repeat_interleave(128, 1) * 2.0 ** -10)
+        X.check(v, ref, step * (1 + 1e-4) + 256 * X.F32_STEP * ref.abs(), "fp8")
+        assert (codes[rows:] == 3).all() and (scales[rows:] == 7.0).all()
+    c.close()
