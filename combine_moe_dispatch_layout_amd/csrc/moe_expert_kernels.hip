@@ -19,6 +19,12 @@
 // past the end gets an address past any descriptor), which is what pads ragged
 // rows and contraction tails.
 //
+// From many tiles to few: k_expert_rows (256 columns x up to 256 rows, one
+// workgroup a compute unit, scheduled by hand) and k_expert_weights_grad (256 x
+// 256, persistent); k_expert_rows_narrow and k_expert_grad_narrow (128 x 128 and
+// 64 x 64, two workgroups a compute unit); k_expert_rows_few (16 or 32 columns x
+// up to 32 rows, one wavefront, no LDS).  launch_rows() chooses.
+//
 // What bounds them (MI355X; a large copy moves 4.76 TB/s, a large library
 // product does 1.39 PFLOP/s NT, 1.21 NN, 1.08 TN in bf16 and 3.05 in plain fp8):
 //   many rows an expert   the matrix cores and the power they may draw: 8192^3
@@ -28,11 +34,15 @@
 //   few rows an expert    reading the matrices: 1 row an expert 6.2 TB/s, 64 rows 5.6, 128
 //                         rows 5.2, 256 rows 4.0 of matrix bytes; what is lost there is the time
 //                         of flight of a stage, so smaller tiles get a third stage
-// Tried and dropped: reading the next steps' lines into L2 ahead (sq 8192 0.90 ms
-// against 0.83: the address unit is busy), raised wave priority around the
-// matrix instructions (1-3% slower), bands of 2, 8 or 16 row tiles (0-3%
-// slower), four wavefronts of 128 x 128 (the compiler moves accumulators
-// about), staggered workgroups in the weights gradient (no change).
+// Tried and dropped: reading the next steps' lines into L2 ahead (each line once
+// 8192^3 0.90 ms against 0.83, shared among the tiles that need it 0.81 against
+// 0.80: loads return in order), 32 x 32 x 16 matrix instructions (1.78 PFLOP/s
+// from registers alone against 2.01), stages of 64 contraction bytes (15.0 TB/s
+// into LDS against 18.4), raised wave priority around the matrix instructions
+// (1-3% slower), bands of 2, 8 or 16 row tiles (0-3% slower), tiles of hot and
+// cold experts in turn (no change), experts' rows in equal tiles (288 rows 4%
+// faster, 416 6% slower), four wavefronts of 128 x 128 (the compiler moves
+// accumulators about), staggered workgroups in the weights gradient (no change).
 #include "moe_ep.h"
 #include "moe_expert.h"
 #include "moe_internal.h"
