@@ -734,7 +734,7 @@ __global__ __launch_bounds__(64, 2) void k_expert_rows_few(ExpertGemmArgs a) {
 
 // ---------------------------------------------------------------- narrow tiles
 // Narrow tiles for products with too few 256-column tiles to occupy the chip: 64 x 64 or 128 x 128, two
-// workgroups a compute unit (64 KB of stages each), so that one computes while the other waits. Steps are not
+// workgroups a compute unit (64 KB of stages each), so that one computes while the other waits.  Steps are not
 // scheduled by hand.  4096 x 4096 bf16, 1 expert: 512 rows 46 us (0.38 PFLOP/s, 64 x 64), 2048 rows
 // 76 us (0.90, 128 x 128); bound by the latency of a step, of which LDS holds one (128 x 128) or three ahead.
 template <bool FP8, int P, int Q, int NW, int STAGES>
@@ -767,7 +767,7 @@ struct NarrowBody {
         }
     };
 
-    __device__ __forceinline__ static void run(char* lds, const LP& lp, const LQ& lq, const Scales& ls, int steps, int rows,
+    __device__ __forceinline__ static void run(char* lds, const LP& lp, const LQ& lq, const Scales& ls, int steps,
                                                f32x4 (&acc)[2][QS], int w, int lane) {
         constexpr int kLoads = LP::kInstr + LQ::kInstr + (FP8 ? 1 : 0);
         const int g = lane >> 4, t = lane & 15, wp = w % WP, wq = w / WP;
@@ -792,39 +792,37 @@ struct NarrowBody {
             fill(step + STAGES - 1, nxt);   // past the end it reads nothing
             const char* sp = lds + cur * kStage;
             const char* sq = sp + P * kStepBytes;
-            if (wq * QS * 16 < rows) {
-                if constexpr (FP8) {
-                    const char* sc = sq + Q * kStepBytes;
-                    i32x8 pf[2];
+            if constexpr (FP8) {
+                const char* sc = sq + Q * kStepBytes;
+                i32x8 pf[2];
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) pf[p] = LP::frag8(sp, wp * 32 + p * 16 + t, g);
+                for (int p = 0; p < 2; ++p) pf[p] = LP::frag8(sp, wp * 32 + p * 16 + t, g);
+#pragma unroll
+                for (int q = 0; q < QS; ++q) {
+                    const int row = (wq * QS + q) * 16 + t;
+                    const i32x8 qf = LQ::frag8(sq, row, g);
+                    const float s =
+                        *reinterpret_cast<const float*>(sc + row * 4) * *reinterpret_cast<const float*>(sc + kRowScales);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            pf[p], qf, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[p][q][r] = __builtin_fmaf(d[r], s, acc[p][q][r]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    bf16x8 pf[2];
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) pf[p] = LP::frag(sp, wp * 32 + p * 16 + t, h * 4 + g);
 #pragma unroll
                     for (int q = 0; q < QS; ++q) {
-                        const int row = (wq * QS + q) * 16 + t;
-                        const i32x8 qf = LQ::frag8(sq, row, g);
-                        const float s =
-                            *reinterpret_cast<const float*>(sc + row * 4) * *reinterpret_cast<const float*>(sc + kRowScales);
+                        const bf16x8 qf = LQ::frag(sq, (wq * QS + q) * 16 + t, h * 4 + g);
 #pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                pf[p], qf, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) acc[p][q][r] = __builtin_fmaf(d[r], s, acc[p][q][r]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        bf16x8 pf[2];
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) pf[p] = LP::frag(sp, wp * 32 + p * 16 + t, h * 4 + g);
-#pragma unroll
-                        for (int q = 0; q < QS; ++q) {
-                            const bf16x8 qf = LQ::frag(sq, (wq * QS + q) * 16 + t, h * 4 + g);
-#pragma unroll
-                            for (int p = 0; p < 2; ++p)
-                                acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[p], qf, acc[p][q], 0, 0, 0);
-                        }
+                        for (int p = 0; p < 2; ++p)
+                            acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[p], qf, acc[p][q], 0, 0, 0);
                     }
                 }
             }
@@ -857,7 +855,7 @@ __global__ __launch_bounds__(64 * NW) void k_expert_rows_narrow(ExpertGemmArgs a
         ls.init(a.q_scales + qrow * kb, tl.rows, a.p_scales + ((int64_t)tl.e * nb + i0 / 128) * kb, kb, w, lane);
     }
     f32x4 acc[2][B::QS];
-    B::run(lds, lp, lq, ls, (int)((ld + kStepBytes - 1) / kStepBytes), tl.rows, acc, w, lane);
+    B::run(lds, lp, lq, ls, (int)((ld + kStepBytes - 1) / kStepBytes), acc, w, lane);
 #pragma unroll
     for (int q = 0; q < B::QS; ++q) {
         const int j = (w / B::WP * B::QS + q) * 16 + (lane & 15);

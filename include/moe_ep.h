@@ -363,7 +363,8 @@ moe_status moe_combine_backward(moe_ctx* ctx, const void* grad_out, const float*
  * For every call: rows that no slot points at are neither read nor written;
  * the buffers of one call may not overlap, but for moe_swiglu_backward's; a handle
  * from another configuration gives MOE_ERR_HANDLE; with no tokens the call
- * returns MOE_OK at once.  All sums are binary32 in a fixed order, rounded once.
+ * returns MOE_OK at once.  All sums are binary32 and rounded once, in an order
+ * that sizes and routing decide: the same call gives the same bits again.
  * NaN and infinities stay in the rows and columns that hold them.  Features
  * are multiples of 8 (E4M3: see there) and at most MOE_MAX_FEATURES, else
  * MOE_ERR_UNSUPPORTED; row buffers and matrices are 16-byte aligned.  The

@@ -433,3 +433,23 @@ def test_activation_of_rows_that_share_wavefronts(gpu, rows, features):
         X.check(v, ref, step * (1 + 1e-4) + 256 * X.F32_STEP * ref.abs(), "fp8")
         assert (codes[rows:] == 3).all() and (scales[rows:] == 7.0).all()
     c.close()
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 4096, 512), (64, 1024, 512), (300, 1024, 1096), (700, 512, 2056), (2000, 256, 8200)])
+def test_the_same_call_gives_the_same_bits(gpu, T, K, N):
+    """From one token to many, every product twice and into another buffer."""
+    c = X.Case(gpu, T=T, k=2, E=8, empty=0.1)
+    w, x, dy = c.randn(8, N, K, scale=K ** -0.5).cuda(), c.randn(T * 2, K).cuda(), c.randn(T * 2, N).cuda()
+    xq, xs = X.quantise(x.float().cpu())
+    wq = torch.randint(0, 120, (8, N, K), dtype=torch.uint8, generator=c.gen).cuda()
+    ws = torch.rand(8, -(-N // 128), K // 128, generator=c.gen).cuda()
+    xq, xs = xq.cuda(), xs.cuda()
+    calls = [lambda: gpu.moe_expert_gemm(c.ctx, x, w, c.handle)[:c.n],
+             lambda: gpu.moe_expert_gemm_fp8(c.ctx, xq, xs, wq, ws, c.handle)[:c.n],
+             lambda: gpu.moe_expert_gemm_backward_rows(c.ctx, dy, w, c.handle)[:c.n],
+             lambda: gpu.moe_expert_gemm_backward_weights(c.ctx, dy, x, c.handle)]
+    for f in calls:
+        first = f().view(torch.int16).clone()
+        for _ in range(3):
+            assert torch.equal(f().view(torch.int16), first)
+    c.close()
