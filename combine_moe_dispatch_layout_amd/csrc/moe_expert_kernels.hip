@@ -733,8 +733,8 @@ __global__ __launch_bounds__(64, 2) void k_expert_rows_few(ExpertGemmArgs a) {
 }
 
 // ---------------------------------------------------------------- narrow tiles
-// Narrow tiles for products with too few 256-column tiles to occupy the chip: 64 x 64 or 128 x 128, two
-// workgroups a compute unit (64 KB of stages each), so that one computes while the other waits.  Steps are not
+// Narrow tiles for products with too few 256-column tiles to occupy the chip: 128 columns x 32 or 128 rows, or 64 x
+// 64; two workgroups a compute unit (64 to 80 KB of stages each), so that one computes while the other waits.  Steps are not
 // scheduled by hand.  4096 x 4096 bf16, 1 expert: 512 rows 46 us (0.38 PFLOP/s, 64 x 64), 2048 rows
 // 76 us (0.90, 128 x 128); bound by the latency of a step, of which LDS holds one (128 x 128) or three ahead.
 template <bool FP8, int P, int Q, int NW, int STAGES>
@@ -767,12 +767,13 @@ struct NarrowBody {
         }
     };
 
-    __device__ __forceinline__ static void run(char* lds, const LP& lp, const LQ& lq, const Scales& ls, int steps,
+    __device__ __forceinline__ static void run(char* lds, const LP& lp, const LQ& lq, const Scales& ls, const Steps& order,
                                                f32x4 (&acc)[2][QS], int w, int lane) {
         constexpr int kLoads = LP::kInstr + LQ::kInstr + (FP8 ? 1 : 0);
         const int g = lane >> 4, t = lane & 15, wp = w % WP, wq = w / WP;
-        auto fill = [&](int step, int slot) {
+        auto fill = [&](int turn, int slot) {
             char* st = lds + slot * kStage;
+            const int step = order.at(turn);   // past the end it reads nothing
             const auto sp = lp.step_of(step);
             const auto sq = lq.step_of(step);
 #pragma unroll
@@ -786,10 +787,10 @@ struct NarrowBody {
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s) fill(s, s);
         int cur = 0, nxt = STAGES - 1;
-        for (int step = 0; step < steps; ++step) {
+        for (int turn = 0; turn < order.n; ++turn) {
             wait_loads<(STAGES - 2) * kLoads>();
             lds_barrier();   // this step has arrived, and everyone is done with the one before
-            fill(step + STAGES - 1, nxt);   // past the end it reads nothing
+            fill(turn + STAGES - 1, nxt);
             const char* sp = lds + cur * kStage;
             const char* sq = sp + P * kStepBytes;
             if constexpr (FP8) {
@@ -855,7 +856,10 @@ __global__ __launch_bounds__(64 * NW) void k_expert_rows_narrow(ExpertGemmArgs a
         ls.init(a.q_scales + qrow * kb, tl.rows, a.p_scales + ((int64_t)tl.e * nb + i0 / 128) * kb, kb, w, lane);
     }
     f32x4 acc[2][B::QS];
-    B::run(lds, lp, lq, ls, (int)((ld + kStepBytes - 1) / kStepBytes), acc, w, lane);
+    // matrices read by one row tile: workgroups of an XCD start at different columns, as in rows_tile()
+    const int n = (int)((ld + kStepBytes - 1) / kStepBytes);
+    const Steps steps = {n, tl.alone ? (int)(blockIdx.x >> 3 & 31) * n / 32 : 0};
+    B::run(lds, lp, lq, ls, steps, acc, w, lane);
 #pragma unroll
     for (int q = 0; q < B::QS; ++q) {
         const int j = (w / B::WP * B::QS + q) * 16 + (lane & 15);
@@ -1174,22 +1178,25 @@ int64_t tile_bound(const ExpertGemmArgs& a, int64_t pairs, int bq, int64_t ni) {
 bool grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_t)1 << 32); }
 
 // Which kernel a forward product runs on, from the numbers of its tiles, were its rows spread evenly over the
-// experts (as many as there are rows, at most): the smallest
-// tiles that still run together.  Cold matrices, us, against the best of the others.
-//   A mean of up to eight rows: one wavefront a tile.
-//     bf16, 16 columns   4096 x 4096, 1 row each, 6 / 8 / 10 / 12 experts: 38 / 57 / 68 / 83 against 52 / 62 / 76 / 78;
-//                        8 rows each, 8 / 10 / 12 experts: 61 / 75 / 91 against 61 / 78 / 80
-//     fp8, 32 columns    2048 x 7168, 1 row each, 6 / 8 / 10 / 12 experts: 20 / 24 / 30 / 35 against 25 / 26 / 44 / 46;
-//                        8 rows each, 6 / 8 experts: 22 / 27 against 25 / 26; 7168 x 4096, 16 x 1 row 87 against 84
-//   Few tiles, any mean, 32 columns: 4096 x 4096 bf16, 2 / 4 / 6 experts of 32 rows 19 / 41 / 62 against 45 / 48 / 53, of
+// experts (as many as there are rows, at most): the smallest tiles that still run together.  Cold matrices, us, against the
+// best of the others.
+//   128 columns x 32 rows, a mean of up to 32 rows, between half of the workgroups that run together and all:
+//     4096 x 4096 bf16, 10 / 12 / 16 experts of 1 row 63 / 72 / 94 against 68 / 78 / 97, 8 of 16 rows 56 against 62, 9 of 32
+//     rows 66 against 76; fp8, 2048 x 7168, 8 x 8 rows 23 against 27.  More only in fp8 and with few rows: 7168 x 4096,
+//     256 x 4 rows 1211 against 1274, popularity falling as rank^-1.2 1322 against 1337 (mean 8), 1661 against 1404 (mean 30);
+//     bf16, 4096 x 4096, 64 x 4 rows 350 against 353, falling popularity (mean 8) 375 against 363.
+//   16 (fp8: 32) columns x 16 rows of one wavefront, a mean of up to 8 rows:
+//     bf16   4096 x 4096, 1 row each, 2 / 6 / 8 / 10 experts: 16 / 37 / 57 / 68 against 44 / 51 / 56 / 63
+//     fp8    2048 x 7168, 1 row each, 6 / 8 / 10 / 12 experts: 20 / 24 / 30 / 35 against 20 / 23 / 39 / 46; 2048 x 2048, 16 x 1
+//            row 15 against 17; 7168 x 4096, 16 x 1 row 87 against 84
+//   32 columns x 32 rows of one wavefront: 4096 x 4096 bf16, 2 / 4 / 6 experts of 32 rows 19 / 41 / 62 against 45 / 48 / 53, of
 //     16 rows 16 / 34 / 54 against 44 / 48 / 52; 1 expert of 64 rows 18 against 42.
-//   64 x 64 tiles that run together (two a compute unit): 4096 x 4096 bf16, 8 experts of 16 rows 62, 128 x 128 69,
-//     256 columns 77; 1 x 512 rows 46 / 57 / 90; beyond, 9 x 64 rows 108 / 82 / 83.
-//   128 x 128 tiles that run together, where 256 columns would leave compute units idle: 4096 x 4096 bf16, 4 x 256 rows
-//     64 against 103, 1 x 2048 rows 76 against 102; with more tiles, 12 x 256 rows 171 against 128; where 256 columns
-//     fill the chip, 16 x 64 rows about 130 against 101.  fp8 with half of a tile's rows idle: 9 x 64 rows 57 against 48.
+//   64 x 64: 4096 x 4096 bf16, 1 x 512 rows 46, 128 x 128 57, 256 columns 90; beyond, 9 x 64 rows 108 / 82 / 83.
+//   128 x 128, where 256 columns would leave compute units idle: 4096 x 4096 bf16, 4 x 256 rows 64 against 103, 1 x 2048
+//     rows 76 against 102; with more tiles, 12 x 256 rows 171 against 128; where 256 columns fill the chip, 16 x 64 rows
+//     about 130 against 101.  fp8 with half of a tile's rows idle: 9 x 64 rows 57 against 48.
 constexpr int kFewMean = 8;
-constexpr int64_t kFewBf16 = 1280, kFewFp8 = 2816, kFewTiles = 640, kNarrowTiles = 512, kWideTiles = 256;
+constexpr int64_t kFew = 1024, kFewFp8 = 2816, kFewTiles = 640, kNarrowTiles = 512, kWideTiles = 256;
 
 template <bool FP8, int PS, int QS>
 hipError_t launch_few(const ExpertGemmArgs& a, int64_t pairs, hipStream_t s) {
@@ -1224,10 +1231,16 @@ hipError_t launch_rows(const ExpertGemmArgs& a, int64_t pairs, hipStream_t s) {
         constexpr int T = kNarrowGrad;
         if (idle) return launch_grad_narrow<false>(a, tile_bound(a, pairs, T, (a.K + T - 1) / T), s);
     } else {
-        if (mean <= kFewMean && even(32, 32) <= (FP8 ? kFewFp8 : kFewBf16)) return launch_few<FP8, FP8 ? 2 : 1, 1>(a, pairs, s);
+        auto narrow32 = [&] { return launch_narrow<FP8, 128, 32, 4, FP8 ? 3 : 4>(a, pairs, s); };
+        const int64_t n32 = even(32, 128);
+        auto few = [&] { return launch_few<FP8, FP8 ? 2 : 1, 1>(a, pairs, s); };
+        if (mean <= kFewMean && even(32, 32) <= kFew) return few();
+        if (mean <= 32 && n32 >= kNarrowTiles / 2 && n32 <= kNarrowTiles) return narrow32();
+        if (FP8 && mean <= kFewMean && even(32, 32) <= kFewFp8) return few();
         if (even(32, 32) <= kFewTiles) return launch_few<FP8, 2, 2>(a, pairs, s);
         if (even(64, 64) <= kNarrowTiles) return launch_narrow<FP8, 64, 64, 4, 4>(a, pairs, s);
         if (idle && (!FP8 || mean > 64)) return launch_narrow<FP8, 128, 128, 8, 2>(a, pairs, s);
+        if (FP8 && mean <= kFewMean) return narrow32();
     }
     const int64_t blocks = (tiles + 255) / 256 * 256;
     if (!grid_fits(blocks, 64 * kWaves)) return hipErrorInvalidConfiguration;

@@ -284,8 +284,8 @@ def test_grids_past_the_launch_limit_are_refused(gpu):
 # Few tiles.  Lengths of a mean of at most 8 (one wavefront a tile of 16 rows), of more (32 rows), and of enough rows
 # and columns for the narrow tiles of a whole workgroup (64 x 64, 128 x 128), each on both sides of its tile sizes.
 FEW = {
-    "mean of 5": ([0, 1, 2, 16, 17, 0, 3, 5, 1, 33, 2, 0, 4, 1, 6, 0], [8, 16, 24, 40, 1000]),
-    "mean of 31": ([0, 1, 15, 16, 17, 31, 32, 33, 64, 100], [8, 24, 40, 72, 1000]),
+    "mean of 5": ([0, 1, 2, 16, 17, 0, 3, 5, 1, 33, 2, 0, 4, 1, 6, 0], [8, 16, 24, 40, 1000, 2056]),
+    "mean of 31": ([0, 1, 15, 16, 17, 31, 32, 33, 64, 100], [8, 24, 40, 72, 1000, 3400]),
     "mean of 65": ([0, 1, 31, 32, 33, 63, 64, 65, 100, 129, 200], [1064, 1096]),
     "mean of 114": ([0, 1, 16, 63, 64, 65, 127, 128, 129, 255, 256, 257], [1608, 2056]),
 }
@@ -452,4 +452,22 @@ def test_the_same_call_gives_the_same_bits(gpu, T, K, N):
         first = f().view(torch.int16).clone()
         for _ in range(3):
             assert torch.equal(f().view(torch.int16), first)
+    c.close()
+
+
+@pytest.mark.parametrize("blocks", [1, 2, 3, 4, 7, 32])
+@pytest.mark.parametrize("padded", [False, True])
+def test_gemm_fp8_of_many_experts_with_few_rows(gpu, padded, blocks):
+    c, E, K, N = X.Case(gpu, T=200, k=4, E=130, R=2, layout=int(padded), src=1, hot=3, max_tokens=200), 130, 128 * blocks, 776
+    wq = (c.randn(E, N, K, scale=112.0).float().clamp(-448, 448)).to(torch.float8_e4m3fn).view(torch.uint8)
+    ws = torch.rand(E, -(-N // 128), blocks, generator=c.gen) * 0.01 + 1e-4
+    xq, xs = X.quantise(c.randn(c.n, K).float())
+    w, x = X.e4m3(wq) * X.expand(ws, N, K), X.e4m3(xq) * xs.double().repeat_interleave(128, 1)
+    ref, mag = X.per_expert(c, x, w), X.per_expert(c, x.abs(), w.abs())
+    out = torch.full((c.size[PACKED], N), 7.0, dtype=torch.bfloat16, device="cuda")
+    gpu.moe_expert_gemm_fp8(c.ctx, c.buffer(RECV, xq, 0x7F), c.buffer(RECV, xs, float("nan")), wq.cuda(), ws.cuda(), c.handle,
+                            out=out, out_order=PACKED)
+    got, rest = c.rows_of(out, PACKED)
+    X.check(got, ref, X.sum_bound(ref, mag, K, X.BF16_HALF), "out")
+    assert (rest == 7.0).all()
     c.close()
