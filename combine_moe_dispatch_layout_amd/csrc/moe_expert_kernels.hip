@@ -21,8 +21,8 @@
 //
 // From many tiles to few: k_expert_rows (256 columns x up to 256 rows, one
 // workgroup a compute unit, scheduled by hand) and k_expert_weights_grad (256 x
-// 256, persistent); k_expert_rows_narrow and k_expert_grad_narrow (128 x 128 and
-// 64 x 64, two workgroups a compute unit); k_expert_rows_few (16 or 32 columns x
+// 256, persistent); k_expert_rows_narrow and k_expert_grad_narrow (128 x 128, 128
+// x 32 and 64 x 64, two workgroups a compute unit); k_expert_rows_few (16 or 32 columns x
 // up to 32 rows, one wavefront, no LDS).  launch_rows() chooses.
 //
 // What bounds them (MI355X; a large copy moves 4.76 TB/s, a large library
