@@ -18,6 +18,9 @@ struct Segments {
     int32_t seg_cap;
     int64_t cap, first;    // padded layout
     uint32_t* err;
+
+    // Offsets of an expert's rows, [lo, hi): they ascend, inside the packed rows.
+    __device__ __forceinline__ bool ascending(int lo, int hi) const { return lo >= 0 && hi >= lo && hi <= max_rows; }
 };
 
 // One product D[j][i] = sum_c P(i, c) Q(j, c) for each expert; i runs along the

@@ -124,7 +124,7 @@ __device__ __forceinline__ int64_t seg_base(const Segments& s, int e, int64_t st
 }
 
 __device__ __forceinline__ int seg_rows(const Segments& s, int lo, int hi) {
-    if (lo < 0 || hi < lo || hi > s.max_rows) {
+    if (!s.ascending(lo, hi)) {
         atomicOr(s.err, kErrBounds);
         return 0;
     }

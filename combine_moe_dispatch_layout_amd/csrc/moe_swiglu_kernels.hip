@@ -59,13 +59,18 @@ __device__ __forceinline__ int64_t row_of(const Segments& s, int r, bool padded)
     return padded ? (int64_t)(run + l) * s.cap + s.first + within : r;
 }
 
+// Rows of all segments; none if the offsets cannot be right.
 __device__ __forceinline__ int total_rows(const Segments& s) {
     const int n = s.eoff[s.E];
-    if (n < 0 || n > s.max_rows) {
-        if (threadIdx.x == 0) atomicOr(s.err, kErrBounds);
-        return 0;
-    }
-    return n;
+    return n >= 0 && n <= s.max_rows ? n : 0;
+}
+
+// Reports offsets that do not ascend.  One workgroup of the launch does it for all: every row is computed alike, so
+// nobody else needs more than the total.
+__device__ __forceinline__ void check_offsets(const Segments& s) {
+    bool right = true;
+    for (int e = threadIdx.x; e < s.E; e += kThreads) right &= s.ascending(s.eoff[e], s.eoff[e + 1]);
+    if (!right) atomicOr(s.err, kErrBounds);
 }
 
 enum Mode { kBf16, kFp8, kBackward };
@@ -74,11 +79,13 @@ enum Mode { kBf16, kFp8, kBackward };
 // number says).  Otherwise 512 channels of one row, which is looked up once for the wavefront.
 template <int MODE, bool FLAT>
 __global__ __launch_bounds__(kThreads) void k_swiglu(SwigluArgs a) {
+    const int workers = gridDim.x - 1;
+    if ((int)blockIdx.x == workers) return check_offsets(a.seg);
     const int lane = threadIdx.x & 63;
     const int slices = (a.I + kSlice - 1) / kSlice, runs = a.I / 8;
     const int rows = total_rows(a.seg);
     const int64_t items = FLAT ? ((int64_t)rows * runs + 63) / 64 : (int64_t)rows * slices;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / 64);
+    const int64_t step = (int64_t)workers * (kThreads / 64);
     for (int64_t it = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
          it < items; it += step) {
         int64_t row;
@@ -150,7 +157,7 @@ hipError_t launch(const SwigluArgs& a, int64_t pairs, hipStream_t s) {
     const bool flat = a.seg.seg_cap == INT32_MAX && (MODE == kBackward || a.I % kSlice != 0);
     const int64_t items = flat ? (pairs * (a.I / 8) + 63) / 64 : pairs * ((a.I + kSlice - 1) / kSlice);
     const int64_t blocks = (items + kThreads / 64 - 1) / (kThreads / 64);
-    const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20));
+    const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20) + 1);   // the last one checks the offsets
     if (flat) k_swiglu<MODE, true><<<grid, dim3(kThreads), 0, s>>>(a);
     else k_swiglu<MODE, false><<<grid, dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();

@@ -1,0 +1,64 @@
+"""Expert offsets that cannot be: what the products and the activation report, and
+which rows they leave alone."""
+import pytest
+import torch
+
+import expert_ref as X
+
+RECV, PACKED = 0, 1
+pytestmark = pytest.mark.gpu
+
+
+def calls(m, c, w, x, gu, d, order):
+    """Every call on the rows, and the outputs that it made."""
+    size, dev = c.size[order], "cuda"
+
+    def new(width, dtype=torch.bfloat16):
+        return torch.full((size, width), 7, dtype=dtype, device=dev)
+    I = gu.shape[1] // 2
+    yield "swiglu", [m.moe_swiglu(c.ctx, gu, c.handle, out=new(I), order=order)]
+    yield "swiglu_fp8", m.moe_swiglu_fp8(c.ctx, gu, c.handle, out=new(I, torch.uint8), scales=new(I // 128, torch.float32), order=order)
+    yield "swiglu_backward", [m.moe_swiglu_backward(c.ctx, d, gu, c.handle, grad_gate_up=new(2 * I), order=order)]
+    yield "gemm", [m.moe_expert_gemm(c.ctx, x, w, c.handle, out=new(w.shape[1]), rows_order=order, out_order=order)]
+    yield "backward_rows", [m.moe_expert_gemm_backward_rows(c.ctx, x, w.transpose(1, 2).contiguous(), c.handle, grad_rows=new(w.shape[1]),
+                                                            rows_order=order, out_order=order)]
+
+
+def setup(m, features=128, **case):
+    c = X.Case(m, **case)
+    order = PACKED
+    w, x = c.randn(c.E, 16, 64).cuda(), c.buffer(order, c.randn(c.n, 64), 0.0)
+    gu, d = c.buffer(order, c.randn(c.n, 2 * features), 0.0), c.buffer(order, c.randn(c.n, features), 0.0)
+    return c, lambda: calls(m, c, w, x, gu, d, order)
+
+
+def offsets(c, values):
+    c.handle.expert_offsets.copy_(torch.tensor(values, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("features", [128, 256, 640])
+@pytest.mark.parametrize("layout", [0, 1])
+def test_offsets_that_descend_are_reported_by_every_call(gpu, layout, features):
+    c, every = setup(gpu, T=20, k=2, E=4, R=2, layout=layout, src=1, features=features)
+    right = c.handle.expert_offsets.clone()
+    for bad in ([0, 5, 3, 20, 40], [-1, 10, 20, 30, 40], [0, 10, 41, 30, 40], [0, 10, 20, 30, 41], [0, 10, 20, 30, -1]):
+        offsets(c, bad)
+        gen = every()
+        for name, outs in gen:
+            assert gpu.moe_poll_error(c.ctx)[0] == gpu.MOE_ERR_DEVICE_BOUNDS, (name, bad)
+            if not 0 <= bad[-1] <= 40 and name.startswith("swiglu"):
+                assert all((o == 7).all() for o in outs), (name, bad)
+    c.handle.expert_offsets.copy_(right)
+    for name, outs in every():
+        assert gpu.moe_poll_error(c.ctx)[0] == gpu.MOE_OK, name
+    c.close()
+
+
+def test_the_last_expert_of_many_is_looked_at(gpu):
+    c, every = setup(gpu, T=20, k=2, E=1024)
+    n = c.handle.expert_offsets.cpu().tolist()
+    for e in (1, 255, 256, 1023):
+        offsets(c, n[:e] + [41] + n[e + 1:])
+        for name, _ in every():
+            assert gpu.moe_poll_error(c.ctx)[0] == gpu.MOE_ERR_DEVICE_BOUNDS, (name, e)
+    c.close()
