@@ -42,7 +42,8 @@ Segments segments(moe_ctx* ctx, const moe_handle* h) {
     Segments s;
     s.eoff = h->expert_offsets;
     s.E = c.num_experts;
-    s.max_rows = (int32_t)((int64_t)c.max_tokens * c.topk);
+    // what the handle's tokens can have, as the grids are sized for (at most the buffers' rows)
+    s.max_rows = (int32_t)((int64_t)h->num_tokens * c.topk);
     // a low-latency window holds max_tokens rows; the dispatch places no more
     s.seg_cap = c.layout == MOE_LAYOUT_PADDED_LL ? c.max_tokens : INT32_MAX;
     s.cap = ctx->g.cap;

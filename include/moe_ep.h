@@ -41,7 +41,7 @@
  *    layout made from other routing (the changed tokens are dropped, see
  *    moe_dispatch), Inf or NaN in an fp8 dispatch or activation (those blocks'
  *    codes and scales are unspecified) and expert offsets of a handle that are
- *    not ascending or pass its rows (the products take those experts to have no
+ *    not ascending or pass num_tokens * topk (the products take those experts to have no
  *    rows; the activation computes the rows before the last offset, none if that
  *    one is out of range).
  *  - bf16 buffers are passed as raw 16-bit storage; fp8 buffers hold OCP

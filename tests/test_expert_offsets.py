@@ -62,3 +62,35 @@ def test_the_last_expert_of_many_is_looked_at(gpu):
         for name, _ in every():
             assert gpu.moe_poll_error(c.ctx)[0] == gpu.MOE_ERR_DEVICE_BOUNDS, (name, e)
     c.close()
+
+
+def test_offsets_past_the_tokens_of_the_handle(gpu):
+    """20 tokens of at most 40 in two slots each: 40 rows, in buffers of 80."""
+    c, every = setup(gpu, T=20, k=2, E=4, max_tokens=40)
+    for bad, kept in (([0, 10, 20, 30, 80], 30), ([0, 10, 20, 30, 41], 30), ([0, 60, 70, 75, 80], 0), ([50, 60, 70, 75, 80], 0)):
+        offsets(c, bad)
+        for name, outs in every():
+            assert gpu.moe_poll_error(c.ctx)[0] == gpu.MOE_ERR_DEVICE_BOUNDS, (name, bad)
+            rows = 0 if name.startswith("swiglu") else kept
+            assert all((o[rows:] == 7).all() for o in outs), (name, bad)
+            assert all((o[:rows] != 7).any() for o in outs) or rows == 0, (name, bad)
+        grad = torch.full((4, 16, 64), 7.0, device="cuda")
+        gpu.moe_expert_gemm_backward_weights(c.ctx, torch.ones(80, 16, dtype=torch.bfloat16, device="cuda"),
+                                             torch.ones(80, 64, dtype=torch.bfloat16, device="cuda"), c.handle, grad_weights=grad)
+        assert gpu.moe_poll_error(c.ctx)[0] == gpu.MOE_ERR_DEVICE_BOUNDS
+        assert (grad[:3] == (10.0 if kept else 0.0)).all() and (grad[3] == 0).all()
+    c.close()
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+def test_a_handle_without_tokens_has_no_rows(gpu, layout):
+    m = gpu
+    ctx = m.Context(m.make_config(4, 128, 3, 1, 2, 0, m.MOE_QUANT_BF16, layout))
+    h = m.Handle(ctx)
+    h.expert_offsets.fill_(5)   # what an earlier call left; a dispatch of no tokens writes zeros
+    bufs, h = m.moe_dispatch(ctx, torch.empty(0, 128, dtype=torch.bfloat16, device="cuda"),
+                             torch.empty(0, 2, dtype=torch.int64, device="cuda"), handle=h)
+    gw = m.moe_expert_gemm_backward_weights(ctx, torch.ones(bufs.recv_rows.shape[0], 16, dtype=torch.bfloat16, device="cuda"),
+                                            bufs.recv_rows, h)
+    assert (gw == 0).all() and m.moe_poll_error(ctx)[0] == m.MOE_OK
+    ctx.close()
