@@ -432,8 +432,10 @@ moe_status moe_expert_gemm_backward_weights(moe_ctx* ctx, const void* grad_out, 
 
 /* The gated activation between two products: for a row of gate and up values
  * side by side (bf16 [rows, 2 * features], gate first),
- * out[r, c] = bf16_rne( g * s * u ), s = 1 / (1 + exp(-g)), computed in binary32.
- * Input and output rows are in the same order. */
+ * out[r, c] = bf16_rne( g * s * u ), s = 1 / (1 + exp(-g)), computed in binary32 (where
+ * exp(-g) passes its range, g below -88.7, s is 0).  Input and output rows are in
+ * the same order.  A gate_up row is one product's output: features is at most
+ * MOE_MAX_FEATURES / 2 in this call and the two below, else MOE_ERR_UNSUPPORTED. */
 moe_status moe_swiglu(moe_ctx* ctx, const void* gate_up, int32_t features, int32_t order,
                       const moe_handle* handle, void* out, void* stream);
 
