@@ -1,5 +1,6 @@
 """How exactly the expert products add.  E4M3 products: rows and matrices whose codes
-spread over the whole format, against the bound that the matrix instruction keeps."""
+spread over the whole format, against the bound that the matrix instruction keeps.
+All of them: exact sums of the longest contractions."""
 import pytest
 import torch
 
@@ -58,8 +59,8 @@ CASES = {
     "32-row tiles": ([1, 3, 0, 8, 1, 2, 1, 1, 5, 1] * 10, 400, 4),
     "64-row tiles": ([31, 33, 64, 65, 100, 129, 200, 0, 1], 1064, 2),
     "128-row tiles": ([64, 65, 127, 128, 129, 255, 256, 257], 1608, 2),
-    "256 columns": ([0, 1, 32, 33, 64, 65, 128, 129, 160, 161, 192, 193, 256, 257] * 8, 264, 4),
-    "256 columns, an odd number of blocks": ([0, 1, 32, 33, 64, 65, 128, 129, 160, 161, 192, 193, 256, 257] * 8, 264, 3),
+    "256 columns": ([0, 1, 32, 33, 64, 65, 128, 129, 160, 161, 192, 193, 256, 257] * 10, 264, 4),
+    "256 columns, an odd number of blocks": ([0, 1, 32, 33, 64, 65, 128, 129, 160, 161, 192, 193, 256, 257] * 10, 264, 3),
 }
 
 
@@ -82,4 +83,138 @@ def test_e4m3_codes_of_every_size(gpu, name):
         lost = (cut(xq[r], wq[e]) * scales).sum(2)
         ref = x @ w.t()
         X.check(out[r], ref, lost * (1 + X.BF16_HALF) + X.sum_bound(ref, x.abs() @ w.abs().t(), K, X.BF16_HALF), "expert %d" % e)
+    c.close()
+
+
+# ---------------------------------------------------------------- long contractions
+# Sums of whole numbers, exact in binary32 in any order, of as many terms as there can be.  A row is +1 and -1; a
+# column of a matrix is zero but for an odd number of channels of each step, +1 or -1 there (three of 64 in bf16, five
+# of 128 in E4M3).  So a step adds an odd number to every result: left out, taken twice or read from another place it
+# shows, for the results are small enough for bf16 to hold nearly all of them exactly.
+def signs(gen, *shape):
+    return torch.randint(0, 2, shape, generator=gen, device=gen.device, dtype=torch.int8) * 2 - 1
+
+
+def odd_steps(gen, E, N, K, step, odd):
+    """[E, N, K] int8, `odd` channels of each `step` (and of what is left of one, at the end)."""
+    w = torch.zeros(E, N, K, dtype=torch.int8, device=gen.device)
+    draw = lambda most, *s: torch.randint(0, most, s, generator=gen, device=gen.device)   # noqa: E731
+    for at, count, wide in ((0, K // step, step), (K // step * step, 1, K % step)):
+        if count == 0 or wide == 0:
+            continue
+        for e in range(E):
+            # one channel in each of `odd` parts of the step, all turned by as many channels
+            where = draw(wide // odd, N, count, odd) + torch.arange(odd, device=gen.device) * (wide // odd)
+            where = (where + draw(wide, N, count, 1)) % wide
+            w[e, :, at:at + count * wide].unflatten(1, (count, wide)).scatter_(2, where, signs(gen, *where.shape))
+    return w
+
+
+@pytest.mark.parametrize("K,step,odd", [(65536, 64, 3), (65528, 64, 3), (16384, 64, 3), (65536, 128, 5), (16384, 128, 5)])
+def test_a_step_left_out_shows(K, step, odd):
+    """The inputs of the tests below: without any one step, or with it twice, not one in a hundred results stays."""
+    g = torch.Generator().manual_seed(K + odd)
+    x, w = signs(g, 3, K), odd_steps(g, 1, 40, K, step, odd)[0]
+    steps = -(-K // step)
+    parts = torch.zeros(3, 40, steps * step, dtype=torch.int32)
+    parts[:, :, :K] = x.int()[:, None] * w.int()[None]
+    parts = parts.unflatten(2, (steps, step)).sum(3)
+    assert (parts % 2 != 0).all()
+    whole = parts.sum(2, keepdim=True)
+    for changed in (whole - parts, whole + parts):
+        assert (changed.float().bfloat16() == whole.float().bfloat16()).float().mean((0, 1)).max() < 0.1
+        assert (changed.float().bfloat16() == whole.float().bfloat16()).float().mean() < 0.01
+
+
+# experts' rows, columns, contraction: one row, a few, 32-, 64- and 128-row tiles, 256 columns of tiles of every size
+LONG = {
+    "a row": ([1, 0, 1], 136, 65536),
+    "a few rows": ([40], 136, 65536),
+    "32-row tiles": ([1] * 60 + [3] * 10, 512, 16384),
+    "64-row tiles": ([33, 64, 65, 100], 2056, 65536),
+    "128-row tiles": ([256, 129, 255], 3400, 65536),
+    "256 columns": ([4, 32, 33, 64, 65, 128, 129, 160, 161, 192, 193, 256, 257] * 10, 264, 16384),
+    "256 columns, longest": ([1, 32, 64, 65, 128, 129, 160, 192, 193, 256], 7168, 65536),
+    "256 columns, odd end": ([1, 32, 64, 65, 128, 129, 160, 192, 193, 256], 7168, 65400),
+}
+
+
+def long_case(gpu, lengths):
+    E = len(lengths)
+    idx = torch.arange(E).repeat_interleave(torch.tensor(lengths)).reshape(-1, 1)
+    c = X.Case(gpu, T=idx.numel(), k=1, E=E, idx=idx)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(17)
+    return c, g
+
+
+def exact_products(c, x, w):
+    """bf16 of x[r] w[e(r)]^T; binary32 products of whole numbers are exact."""
+    out = torch.empty(x.shape[0], w.shape[1], dtype=torch.bfloat16, device=x.device)
+    for e, r in enumerate(c.segments()):
+        if r.numel():
+            out[r.cuda()] = (x[r.cuda()].float() @ w[e].float().t().contiguous()).bfloat16()
+    return out
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", LONG)
+def test_long_sums_bf16(gpu, name):
+    lengths, N, K = LONG[name]
+    c, g = long_case(gpu, lengths)
+    x, w = signs(g, c.n, K).bfloat16(), odd_steps(g, c.E, N, K, 64, 3).bfloat16()
+    out = gpu.moe_expert_gemm(c.ctx, x, w, c.handle)
+    assert torch.equal(out, exact_products(c, x, w))
+    c.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", [n for n in LONG if LONG[n][2] % 128 == 0])
+def test_long_sums_e4m3(gpu, name):
+    """With scales of 1/2 to 2 that are powers of two, so that every sum stays exact."""
+    lengths, N, K = LONG[name]
+    c, g = long_case(gpu, lengths)
+    code = lambda v: v.to(torch.bfloat16).to(torch.float8_e4m3fn).view(torch.uint8)   # noqa: E731
+    power = lambda *s: torch.exp2(torch.randint(-1, 1, s, generator=g, device="cuda").float())   # noqa: E731
+    x, w = signs(g, c.n, K), odd_steps(g, c.E, N, K, 128, 5)
+    xs, ws = power(c.n, K // 128), power(c.E, -(-N // 128), K // 128) * 2
+    out = gpu.moe_expert_gemm_fp8(c.ctx, code(x), xs, code(w), ws, c.handle)
+    for e, r in enumerate(c.segments()):
+        if r.numel():
+            r = r.cuda()
+            v = w[e].float() * ws[e].repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)
+            ref = (x[r].float() * xs[r].repeat_interleave(128, 1)) @ v.t().contiguous()
+            assert torch.equal(out[r], ref.bfloat16()), e
+    c.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", LONG)
+def test_long_sums_of_the_rows_gradient(gpu, name):
+    """The contraction runs over the matrices' rows."""
+    lengths, K, N = LONG[name]
+    c, g = long_case(gpu, lengths)
+    d, wt = signs(g, c.n, N).bfloat16(), odd_steps(g, c.E, K, N, 64, 3).bfloat16()
+    grad = gpu.moe_expert_gemm_backward_rows(c.ctx, d, wt.transpose(1, 2).contiguous(), c.handle)
+    assert torch.equal(grad, exact_products(c, d, wt))
+    c.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lengths,K,N", [([20000, 1, 0, 16411], 264, 136), ([20000, 3, 0, 16411], 2056, 1096)])
+def test_long_sums_of_the_weights_gradient(gpu, lengths, K, N, dtype):
+    """The contraction runs over an expert's rows."""
+    c, g = long_case(gpu, lengths)
+    x = torch.cat([odd_steps(g, 1, K, n, 64, 3)[0].t() if n > 3 else signs(g, n, K) for n in lengths]).bfloat16().contiguous()
+    d = signs(g, c.n, N).bfloat16()
+    for before in (None, signs(g, c.E, N, K).to(dtype)):
+        grad = torch.empty(c.E, N, K, dtype=dtype, device="cuda") if before is None else before.clone()
+        gpu.moe_expert_gemm_backward_weights(c.ctx, d, x, c.handle, grad_weights=grad, accumulate=before is not None)
+        for e, r in enumerate(c.segments()):
+            ref = torch.zeros(N, K, device="cuda") if before is None else before[e].float()
+            if r.numel():
+                r = r.cuda()
+                ref = ref + d[r].float().t().contiguous() @ x[r].float()
+            assert torch.equal(grad[e], ref.to(dtype)), e
     c.close()
