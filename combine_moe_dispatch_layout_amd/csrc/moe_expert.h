@@ -47,7 +47,7 @@ struct SwigluArgs {
     int32_t padded;
 };
 
-// max_tiles: upper bound on the row tiles of one launch (host, from the token count).
+// pairs: tokens times slots, as many rows as the segments can have (host, from the token count).
 hipError_t launch_expert_gemm(const ExpertGemmArgs& a, bool fp8, int64_t pairs, hipStream_t s);
 hipError_t launch_expert_gemm_bwd_rows(const ExpertGemmArgs& a, int64_t pairs, hipStream_t s);
 hipError_t launch_expert_gemm_bwd_weights(const ExpertGemmArgs& a, hipStream_t s);

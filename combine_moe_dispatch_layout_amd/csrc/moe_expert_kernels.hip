@@ -1196,7 +1196,12 @@ bool grid_fits(int64_t blocks, int threads) { return blocks * threads < ((int64_
 //   16 (fp8: 32) columns x 16 rows of one wavefront, a mean of up to 8 rows:
 //     bf16   4096 x 4096, 1 row each, 2 / 6 / 8 / 10 experts: 16 / 37 / 57 / 68 against 44 / 51 / 56 / 63
 //     fp8    2048 x 7168, 1 row each, 6 / 8 / 10 / 12 experts: 20 / 24 / 30 / 35 against 20 / 23 / 39 / 46; 2048 x 2048, 16 x 1
-//            row 15 against 17; 7168 x 4096, 16 x 1 row 87 against 84
+//            row 15 against 17; 7168 x 4096, 16 x 1 row 87 against 84.  fp8 takes them once more, from where 128 columns x 32
+//            rows begin a second round of workgroups (more than 512) to where that has made up for it: 1 row each, 560 / 704 /
+//            760 tiles of 128 x 32, out of cold caches, in columns 2048: rows of 6144 143 / 160 / 172 against 168 / 174 / 176,
+//            4224 116 / 128 / 136 against 132 / 136 / 139, 8192 184 / 207 / 217 against 199 / 207 / 211, 12288 248 / 282 / 305
+//            against 272 / 282 / 286; alike at 1024, 2048, 3968, 5120, 7168, 10240 and 16384 and with 8 rows each.  Rows of
+//            4096 bytes lose by it, 126 / 140 / 146 against 125 / 130 / 131: these tiles all start at one column.
 //   32 columns x 32 rows of one wavefront: 4096 x 4096 bf16, 2 / 4 / 6 experts of 32 rows 19 / 41 / 62 against 45 / 48 / 53, of
 //     16 rows 16 / 34 / 54 against 44 / 48 / 52; 1 expert of 64 rows 18 against 42.
 //   64 x 64: 4096 x 4096 bf16, 1 x 512 rows 46, 128 x 128 57, 256 columns 90; beyond, 9 x 64 rows 108 / 82 / 83.

@@ -57,6 +57,7 @@ CASES = {
     "a row": ([1, 0, 1], 136, 5),
     "a few rows": ([40], 136, 4),
     "32-row tiles": ([1, 3, 0, 8, 1, 2, 1, 1, 5, 1] * 10, 400, 4),
+    "one wavefront a tile, many tiles": ([1, 0, 3, 16, 17, 2, 1, 5, 0, 8] * 14, 520, 4),
     "64-row tiles": ([31, 33, 64, 65, 100, 129, 200, 0, 1], 1064, 2),
     "128-row tiles": ([64, 65, 127, 128, 129, 255, 256, 257], 1608, 2),
     "256 columns": ([0, 1, 32, 33, 64, 65, 128, 129, 160, 161, 192, 193, 256, 257] * 10, 264, 4),
@@ -131,6 +132,7 @@ LONG = {
     "a row": ([1, 0, 1], 136, 65536),
     "a few rows": ([40], 136, 65536),
     "32-row tiles": ([1] * 60 + [3] * 10, 512, 16384),
+    "one wavefront a tile, many tiles": ([1, 0, 3, 16, 17, 2, 1, 5, 0, 8] * 14, 520, 16384),
     "64-row tiles": ([33, 64, 65, 100], 2056, 65536),
     "128-row tiles": ([256, 129, 255], 3400, 65536),
     "256 columns": ([4, 32, 33, 64, 65, 128, 129, 160, 161, 192, 193, 256, 257] * 10, 264, 16384),
