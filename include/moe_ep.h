@@ -362,7 +362,9 @@ moe_status moe_combine_backward(moe_ctx* ctx, const void* grad_out, const float*
  * the second product's input stay packed, and its output goes back to the
  * receive layout.
  *
- * For every call: rows that no slot points at are neither read nor written;
+ * For every call: rows that no slot points at are neither read nor written (but for
+ * those of tokens dropped with MOE_ERR_STALE_LAYOUT: their places stay in the
+ * segments, are computed on as the buffers hold them, and enter the weights gradient);
  * the buffers of one call may not overlap, but for moe_swiglu_backward's; a handle
  * from another configuration gives MOE_ERR_HANDLE; with no tokens the call
  * returns MOE_OK at once.  All sums are binary32 (E4M3: but for the sums of eight

@@ -94,3 +94,32 @@ def test_a_handle_without_tokens_has_no_rows(gpu, layout):
                                             bufs.recv_rows, h)
     assert (gw == 0).all() and m.moe_poll_error(ctx)[0] == m.MOE_OK
     ctx.close()
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+def test_after_a_stale_layout_the_other_tokens_are_right(gpu, layout):
+    """Tokens whose routing changed after the layout are dropped and reported; their places stay in the segments."""
+    m, T, k, E, K, N = gpu, 40, 2, 6, 128, 72
+    g = torch.Generator().manual_seed(4)
+    ctx = m.Context(m.make_config(T, K, E, 1, k, 0, m.MOE_QUANT_BF16, layout))
+    idx = torch.rand(T, E, generator=g).topk(k, dim=1).indices
+    x = torch.randn(T, K, generator=g).bfloat16()
+    w = (torch.randn(E, N, K, generator=g) * K ** -0.5).bfloat16()
+    dev = idx.cuda()
+    m.moe_dispatch_layout(ctx, dev)
+    changed = torch.zeros(T, dtype=torch.bool)
+    changed[3::7] = True
+    dev[changed.cuda(), 0] = (dev[changed.cuda(), 0] + 1) % E
+    bufs = m.DispatchBuffers(ctx)
+    bufs.recv_rows.fill_(float("nan"))
+    bufs, h = m.moe_dispatch(ctx, x.cuda(), dev, bufs=bufs, reuse_layout=True)
+    out = m.moe_expert_gemm(ctx, bufs.recv_rows, w.cuda(), h).cpu()
+    assert m.moe_poll_error(ctx)[0] == m.MOE_ERR_STALE_LAYOUT
+    pos = h.pos.cpu()
+    assert (pos[changed] == -1).all() and (pos[~changed] >= 0).all()
+    for t in torch.nonzero(~changed).flatten().tolist():
+        for j in range(k):
+            e = int(idx[t, j])
+            ref, mag = w[e].double() @ x[t].double(), w[e].double().abs() @ x[t].double().abs()
+            X.check(out[pos[t, j]], ref, X.sum_bound(ref, mag, K, X.BF16_HALF), "token %d" % t)
+    ctx.close()
