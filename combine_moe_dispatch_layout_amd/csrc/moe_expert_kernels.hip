@@ -41,7 +41,8 @@
 //                         gradients (1.45 PFLOP/s), 0.50 ms in fp8 with block scales (2.18)
 //   few rows an expert    reading the matrices: 1 row an expert 6.2 TB/s, 64 rows 5.6, 128
 //                         rows 5.2, 256 rows 4.0 of matrix bytes; what is lost there is the time
-//                         of flight of a stage, so smaller tiles get a third stage
+//                         of flight of a stage, so smaller tiles get a third stage (of which
+//                         most barriers leave one in flight, see lds_barrier())
 // Tried and dropped: reading the next steps' lines into L2 ahead (each line once
 // 8192^3 0.90 ms against 0.83, shared among the tiles that need it 0.81 against
 // 0.80: loads return in order), 32 x 32 x 16 matrix instructions (1.78 PFLOP/s
@@ -349,7 +350,10 @@ __device__ __forceinline__ void wait_loads() {
     __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
 }
 
-// Barrier that orders LDS accesses only: loads into LDS stay in flight across it.
+// Barrier that orders LDS accesses only.  The compiler counts loads into LDS as LDS accesses: where it cannot tell
+// that none in flight belongs to this fence it puts s_waitcnt vmcnt(0) before the barrier, whatever wait_loads() left in
+// flight.  So it is in every loop of the narrow kernels, in two of three steps of the three-stage tiles, and at the
+// first barrier of a tile: right, but with one step in flight where the stages could hold two or three.
 __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
     __builtin_amdgcn_s_barrier();
@@ -369,8 +373,9 @@ struct Stage {
 // fragments are read kAhead groups before they are used, bf16's Q fragments half a step before.  After
 // the group whose reads are the last from the stage, one barrier says that every wavefront is done
 // with it and that the next stage has arrived; the remaining groups issue the loads that refill the
-// freed stage, for STAGES steps on, and read the first fragments of the next.  So nothing is waited
-// for but loads that had STAGES - 1 steps' time to arrive.  Groups are kept in this order (the
+// freed stage, for STAGES steps on, and read the first fragments of the next.  What is waited for are
+// loads that had STAGES - 1 steps' time to arrive, or one step's where lds_barrier() waits for all of
+// them (two of three steps with three stages).  Groups are kept in this order (the
 // scheduler is fenced off between them): with all loads right behind the barrier the wavefronts
 // queue for the address unit while the matrix cores are idle.
 template <int NW, int BQ, int WP, int STAGES, bool FP8, bool PMC, bool QMC>
@@ -506,7 +511,7 @@ struct TileBody {
             for (int q = 0; q < QS; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
         Frag pr[kRing], qc[QS];
         float sc[QS];
-        wait_loads<(STAGES - 1) * kLoads>();
+        wait_loads<(STAGES - 1) * kLoads>();   // the first stage's; lds_barrier() waits for the others' too
         lds_barrier();
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) pr[i] = read_p(st[0], i, w, lane);
@@ -744,7 +749,8 @@ __global__ __launch_bounds__(64, 2) void k_expert_rows_few(ExpertGemmArgs a) {
 // Narrow tiles for products with too few 256-column tiles to occupy the chip: 128 columns x 32 or 128 rows, or 64 x
 // 64; two workgroups a compute unit (64 to 80 KB of stages each), so that one computes while the other waits.  Steps are not
 // scheduled by hand.  4096 x 4096 bf16, 1 expert: 512 rows 46 us (0.38 PFLOP/s, 64 x 64), 2048 rows
-// 76 us (0.90, 128 x 128); bound by the latency of a step, of which LDS holds one (128 x 128) or three ahead.
+// 76 us (0.90, 128 x 128); bound by the latency of a step.  LDS holds one step ahead (128 x 128), two (fp8, 128 x 32) or
+// three, but one is in flight: the barrier of a step waits for all loads (see lds_barrier()).
 template <bool FP8, int P, int Q, int NW, int STAGES>
 struct NarrowBody {
     using LP = LoadKC<P, NW, !FP8>;
@@ -991,7 +997,12 @@ struct ExpertList {
 // Tiles of 256 x 256 over the matrices of experts with rows; those of the others are zeroed as one run of
 // memory (160 experts of 2320 x 624 with 2 rows in all: 463 MB, 90 us, as tiles of zeros 225).  With few rows an
 // expert it is bound by writing the gradients: 64 matrices of 4096 x 4096 take 0.39 ms at 4 rows each (5.5 TB/s
-// written), 0.54 at 128, 1.64 at 768 (1.01 PFLOP/s), 3.6 at 2048 (1.21).
+// written), 0.54 at 128, 1.64 at 768 (1.01 PFLOP/s), 3.6 at 2048 (1.21).  That is bf16, written, of matrices of 256
+// tiles, so that every workgroup gets one tile of each expert.  Other matrices share out less evenly: 49,152 rows over 64
+// experts with popularity falling as rank^-1.2, 1536 x 2048, 0.40 ms, 0.33 with equal popularity; 128 experts 0.50 and 0.44;
+// 2816 x 2048 0.62 and 0.59.  Other results cost more, for put() loads, adds and stores 32 times one after the other,
+// behind the next tile's loads: skewed 4096 x 4096 1.78 ms, fp32 2.18, added to bf16 2.57, added to fp32 2.94; at 128 rows
+// each 0.66, 1.21, 1.64 and 2.01.
 constexpr int kWeightsGradBlocks = 256;
 constexpr int kZeroChunk = 64 * 1024;   // bytes of zeros a workgroup writes in turn
 
@@ -1041,7 +1052,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_expert_weights_grad
         B::begin(st, lp, lq, ls, steps);
     };
     // Each workgroup takes every kWeightsGradBlocks-th tile, and starts the next one's loads before it
-    // stores.
+    // stores (the next tile's first barrier waits for those loads and for the stores).
     int64_t t = xcd_tile(blockIdx.x);
     if (t < tiles) start(t, lane);
     while (t < tiles) {
