@@ -372,7 +372,9 @@ moe_status moe_combine_backward(moe_ctx* ctx, const void* grad_out, const float*
  * decide: the same call gives the same bits again.
  * NaN and infinities stay in the rows and columns that hold them.  Features
  * are multiples of 8 (E4M3: see there) and at most MOE_MAX_FEATURES, else
- * MOE_ERR_UNSUPPORTED; row buffers and matrices are 16-byte aligned.  The
+ * MOE_ERR_UNSUPPORTED, as is a product or rows gradient of more tiles of 256 x 256
+ * than a launch holds ((num_tokens * topk / 256 + E) * ceil(columns / 256), rounded
+ * up to 256s, of 2^23 or more); row buffers and matrices are 16-byte aligned.  The
  * workgroup cap (moe_ctx_set_max_workgroups) leaves compute units to these
  * products and does not apply to them. */
 typedef enum moe_rows_order {
