@@ -5,7 +5,7 @@ import torch
 
 import expert_ref as X
 
-RECV, PACKED = 0, 1
+PACKED = 1
 pytestmark = pytest.mark.gpu
 
 
@@ -24,7 +24,7 @@ def calls(m, c, w, x, gu, d, order):
                                                             rows_order=order, out_order=order)]
 
 
-def setup(m, features=128, **case):
+def rows_and_calls(m, features=128, **case):
     c = X.Case(m, **case)
     order = PACKED
     w, x = c.randn(c.E, 16, 64).cuda(), c.buffer(order, c.randn(c.n, 64), 0.0)
@@ -39,7 +39,7 @@ def offsets(c, values):
 @pytest.mark.parametrize("features", [128, 256, 640])
 @pytest.mark.parametrize("layout", [0, 1])
 def test_offsets_that_descend_are_reported_by_every_call(gpu, layout, features):
-    c, every = setup(gpu, T=20, k=2, E=4, R=2, layout=layout, src=1, features=features)
+    c, every = rows_and_calls(gpu, T=20, k=2, E=4, R=2, layout=layout, src=1, features=features)
     right = c.handle.expert_offsets.clone()
     for bad in ([0, 5, 3, 20, 40], [-1, 10, 20, 30, 40], [0, 10, 41, 30, 40], [0, 10, 20, 30, 41], [0, 10, 20, 30, -1]):
         offsets(c, bad)
@@ -55,7 +55,7 @@ def test_offsets_that_descend_are_reported_by_every_call(gpu, layout, features):
 
 
 def test_the_last_expert_of_many_is_looked_at(gpu):
-    c, every = setup(gpu, T=20, k=2, E=1024)
+    c, every = rows_and_calls(gpu, T=20, k=2, E=1024)
     n = c.handle.expert_offsets.cpu().tolist()
     for e in (1, 255, 256, 1023):
         offsets(c, n[:e] + [41] + n[e + 1:])
@@ -66,7 +66,7 @@ def test_the_last_expert_of_many_is_looked_at(gpu):
 
 def test_offsets_past_the_tokens_of_the_handle(gpu):
     """20 tokens of at most 40 in two slots each: 40 rows, in buffers of 80."""
-    c, every = setup(gpu, T=20, k=2, E=4, max_tokens=40)
+    c, every = rows_and_calls(gpu, T=20, k=2, E=4, max_tokens=40)
     for bad, kept in (([0, 10, 20, 30, 80], 30), ([0, 10, 20, 30, 41], 30), ([0, 60, 70, 75, 80], 0), ([50, 60, 70, 75, 80], 0)):
         offsets(c, bad)
         for name, outs in every():
