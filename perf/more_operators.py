@@ -364,7 +364,7 @@ def _plain_route(s):
     if c["norm"]:
         total = chosen.sum(1, keepdim=True)
         total = torch.where(total > 0, total, 1)
-        d = (d - (d * chosen).sum(1, keepdim=True) / total) / total
+        d = (d - (d * (chosen / total)).sum(1, keepdim=True)) / total   # of one expert alone nothing is left
     ds = torch.zeros_like(score).scatter_add_(1, at, torch.where(there, d, 0))
     if c["score"] == "sigmoid":
         grad = ds * score * (1 - score)
@@ -436,11 +436,12 @@ def exact(c, seed):
             order = torch.where(keep.repeat_interleave(E // G, 1), order, -math.inf)
         best = order.topk(k, 1)
         there = best.values > -math.inf
-        chosen = torch.where(there, p.gather(1, best.indices), 0.0)
-        w = chosen * c["scale"]
-        if c["norm"]:
-            total = chosen.sum(1, keepdim=True)
-            w = w / torch.where(total > 0, total, 1.0)
+        if c["norm"]:   # shares of a sum are a softmax of the logarithms
+            log = v if c["score"] == "softmax" else -torch.nn.functional.softplus(-v)
+            log = torch.where(there, log.gather(1, best.indices), -math.inf)
+            w = torch.where(there, torch.softmax(torch.where(there.any(1, keepdim=True), log, 0.0), 1), 0.0) * c["scale"]
+        else:
+            w = torch.where(there, p.gather(1, best.indices), 0.0) * c["scale"]
         if not c["train"]:
             return None, w.detach()
         if c["bf16"]:
