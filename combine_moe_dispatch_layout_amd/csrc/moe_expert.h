@@ -12,13 +12,14 @@ namespace moe {
 // seg_cap of them placed; they start at row eoff[e] of a packed buffer and at
 // row e * cap + first of a padded one.
 struct Segments {
-    const int32_t* eoff;   // [E+1], the handle's expert offsets
+    const int32_t* eoff;   // [E+1], the handle's expert offsets; NULL for one matrix (E = 1) with max_rows rows
     int32_t E;
     int32_t max_rows;      // eoff[E] may not exceed it
     int32_t seg_cap;
     int64_t cap, first;    // padded layout
     uint32_t* err;
 
+    __device__ __forceinline__ int offset(int e) const { return eoff != nullptr ? eoff[e] : e != 0 ? max_rows : 0; }
     // Offsets of an expert's rows, [lo, hi): they ascend, inside the packed rows.
     __device__ __forceinline__ bool ascending(int lo, int hi) const { return lo >= 0 && hi >= lo && hi <= max_rows; }
 };
