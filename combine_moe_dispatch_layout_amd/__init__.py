@@ -1,4 +1,5 @@
-"""MI355X-native MoE token dispatch-layout / dispatch / combine, and the experts' products in between.
+"""MI355X-native MoE token dispatch-layout / dispatch / combine, the experts' products in between, and the
+router, dense product and few-token layer around them.
 
 The work happens in libmoe_ep.so (hand-written HIP for gfx950, C ABI in
 include/moe_ep.h); this package is its thin Python binding.  PyTorch is used
@@ -21,4 +22,8 @@ from ._binding import (  # noqa: F401
     MOE_QUANT_FP8_E4M3, load_library, make_config, moe_combine, moe_combine_backward, moe_dispatch,
     moe_dispatch_backward, moe_dispatch_layout, moe_dispatch_noalloc, moe_expert_gemm, moe_expert_gemm_backward_rows,
     moe_expert_gemm_backward_weights, moe_expert_gemm_fp8, moe_poll_error, moe_size_hint, moe_swiglu,
-    moe_swiglu_backward, moe_swiglu_fp8, prepare_combine, prepare_dispatch, status_str)
+    moe_swiglu_backward, moe_swiglu_fp8, prepare_combine, prepare_dispatch, status_str,
+    MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_SWIGLU, MOE_KERNEL_LAYER,
+    MOE_KERNEL_LINEAR, MOE_KERNEL_LINEAR_BWD, MOE_KERNEL_ROUTE, MOE_KERNEL_ROUTE_BWD, MOE_LAYER_MAX_ROWS, MOE_LOGIT_BF16,
+    MOE_LOGIT_F32, MOE_MAX_GROUPS, MOE_OUT_BF16, MOE_OUT_F32, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, moe_layer, moe_layer_fp8,
+    moe_linear, moe_linear_backward, moe_linear_backward_workspace, moe_route, moe_route_backward)

@@ -42,14 +42,23 @@ MOE_LAYOUT_PADDED_LL = 1
 
 (MOE_KERNEL_LAYOUT, MOE_KERNEL_DISPATCH, MOE_KERNEL_COMBINE, MOE_KERNEL_DISPATCH_BWD,
  MOE_KERNEL_COMBINE_BWD, MOE_KERNEL_EXPERT_GEMM, MOE_KERNEL_EXPERT_BWD_ROWS, MOE_KERNEL_EXPERT_BWD_WEIGHTS,
- MOE_KERNEL_SWIGLU, MOE_KERNEL_SWIGLU_BWD) = range(10)
+ MOE_KERNEL_SWIGLU, MOE_KERNEL_SWIGLU_BWD, MOE_KERNEL_ROUTE, MOE_KERNEL_ROUTE_BWD, MOE_KERNEL_LINEAR,
+ MOE_KERNEL_LINEAR_BWD, MOE_KERNEL_LAYER) = range(15)
 KERNEL_NAMES = ("layout", "dispatch", "combine", "dispatch_bwd", "combine_bwd", "expert_gemm", "expert_bwd_rows",
-                "expert_bwd_weights", "swiglu", "swiglu_bwd")
+                "expert_bwd_weights", "swiglu", "swiglu_bwd", "route", "route_bwd", "linear", "linear_bwd", "layer")
 
 # order of a row buffer of the expert products and the activation
 MOE_ROWS_RECV, MOE_ROWS_PACKED = 0, 1
 MOE_GRAD_BF16, MOE_GRAD_F32 = 0, 1
 MOE_MAX_FEATURES = 65536
+
+# the router, the dense product, the layer of a few tokens
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_LOGIT_F32, MOE_LOGIT_BF16 = 0, 1
+MOE_MAX_GROUPS = 64
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_SWIGLU = range(6)
+MOE_OUT_BF16, MOE_OUT_F32 = 0, 1
+MOE_LAYER_MAX_ROWS = 1024
 
 
 class MoeError(RuntimeError):
@@ -78,6 +87,11 @@ class moe_handle(ctypes.Structure):
                 ("num_tokens", ctypes.c_int32), ("tag", ctypes.c_uint32)]
 
 
+class moe_router(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("normalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 # the full list of symbols include/moe_ep.h declares
 EXPORTS = ("moe_status_str", "moe_size_hint", "moe_ctx_create", "moe_ctx_destroy", "moe_ctx_config",
            "moe_ctx_tune", "moe_dispatch_layout", "moe_dispatch", "moe_combine", "moe_dispatch_backward",
@@ -86,7 +100,8 @@ EXPORTS = ("moe_status_str", "moe_size_hint", "moe_ctx_create", "moe_ctx_destroy
            "moe_timing_launches", "moe_dispatch_noalloc",
            "moe_dispatch_layout_prefetch", "moe_expert_gemm", "moe_expert_gemm_fp8",
            "moe_expert_gemm_backward_rows", "moe_expert_gemm_backward_weights", "moe_swiglu", "moe_swiglu_fp8",
-           "moe_swiglu_backward")
+           "moe_swiglu_backward", "moe_route", "moe_route_backward", "moe_linear", "moe_linear_backward",
+           "moe_linear_backward_workspace", "moe_layer", "moe_layer_fp8")
 
 _lib = None
 
@@ -136,6 +151,13 @@ def load_library(path=LIB_PATH):
         "moe_swiglu": [vp, vp, i32, i32, ctypes.POINTER(moe_handle), vp, vp],
         "moe_swiglu_fp8": [vp, vp, i32, i32, ctypes.POINTER(moe_handle), vp, vp, vp],
         "moe_swiglu_backward": [vp, vp, vp, i32, i32, ctypes.POINTER(moe_handle), vp, vp],
+        "moe_route": [vp, vp, i32, ctypes.c_int64, i32, ctypes.POINTER(moe_router), vp, vp, vp, vp],
+        "moe_route_backward": [vp, vp, vp, i32, ctypes.c_int64, vp, i32, ctypes.POINTER(moe_router), vp, vp],
+        "moe_linear": [vp, vp, i32, vp, i32, i32, vp, i32, vp, vp, i32, vp, vp],
+        "moe_linear_backward": [vp, vp, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp, i32, i32, vp, vp, vp],
+        "moe_linear_backward_workspace": [i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
+        "moe_layer": [vp, vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, vp],
+        "moe_layer_fp8": [vp, vp, vp, vp, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp],
     }
     for name, args in sigs.items():
         f = getattr(lib, name)
@@ -682,8 +704,197 @@ def moe_swiglu_backward(ctx, grad_out, gate_up, handle, grad_gate_up=None, order
         grad_gate_up = _expert_out(ctx, 2 * features, torch.bfloat16, order)
     po = _expert_rows(ctx, grad_gate_up, torch.bfloat16, 2 * features, order, "grad_gate_up")
     _check(load_library().moe_swiglu_backward(ctx.handle, pd, pg, features, order, ctypes.byref(handle.c), po, _stream()),
-           "moe_swiglu_backward")
+           "moe_swiglu_backward", "moe_route", "moe_route_backward", "moe_linear", "moe_linear_backward",
+           "moe_linear_backward_workspace", "moe_layer", "moe_layer_fp8")
     return grad_gate_up
+
+
+# ---------------------------------------------------------------- around the experts
+def _arg(ctx, t, dtype, shape, name):
+    """Pointer of a contiguous tensor of this dtype and shape on the context's device."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == ctx.device:
+        return t.data_ptr()
+    if not (t.is_cuda and t.dtype is dtype and t.is_contiguous()):
+        raise TypeError("%s must be a contiguous %s CUDA tensor" % (name, dtype))
+    if t.get_device() != ctx.device:
+        raise ValueError("%s is on %s, the context on cuda:%d" % (name, t.device, ctx.device))
+    raise ValueError("%s must be %s, is %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _empty(ctx, shape, dtype):
+    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", ctx.device))
+
+
+def _workspace(ctx, t, nbytes):
+    """Pointer of at least nbytes bytes (the tensor that a call made for itself may go when it returns: its memory is
+    used again in the order of the stream), and the tensor."""
+    if nbytes == 0:
+        return None, None
+    if t is None:
+        t = _empty(ctx, nbytes, torch.uint8)
+    elif not (t.is_cuda and t.is_contiguous() and t.get_device() == ctx.device):
+        raise TypeError("workspace must be a contiguous CUDA tensor on cuda:%d" % ctx.device)
+    elif t.numel() * t.element_size() < nbytes:
+        raise ValueError("workspace holds %d bytes, needs %d" % (t.numel() * t.element_size(), nbytes))
+    return t.data_ptr(), t
+
+
+def _logits(ctx, t):
+    """Pointer, type and row stride of a router's logits [T, E]."""
+    kind = {torch.float32: MOE_LOGIT_F32, torch.bfloat16: MOE_LOGIT_BF16}.get(t.dtype)
+    if kind is None or not t.is_cuda:
+        raise TypeError("logits must be a float32 or bfloat16 CUDA tensor")
+    if t.get_device() != ctx.device:
+        raise ValueError("logits is on %s, the context on cuda:%d" % (t.device, ctx.device))
+    E = ctx.cfg.num_experts
+    if t.dim() != 2 or t.shape[1] != E or (E > 1 and t.stride(1) != 1):
+        raise ValueError("logits must be [T, %d], its rows contiguous" % E)
+    stride = t.stride(0) if t.shape[0] > 1 else E
+    if stride < E:
+        raise ValueError("rows of logits overlap")
+    return t.data_ptr(), kind, stride
+
+
+def moe_route(ctx, logits, score=MOE_SCORE_SOFTMAX, bias=None, groups=1, topk_groups=1, group_top=1, normalize=True, scale=1.0,
+              topk_idx=None, topk_weights=None):
+    """The k experts of each token and their weights, from logits fp32 or bf16 [T, E] (any row stride): returns
+    (topk_idx int64 [T, k], topk_weights fp32 [T, k]).  bias (fp32 [E]) is added to the scores for the choice alone; of
+    `groups` groups of neighbouring experts the topk_groups with the largest sums of their group_top best scores stay."""
+    p, kind, stride = _logits(ctx, logits)
+    T, k = logits.shape[0], ctx.cfg.topk
+    pb = _arg(ctx, bias, torch.float32, (ctx.cfg.num_experts,), "bias") if bias is not None else None
+    if topk_idx is None:
+        topk_idx = _empty(ctx, (T, k), torch.int64)
+    if topk_weights is None:
+        topk_weights = _empty(ctx, (T, k), torch.float32)
+    router = moe_router(score, groups, topk_groups, group_top, int(bool(normalize)), scale)
+    _check(load_library().moe_route(ctx.handle, p, kind, stride, T, ctypes.byref(router), pb,
+                                    _arg(ctx, topk_idx, torch.int64, (T, k), "topk_idx"),
+                                    _arg(ctx, topk_weights, torch.float32, (T, k), "topk_weights"), _stream()), "moe_route")
+    return topk_idx, topk_weights
+
+
+def moe_route_backward(ctx, grad_weights, logits, topk_idx, score=MOE_SCORE_SOFTMAX, normalize=True, scale=1.0, grad_logits=None):
+    """Gradient of moe_route's weights for the logits: fp32 [T, E].  score, normalize and scale as they were there."""
+    p, kind, stride = _logits(ctx, logits)
+    T, E, k = logits.shape[0], ctx.cfg.num_experts, ctx.cfg.topk
+    if grad_logits is None:
+        grad_logits = _empty(ctx, (T, E), torch.float32)
+    router = moe_router(score, 1, 1, 1, int(bool(normalize)), scale)
+    _check(load_library().moe_route_backward(ctx.handle, _arg(ctx, grad_weights, torch.float32, (T, k), "grad_weights"), p, kind,
+                                             stride, _arg(ctx, topk_idx, torch.int64, (T, k), "topk_idx"), T, ctypes.byref(router),
+                                             _arg(ctx, grad_logits, torch.float32, (T, E), "grad_logits"), _stream()),
+           "moe_route_backward")
+    return grad_logits
+
+
+_OUT_TYPES = {torch.bfloat16: MOE_OUT_BF16, torch.float32: MOE_OUT_F32}
+
+
+def _linear_sizes(x, weights, act):
+    """Rows, in_features, features and the matrix's rows."""
+    if x.dim() != 2 or weights.dim() != 2:
+        raise ValueError("x must be [T, in_features] and weights [M, in_features]")
+    M, K = weights.shape
+    if act == MOE_ACT_SWIGLU and M % 2:
+        raise ValueError("weights of a gated product have 2 * features rows")
+    return x.shape[0], K, M // 2 if act == MOE_ACT_SWIGLU else M, M
+
+
+def moe_linear(ctx, x, weights, bias=None, act=MOE_ACT_NONE, residual=None, out=None, out_dtype=torch.bfloat16, pre=None):
+    """act(x weights^T + bias) + residual: x bf16 [T, K], weights bf16 [M, K], bias bf16 [M], residual bf16 [T, F] ->
+    [T, F], bf16 or fp32 (out's dtype, or out_dtype), F = M, or M / 2 for MOE_ACT_SWIGLU.  pre: bf16 [T, M], receives
+    what moe_linear_backward needs."""
+    T, K, F, M = _linear_sizes(x, weights, act)
+    if out is None:
+        out = _empty(ctx, (T, F), out_dtype)
+    kind = _OUT_TYPES.get(out.dtype)
+    if kind is None:
+        raise TypeError("out must be bfloat16 or float32")
+    bf16 = torch.bfloat16
+    _check(load_library().moe_linear(
+        ctx.handle, _arg(ctx, x, bf16, (T, K), "x"), T, _arg(ctx, weights, bf16, (M, K), "weights"), K, F,
+        _arg(ctx, bias, bf16, (M,), "bias") if bias is not None else None, act,
+        _arg(ctx, residual, bf16, (T, F), "residual") if residual is not None else None, _arg(ctx, out, out.dtype, (T, F), "out"),
+        kind, _arg(ctx, pre, bf16, (T, M), "pre") if pre is not None else None, _stream()), "moe_linear")
+    return out
+
+
+def moe_linear_backward_workspace(T, features, act=MOE_ACT_NONE, out_dtype=torch.bfloat16, bias=False):
+    """Bytes that moe_linear_backward works in."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_linear_backward_workspace(T, features, act, _OUT_TYPES[out_dtype], int(bool(bias)), ctypes.byref(n)),
+           "moe_linear_backward_workspace")
+    return n.value
+
+
+def moe_linear_backward(ctx, grad_out, x, weights, act=MOE_ACT_NONE, pre=None, bias=False, need_x=True, need_weights=True,
+                        grad_x=None, grad_weights=None, grad_bias=None, accumulate=False, workspace=None):
+    """Gradients of moe_linear: returns (grad_x bf16 [T, K], grad_weights [M, K] bf16 or fp32 as given, grad_bias fp32
+    [M]).  grad_out: bf16 or fp32 [T, F]; pre: as moe_linear left it.  grad_bias is None unless bias is true or it is
+    given; need_x and need_weights leave out the others.  accumulate: add to grad_weights and grad_bias."""
+    T, K, F, M = _linear_sizes(x, weights, act)
+    kind = _OUT_TYPES.get(grad_out.dtype)
+    if kind is None:
+        raise TypeError("grad_out must be bfloat16 or float32")
+    if accumulate and ((need_weights and grad_weights is None) or (bias and grad_bias is None)):
+        raise ValueError("accumulate needs grad_weights and grad_bias")
+    bf16, f32 = torch.bfloat16, torch.float32
+    if grad_x is None and need_x:
+        grad_x = _empty(ctx, (T, K), bf16)
+    if grad_weights is None and need_weights:
+        grad_weights = _empty(ctx, (M, K), bf16)
+    if grad_bias is None and bias:
+        grad_bias = _empty(ctx, (M,), f32)
+    if grad_weights is not None and grad_weights.dtype is not bf16 and grad_weights.dtype is not f32:
+        raise TypeError("grad_weights must be bfloat16 or float32")
+    pw, workspace = _workspace(ctx, workspace, moe_linear_backward_workspace(T, F, act, grad_out.dtype, grad_bias is not None))
+    _check(load_library().moe_linear_backward(
+        ctx.handle, _arg(ctx, grad_out, grad_out.dtype, (T, F), "grad_out"), kind, T, _arg(ctx, x, bf16, (T, K), "x"),
+        _arg(ctx, weights, bf16, (M, K), "weights"), K, F, act,
+        _arg(ctx, pre, bf16, (T, M), "pre") if pre is not None else None,
+        _arg(ctx, grad_x, bf16, (T, K), "grad_x") if grad_x is not None else None,
+        _arg(ctx, grad_weights, grad_weights.dtype, (M, K), "grad_weights") if grad_weights is not None else None,
+        MOE_GRAD_F32 if grad_weights is not None and grad_weights.dtype is f32 else MOE_GRAD_BF16, int(bool(accumulate)),
+        _arg(ctx, grad_bias, f32, (M,), "grad_bias") if grad_bias is not None else None, pw, _stream()), "moe_linear_backward")
+    return grad_x, grad_weights, grad_bias
+
+
+def _layer_args(ctx, x, topk_idx, topk_weights, w1, w2, dtype, residual, out, workspace):
+    c = ctx.cfg
+    if x.dim() != 2 or w2.dim() != 3:
+        raise ValueError("x must be [T, %d] and w2 [%d, %d, features]" % (c.hidden, c.num_experts, c.hidden))
+    T, E, H, k, I = x.shape[0], c.num_experts, c.hidden, c.topk, w2.shape[2]
+    bf16 = torch.bfloat16
+    if out is None:
+        out = _empty(ctx, (T, H), bf16)
+    ps, workspace = _workspace(ctx, workspace, T * k * I * 2)
+    return (T, I, out, workspace, _arg(ctx, x, bf16, (T, H), "x"), _arg(ctx, topk_idx, torch.int64, (T, k), "topk_idx"),
+            _arg(ctx, topk_weights, torch.float32, (T, k), "topk_weights"), _arg(ctx, w1, dtype, (E, 2 * I, H), "w1"),
+            _arg(ctx, w2, dtype, (E, H, I), "w2"), _arg(ctx, residual, bf16, (T, H), "residual") if residual is not None else None,
+            _arg(ctx, out, bf16, (T, H), "out"), ps)
+
+
+def moe_layer(ctx, x, topk_idx, topk_weights, w1, w2, residual=None, out=None, workspace=None):
+    """The experts of a few tokens (T * k at most MOE_LAYER_MAX_ROWS) in one call: x bf16 [T, H], topk_idx int64 and
+    topk_weights fp32 [T, k], w1 bf16 [E, 2I, H] (gates first), w2 bf16 [E, H, I], residual bf16 [T, H] -> bf16 [T, H].
+    workspace: at least T * k * I * 2 bytes."""
+    T, I, out, workspace, px, pi, pw, p1, p2, pr, po, ps = _layer_args(ctx, x, topk_idx, topk_weights, w1, w2, torch.bfloat16, residual,
+                                                                       out, workspace)
+    _check(load_library().moe_layer(ctx.handle, px, pi, pw, T, p1, p2, I, pr, po, ps, _stream()), "moe_layer")
+    return out
+
+
+def moe_layer_fp8(ctx, x, topk_idx, topk_weights, w1, w1_scales, w2, w2_scales, residual=None, out=None, workspace=None):
+    """moe_layer with matrices of E4M3 codes (uint8) and fp32 scales of 128 x 128 blocks, w1_scales [E, 2I/128, H/128]
+    and w2_scales [E, H/128, I/128]."""
+    T, I, out, workspace, px, pi, pw, p1, p2, pr, po, ps = _layer_args(ctx, x, topk_idx, topk_weights, w1, w2, torch.uint8, residual,
+                                                                       out, workspace)
+    E, H = ctx.cfg.num_experts, ctx.cfg.hidden
+    s1 = _arg(ctx, w1_scales, torch.float32, (E, 2 * I // 128, H // 128), "w1_scales")
+    s2 = _arg(ctx, w2_scales, torch.float32, (E, H // 128, I // 128), "w2_scales")
+    _check(load_library().moe_layer_fp8(ctx.handle, px, pi, pw, T, p1, s1, p2, s2, I, pr, po, ps, _stream()), "moe_layer_fp8")
+    return out
 
 
 # ---------------------------------------------------------------- prepared calls

@@ -73,7 +73,8 @@ inline bool on_ctx_device(const moe_ctx* ctx) {
 inline const char* kernel_name(int id) {
     static const char* names[MOE_KERNEL_COUNT] = {"layout", "dispatch", "combine", "dispatch_backward",
                                                   "combine_backward", "expert_gemm", "expert_gemm_backward_rows",
-                                                  "expert_gemm_backward_weights", "swiglu", "swiglu_backward"};
+                                                  "expert_gemm_backward_weights", "swiglu", "swiglu_backward", "route",
+                                                  "route_backward", "linear", "linear_backward", "layer"};
     return id >= 0 && id < MOE_KERNEL_COUNT ? names[id] : "?";
 }
 

@@ -1,0 +1,395 @@
+// The router: experts and weights of each token from its logits, and the logits'
+// gradient.
+//
+// A token's logits sit in the registers of W lanes, expert u * W + l in lane l's u-th.
+// What is chosen is decided by keys that are compared exactly: without a bias and
+// without groups the logit itself (binary32; the score grows with it), otherwise
+// score + bias in binary64, so that two experts closer than binary32 can tell are
+// still taken in the formula's order.  The weights need no more than binary32.
+#include <type_traits>
+
+#include "moe_ep.h"
+#include "moe_internal.h"
+#include "moe_layer.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+
+// The value of the lane whose number differs in bit STEP, or of one that holds the same (what
+// a reduction over aligned runs of lanes needs): quads, then mirrored halves of 16 lanes, then exchanges.
+template <int STEP>
+__device__ __forceinline__ uint32_t other(uint32_t v) {
+    if constexpr (STEP == 1) return __builtin_amdgcn_update_dpp(v, v, 0xB1, 0xF, 0xF, true);
+    else if constexpr (STEP == 2) return __builtin_amdgcn_update_dpp(v, v, 0x4E, 0xF, 0xF, true);
+    else if constexpr (STEP == 4) return __builtin_amdgcn_update_dpp(v, v, 0x141, 0xF, 0xF, true);
+    else if constexpr (STEP == 8) return __builtin_amdgcn_update_dpp(v, v, 0x140, 0xF, 0xF, true);
+    else return __shfl_xor(v, STEP, 64);
+}
+template <int STEP, class T>
+__device__ __forceinline__ T other_of(T v) {
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(T, other<STEP>(__builtin_bit_cast(uint32_t, v)));
+    } else {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        return __builtin_bit_cast(T, ((uint64_t)other<STEP>((uint32_t)(b >> 32)) << 32) | other<STEP>((uint32_t)b));
+    }
+}
+// f(f(..)) over the W lanes of a token; every lane gets the result.
+template <int W, class T, class F>
+__device__ __forceinline__ T over(T v, F f) {
+    v = f(v, other_of<1>(v));
+    v = f(v, other_of<2>(v));
+    v = f(v, other_of<4>(v));
+    v = f(v, other_of<8>(v));
+    if constexpr (W == 64) {
+        v = f(v, other_of<16>(v));
+        v = f(v, other_of<32>(v));
+    }
+    return v;
+}
+struct Max {
+    template <class T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return a > b ? a : b; }
+};
+struct Min {
+    template <class T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return a < b ? a : b; }
+};
+struct Add {
+    template <class T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+
+template <class Key>
+__device__ __forceinline__ Key lowest() { return -(Key)__builtin_inff(); }
+
+__device__ __forceinline__ float logit_of(const void* logits, int64_t at, bool bf16) {
+    return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[at] << 16)
+                : static_cast<const float*>(logits)[at];
+}
+
+// 1 / (1 + e^-v) and its complement, both without cancellation.
+__device__ __forceinline__ float sigmoid32(float v) { return 1.0f / (1.0f + expf(-v)); }
+
+// A token on W lanes, PER logits a lane.  Key: float where keys are logits, double where they are scores.
+template <bool BF16, class Key, int W, int PER>
+__global__ __launch_bounds__(kThreads) void k_route(RouteArgs a) {
+    constexpr bool kScored = sizeof(Key) == 8;
+    constexpr float kNone = -__builtin_inff();
+    const int lane = threadIdx.x & 63, l = lane & (W - 1);
+    const int t = (int)blockIdx.x * (kThreads / W) + (int)threadIdx.x / W;
+    const bool live = t < a.T;
+    float v[PER];
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        const int e = u * W + l;
+        v[u] = live && e < a.E ? logit_of(a.logits, t * a.stride + e, BF16) : kNone;
+        // infinite or NaN: not chosen, reported; -inf: not chosen
+        if (!(v[u] < __builtin_inff())) {
+            bad = true;
+            v[u] = kNone;
+        }
+    }
+    if (__ballot(bad) != 0 && lane == 0) atomicOr(a.err, kErrNonFinite);
+    float top = v[0];
+#pragma unroll
+    for (int u = 1; u < PER; ++u) top = fmaxf(top, v[u]);
+    top = over<W>(top, Max());
+    if (!(top > kNone)) top = 0.0f;   // nothing can be chosen: every exponential is zero
+
+    Key key[PER];
+    float total = 0.0f;   // of the softmax's exponentials
+    if constexpr (!kScored) {
+#pragma unroll
+        for (int u = 0; u < PER; ++u) key[u] = v[u];
+        if (!a.sigmoid && !a.normalize) {
+#pragma unroll
+            for (int u = 0; u < PER; ++u) total += expf(v[u] - top);
+            total = over<W>(total, Add());
+        }
+    } else {
+        double sum = 0.0;
+        if (a.sigmoid) {
+#pragma unroll
+            for (int u = 0; u < PER; ++u) key[u] = 1.0 / (1.0 + exp(-(double)v[u]));
+        } else {
+#pragma unroll
+            for (int u = 0; u < PER; ++u) {
+                key[u] = exp((double)v[u] - (double)top);
+                sum += key[u];
+            }
+            sum = over<W>(sum, Add());
+            total = (float)sum;
+            if (!(sum > 0.0)) sum = 1.0;
+#pragma unroll
+            for (int u = 0; u < PER; ++u) key[u] /= sum;
+        }
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            const int e = u * W + l;
+            if (a.bias != nullptr && e < a.E) key[u] += (double)a.bias[e];
+            if (!(v[u] > kNone) || key[u] != key[u]) key[u] = lowest<Key>();
+        }
+        if (a.groups > 1) {
+            // A group's score by one lane, its experts in turn, through LDS.
+            extern __shared__ double shared[];
+            double* mine = shared + (threadIdx.x / W) * a.E;
+#pragma unroll
+            for (int u = 0; u < PER; ++u)
+                if (u * W + l < a.E) mine[u * W + l] = key[u];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+            const int size = a.E / a.groups;
+            double score[64 / W];   // of group i * W + l
+#pragma unroll
+            for (int i = 0; i < 64 / W; ++i) {
+                const int g = i * W + l;
+                double first = lowest<Key>(), second = lowest<Key>();
+                if (g < a.groups)
+                    for (int n = 0; n < size; ++n) {
+                        const double x = mine[g * size + n];
+                        second = fmax(second, fmin(first, x));
+                        first = fmax(first, x);
+                    }
+                score[i] = a.top > 1 && second > lowest<Key>() ? first + second : first;
+            }
+            uint64_t kept = 0;
+            for (int n = 0; n < a.keep; ++n) {
+                double m = score[0];
+#pragma unroll
+                for (int i = 1; i < 64 / W; ++i) m = fmax(m, score[i]);
+                m = over<W>(m, Max());
+                if (!(m > lowest<Key>())) break;
+                int g = INT32_MAX;
+#pragma unroll
+                for (int i = 64 / W - 1; i >= 0; --i)
+                    if (score[i] == m) g = i * W + l;
+                g = over<W>(g, Min());
+                kept |= 1ull << g;
+#pragma unroll
+                for (int i = 0; i < 64 / W; ++i)
+                    if (i * W + l == g) score[i] = lowest<Key>();
+            }
+#pragma unroll
+            for (int u = 0; u < PER; ++u) {
+                const uint32_t e = u * W + l;
+                const uint32_t g = a.group_magic ? __umulhi(e, a.group_magic) : e;
+                if (!(kept >> (g & 63) & 1)) key[u] = lowest<Key>();
+            }
+        }
+    }
+
+    // The best of what is left, k times; of equal keys the lowest expert.  Lane j keeps the j-th (k <= 32: two on 16 lanes).
+    constexpr int kSlots = W == 64 ? 1 : 2;
+    int mine_e[kSlots];
+    float mine_v[kSlots];
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+        mine_e[i] = -1;
+        mine_v[i] = kNone;
+    }
+    for (int j = 0; j < a.k; ++j) {
+        Key m = key[0];
+#pragma unroll
+        for (int u = 1; u < PER; ++u) m = Max()(m, key[u]);
+        m = over<W>(m, Max());
+        if (__ballot(m > lowest<Key>()) == 0) break;
+        int e = INT32_MAX;
+        float x = kNone;
+#pragma unroll
+        for (int u = PER - 1; u >= 0; --u)
+            if (key[u] == m) {
+                e = u * W + l;
+                x = v[u];
+            }
+        const int chosen = over<W>(e, Min());
+        x = over<W>(e == chosen ? x : kNone, Max());   // its logit
+        if (m > lowest<Key>()) {
+#pragma unroll
+            for (int u = 0; u < PER; ++u)
+                if (u * W + l == chosen) key[u] = lowest<Key>();
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i)
+                if (i * W + l == j) {
+                    mine_e[i] = chosen;
+                    mine_v[i] = x;
+                }
+        }
+    }
+    // weights: shares of the chosen scores' sum, or the scores themselves
+    float peak = kNone;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) peak = fmaxf(peak, mine_v[i]);
+    peak = over<W>(peak, Max());
+    float w[kSlots], sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+        const float x = mine_v[i];
+        if (mine_e[i] < 0) w[i] = 0.0f;
+        else if (a.sigmoid) {
+            // shares do not change when every score is divided by e^peak: a sum of small scores stays away from zero
+            if (a.normalize && peak < 0.0f) w[i] = expf(x - peak) / (1.0f + expf(x));
+            else w[i] = sigmoid32(x);
+        } else w[i] = expf(x - (a.normalize ? peak : top));
+        sum += w[i];
+    }
+    sum = over<W>(sum, Add());
+    const float by = !a.normalize ? (a.sigmoid ? a.scale : a.scale / (total > 0.0f ? total : 1.0f)) : sum > 0.0f ? a.scale / sum : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+        const int j = i * W + l;
+        if (live && j < a.k) {
+            a.idx[(int64_t)t * a.k + j] = mine_e[i];
+            a.weights[(int64_t)t * a.k + j] = w[i] * by;
+        }
+    }
+}
+
+// The gradient of a token's logits.  With r the weights without their factor c and g their gradients:
+//   sigmoid              c g s (1 - s) for each slot's expert
+//   shares (normalised)  c r (g - sum g r) for each slot's expert, for sigmoids times 1 - s as well
+//   softmax              c p g for each slot's expert, -c p (sum g p) for every expert
+template <bool BF16, int W, int PER>
+__global__ __launch_bounds__(kThreads) void k_route_bwd(RouteBwdArgs a) {
+    constexpr float kNone = -__builtin_inff();
+    constexpr int kSlots = W == 64 ? 1 : 2;
+    const int l = threadIdx.x & (W - 1);
+    const int t = (int)blockIdx.x * (kThreads / W) + (int)threadIdx.x / W;
+    const bool live = t < a.T;
+    const bool spread = !a.sigmoid && !a.normalize;   // every expert has a gradient
+    float v[PER];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        const int e = u * W + l;
+        v[u] = spread && live && e < a.E ? logit_of(a.logits, t * a.stride + e, BF16) : kNone;
+        if (!(v[u] < __builtin_inff())) v[u] = kNone;
+    }
+    int e[kSlots];
+    float x[kSlots], g[kSlots], peak = kNone;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+        const int j = i * W + l;
+        const int64_t id = live && j < a.k ? a.idx[(int64_t)t * a.k + j] : -1;
+        if (id < -1 || id >= a.E) atomicOr(a.err, kErrBadTopk);
+        e[i] = id >= 0 && id < a.E ? (int)id : -1;
+        x[i] = e[i] >= 0 ? logit_of(a.logits, t * a.stride + e[i], BF16) : kNone;
+        if (!(x[i] < __builtin_inff() && x[i] > kNone)) e[i] = -1;   // it cannot have been chosen
+        if (e[i] < 0) x[i] = kNone;
+        g[i] = e[i] >= 0 ? a.grad[(int64_t)t * a.k + j] : 0.0f;
+        peak = fmaxf(peak, x[i]);
+    }
+    peak = over<W>(peak, Max());
+    float top = kNone, total = 1.0f;
+    if (spread) {
+#pragma unroll
+        for (int u = 0; u < PER; ++u) top = fmaxf(top, v[u]);
+        top = over<W>(top, Max());
+        if (!(top > kNone)) top = 0.0f;
+        total = 0.0f;
+#pragma unroll
+        for (int u = 0; u < PER; ++u) total += expf(v[u] - top);
+        total = over<W>(total, Add());
+        if (!(total > 0.0f)) total = 1.0f;
+    }
+    float r[kSlots], sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+        if (e[i] < 0) r[i] = 0.0f;
+        else if (a.sigmoid) r[i] = a.normalize && peak < 0.0f ? expf(x[i] - peak) / (1.0f + expf(x[i])) : sigmoid32(x[i]);
+        else r[i] = expf(x[i] - (a.normalize ? peak : top)) / total;
+        sum += r[i];
+    }
+    if (a.normalize) {
+        sum = over<W>(sum, Add());
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) r[i] = sum > 0.0f ? r[i] / sum : 0.0f;
+    }
+    float mean = 0.0f;   // sum of g r, where the scores share a sum
+    if (a.normalize || !a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) mean += g[i] * r[i];
+        mean = over<W>(mean, Add());
+    }
+    float d[kSlots];
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+        d[i] = a.scale * r[i] * (spread ? g[i] : g[i] - mean);
+        if (a.sigmoid && e[i] >= 0) d[i] *= sigmoid32(-x[i]);
+    }
+    float out[PER];
+    const float rest = a.scale * mean;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) out[u] = spread ? -(expf(v[u] - top) / total) * rest : 0.0f;
+    // each chosen expert's own, from the lane that has its slot
+    for (int j = 0; j < a.k; ++j) {
+        const int from = (threadIdx.x & 63 & ~(W - 1)) | (j & (W - 1));
+        int ej = e[0];
+        float dj = d[0];
+        if (kSlots > 1 && j >= W) {
+            ej = e[kSlots - 1];
+            dj = d[kSlots - 1];
+        }
+        ej = __shfl(ej, from, 64);
+        dj = __shfl(dj, from, 64);
+#pragma unroll
+        for (int u = 0; u < PER; ++u)
+            if (u * W + l == ej) out[u] += dj;
+    }
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+        const int ex = u * W + l;
+        if (live && ex < a.E) a.grad_logits[(int64_t)t * a.E + ex] = out[u];
+    }
+}
+
+template <class F16, class F64>
+hipError_t by_experts(int E, F16 on16, F64 on64) {
+    using std::integral_constant;
+    if (E <= 16) return on16(integral_constant<int, 1>());
+    if (E <= 64) return on16(integral_constant<int, 4>());
+    if (E <= 128) return on16(integral_constant<int, 8>());
+    if (E <= 256) return on16(integral_constant<int, 16>());
+    if (E <= 512) return on64(integral_constant<int, 8>());
+    return on64(integral_constant<int, 16>());
+}
+
+template <bool BF16, class Key>
+hipError_t route(const RouteArgs& a, hipStream_t s) {
+    auto go = [&](auto w, auto per) {
+        constexpr int W = decltype(w)::value, PER = decltype(per)::value;
+        const int tokens = kThreads / W;
+        const size_t lds = sizeof(Key) == 8 && a.groups > 1 ? (size_t)tokens * a.E * sizeof(double) : 0;
+        k_route<BF16, Key, W, PER><<<dim3((unsigned)((a.T + tokens - 1) / tokens)), dim3(kThreads), lds, s>>>(a);
+        return hipGetLastError();
+    };
+    return by_experts(a.E, [&](auto per) { return go(std::integral_constant<int, 16>(), per); },
+                      [&](auto per) { return go(std::integral_constant<int, 64>(), per); });
+}
+
+template <bool BF16>
+hipError_t route_bwd(const RouteBwdArgs& a, hipStream_t s) {
+    auto go = [&](auto w, auto per) {
+        constexpr int W = decltype(w)::value, PER = decltype(per)::value;
+        const int tokens = kThreads / W;
+        k_route_bwd<BF16, W, PER><<<dim3((unsigned)((a.T + tokens - 1) / tokens)), dim3(kThreads), 0, s>>>(a);
+        return hipGetLastError();
+    };
+    return by_experts(a.E, [&](auto per) { return go(std::integral_constant<int, 16>(), per); },
+                      [&](auto per) { return go(std::integral_constant<int, 64>(), per); });
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteArgs& a, bool bf16, hipStream_t s) {
+    const bool scored = a.bias != nullptr || a.groups > 1;
+    if (bf16) return scored ? route<true, double>(a, s) : route<true, float>(a, s);
+    return scored ? route<false, double>(a, s) : route<false, float>(a, s);
+}
+
+hipError_t launch_route_bwd(const RouteBwdArgs& a, bool bf16, hipStream_t s) {
+    return bf16 ? route_bwd<true>(a, s) : route_bwd<false>(a, s);
+}
+
+}  // namespace moe

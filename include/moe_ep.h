@@ -40,7 +40,8 @@
  *    buffer or a low-latency window overflow (the row is not placed), a reused
  *    layout made from other routing (the changed tokens are dropped, see
  *    moe_dispatch), Inf or NaN in an fp8 dispatch or activation (those blocks'
- *    codes and scales are unspecified) and expert offsets of a handle that are
+ *    codes and scales are unspecified), a logit that is NaN or +infinite (moe_route:
+ *    that expert is not chosen) and expert offsets of a handle that are
  *    not ascending or pass num_tokens * topk (the products take those experts to have no
  *    rows; the activation computes the rows before the last offset, none if that
  *    one is out of range).
@@ -60,9 +61,10 @@
 extern "C" {
 #endif
 
-#define MOE_EP_ABI_VERSION 6   /* 3: moe_timing_launches; 4: stale-layout and non-finite
+#define MOE_EP_ABI_VERSION 7   /* 3: moe_timing_launches; 4: stale-layout and non-finite
                                   flags, moe_dispatch_noalloc; 5: moe_dispatch_layout_prefetch;
-                                  6: expert products and gated activation, MOE_KERNEL_COUNT 10 */
+                                  6: expert products and gated activation, MOE_KERNEL_COUNT 10;
+                                  7: router, dense product, layer of a few tokens, MOE_KERNEL_COUNT 15 */
 
 /* ---------------------------------------------------------------- status */
 typedef enum moe_status {
@@ -457,6 +459,146 @@ moe_status moe_swiglu_backward(moe_ctx* ctx, const void* grad_out, const void* g
                                int32_t features, int32_t order, const moe_handle* handle,
                                void* grad_gate_up, void* stream);
 
+/* ---------------------------------------------------------------- router */
+/* What stands before the dispatch (an addition: the pages begin with topk_idx, and
+ * name group-limited gating, which these calls have): the experts and weights of
+ * each token from its logits, in the form that moe_dispatch, moe_combine and moe_layer
+ * read.  E and k are the context's; num_tokens is at most max_tokens. */
+typedef enum moe_score {
+    MOE_SCORE_SOFTMAX = 0,     /* s = softmax of the token's logits, over all its experts */
+    MOE_SCORE_SIGMOID = 1      /* s = 1 / (1 + exp(-logit)) */
+} moe_score;
+typedef enum moe_logit_type {
+    MOE_LOGIT_F32 = 0,
+    MOE_LOGIT_BF16 = 1
+} moe_logit_type;
+#define MOE_MAX_GROUPS 64
+
+typedef struct moe_router {    /* host struct */
+    int32_t score;             /* moe_score */
+    int32_t groups;            /* G, 1..MOE_MAX_GROUPS, divides E: groups of E / G neighbouring experts; 1 = no groups */
+    int32_t topk_groups;       /* 1..G: groups that stay; their experts alone can be chosen */
+    int32_t group_top;         /* 1 or 2: a group's score is the sum of so many of its largest s + bias */
+    int32_t normalize;         /* 1: a token's weights are divided by their sum */
+    float   scale;             /* factor of all weights; finite */
+} moe_router;
+
+/* topk_idx[t] = the k experts with the largest s + bias, descending, ties to the lowest
+ * expert; topk_weights[t, j] = scale * s[topk_idx[t, j]], divided by the sum of the chosen s
+ * if asked (bias decides what is chosen and does not enter the weights).
+ *   logits        [num_tokens, E] fp32 or bf16; rows `logits_stride` elements apart
+ *                 (>= E); aligned to their type
+ *   bias          fp32 [E], nullable; not NaN
+ *   topk_idx      int64 [num_tokens, k]
+ *   topk_weights  fp32 [num_tokens, k]
+ * A logit of -inf masks its expert: it is not chosen, has score 0 and adds nothing to its group.
+ * So does NaN or +inf, which moe_poll_error reports (MOE_ERR_NONFINITE).  Where fewer than k
+ * experts are left the last slots are -1 with weight 0; a token with none has -1 throughout.
+ * Without bias and groups experts are compared by their logits, otherwise by
+ * s + bias in binary64.  Weights are computed in binary32. */
+moe_status moe_route(moe_ctx* ctx, const void* logits, int32_t logit_type, int64_t logits_stride,
+                     int32_t num_tokens, const moe_router* router, const float* bias,
+                     int64_t* topk_idx, float* topk_weights, void* stream);
+
+/* Gradient of topk_weights with respect to the logits (the choice itself has none):
+ *   grad_weights  fp32 [num_tokens, k]; not read for an empty slot
+ *   topk_idx      what moe_route gave (or any experts: a slot -1, or of a masked expert, has no
+ *                 part; an expert in two slots gets both gradients; an id outside
+ *                 [-1, E) is taken as -1 and reported)
+ *   grad_logits   fp32 [num_tokens, E], contiguous, written whole */
+moe_status moe_route_backward(moe_ctx* ctx, const float* grad_weights, const void* logits,
+                              int32_t logit_type, int64_t logits_stride, const int64_t* topk_idx,
+                              int32_t num_tokens, const moe_router* router, float* grad_logits,
+                              void* stream);
+
+/* ---------------------------------------------------------------- dense product */
+/* The product around the experts: the router's logits, the shared expert that
+ * every token passes.  Any number of rows (max_tokens does not bound it); of the
+ * context only the device and the error word are used. */
+typedef enum moe_act {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,
+    MOE_ACT_SILU = 2,          /* v / (1 + exp(-v)) */
+    MOE_ACT_GELU = 3,          /* v / 2 * (1 + erf(v / sqrt(2))) */
+    MOE_ACT_GELU_TANH = 4,     /* v / 2 * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3))) */
+    MOE_ACT_SWIGLU = 5         /* silu(gate) * up of 2 F columns, gates first */
+} moe_act;
+typedef enum moe_out_type {
+    MOE_OUT_BF16 = 0,
+    MOE_OUT_F32 = 1
+} moe_out_type;
+
+/* out[r, n] = act( sum over c of x[r, c] * W[n, c] + bias[n] ) + residual[r, n].
+ * With M = F, or 2 F for MOE_ACT_SWIGLU:
+ *   x          bf16 [num_rows, in_features]
+ *   weights    bf16 [M, in_features]
+ *   bias       bf16 [M], nullable
+ *   residual   bf16 [num_rows, F], nullable; may be out where that is bf16
+ *   out        [num_rows, F] of out_type
+ *   pre        bf16 [num_rows, M], nullable: receives the sums with their bias, for
+ *              moe_linear_backward
+ * F is `features`, in_features and F multiples of 8, M and in_features at most MOE_MAX_FEATURES, else
+ * MOE_ERR_UNSUPPORTED (as are more tiles of 256 x 256 than 2^23 - 256); buffers 16-byte aligned; only residual and out
+ * may overlap.  Sums and epilogue are binary32, each output is rounded once, in an order that the sizes decide. */
+moe_status moe_linear(moe_ctx* ctx, const void* x, int32_t num_rows, const void* weights,
+                      int32_t in_features, int32_t features, const void* bias, int32_t act,
+                      const void* residual, void* out, int32_t out_type, void* pre, void* stream);
+
+/* Gradients of moe_linear.  With d[r, m] the gradient before the activation (grad_out * act'(pre)):
+ *   grad_x[r, c] = sum over m of d[r, m] * W[m, c]        bf16 [num_rows, in_features], nullable
+ *   grad_weights[m, c] = sum over r of d[r, m] * x[r, c]  [M, in_features] of grad_type, nullable
+ *   grad_bias[m] = sum over r of d[r, m]                  fp32 [M], nullable
+ * (The residual's gradient is grad_out.)
+ *   grad_out    [num_rows, F] of out_type
+ *   x, weights  as in moe_linear; weights is read for grad_x, x for grad_weights (else NULL will do)
+ *   pre         what moe_linear wrote; not read for MOE_ACT_NONE (may be NULL)
+ *   accumulate  1: grad_weights and grad_bias are added to what they hold
+ *   workspace   moe_linear_backward_workspace bytes, 16-byte aligned: holds d, rounded to bf16 for the products
+ *               (grad_bias adds the binary32 values), and sums; NULL if that is 0
+ * With no rows grad_weights and grad_bias are zeroed (or left, with accumulate). */
+moe_status moe_linear_backward(moe_ctx* ctx, const void* grad_out, int32_t out_type, int32_t num_rows,
+                               const void* x, const void* weights, int32_t in_features,
+                               int32_t features, int32_t act, const void* pre, void* grad_x,
+                               void* grad_weights, int32_t grad_type, int32_t accumulate,
+                               float* grad_bias, void* workspace, void* stream);
+/* Bytes of its workspace (host; needs no GPU). */
+moe_status moe_linear_backward_workspace(int32_t num_rows, int32_t features, int32_t act,
+                                         int32_t out_type, int32_t with_bias, size_t* bytes);
+
+/* ---------------------------------------------------------------- a few tokens */
+/* Everything between the router and the layer's output, for decode-sized
+ * batches and inference: what dispatch, expert products, activation and combine
+ * give, without receive rows in between.  For a slot (t, j) with expert e = topk_idx[t, j]:
+ *   (g, u) = W1[e] x[t],   y = W2[e] (silu(g) * u)
+ *   out[t] = residual[t] + sum over valid j, ascending, of topk_weights[t, j] * y
+ *   x             bf16 [num_tokens, H]
+ *   topk_idx      int64 [num_tokens, k]; -1 = empty slot (its weight is not used), an id outside
+ *                 [-1, E) is taken as -1 and reported; a repeated expert counts each time
+ *   topk_weights  fp32 [num_tokens, k]
+ *   w1, w2        bf16 [E, 2 * features, H] (gates first) and [E, H, features]
+ *   residual      bf16 [num_tokens, H], nullable; may be out
+ *   out           bf16 [num_tokens, H]; a token without an expert gets its residual, or 0
+ *   workspace     num_tokens * k * features * 2 bytes, 16-byte aligned: silu(g) * u, rounded to bf16
+ * num_tokens is at most max_tokens, and num_tokens * k at most MOE_LAYER_MAX_ROWS, else
+ * MOE_ERR_CAPACITY and MOE_ERR_UNSUPPORTED.  features is a multiple of 8 and at most MOE_MAX_FEATURES / 2; buffers are
+ * 16-byte aligned (topk_idx 8, topk_weights and scales 4); only residual and out may overlap.  All sums are binary32, y is not
+ * rounded, and the order of sums is that of sizes and routing. */
+#define MOE_LAYER_MAX_ROWS 1024
+moe_status moe_layer(moe_ctx* ctx, const void* x, const int64_t* topk_idx, const float* topk_weights,
+                     int32_t num_tokens, const void* w1, const void* w2, int32_t features,
+                     const void* residual, void* out, void* workspace, void* stream);
+
+/* The same with matrices of E4M3 codes and a scale for each 128 x 128 block:
+ *   w1_scales  fp32 [E, 2 * features / 128, H / 128]
+ *   w2_scales  fp32 [E, H / 128, features / 128]
+ * H and features multiples of 128.  Rows and activations stay bf16 (the codes are widened exactly): few
+ * rows cost nothing beside the matrices, so nothing is lost by quantising them. */
+moe_status moe_layer_fp8(moe_ctx* ctx, const void* x, const int64_t* topk_idx,
+                         const float* topk_weights, int32_t num_tokens, const void* w1,
+                         const float* w1_scales, const void* w2, const float* w2_scales,
+                         int32_t features, const void* residual, void* out, void* workspace,
+                         void* stream);
+
 /* ---------------------------------------------------------------- overlap */
 /* Resource control (DeepTech release article, feature list: flexible GPU
  * resource control and SM-count control for the high-throughput kernels; the
@@ -517,7 +659,12 @@ typedef enum moe_kernel_id {
     MOE_KERNEL_EXPERT_BWD_WEIGHTS = 7,
     MOE_KERNEL_SWIGLU = 8,             /* gated activation, bf16 and fp8 */
     MOE_KERNEL_SWIGLU_BWD = 9,
-    MOE_KERNEL_COUNT = 10
+    MOE_KERNEL_ROUTE = 10,
+    MOE_KERNEL_ROUTE_BWD = 11,
+    MOE_KERNEL_LINEAR = 12,
+    MOE_KERNEL_LINEAR_BWD = 13,        /* all launches of a call as one */
+    MOE_KERNEL_LAYER = 14,             /* both launches of a call as one */
+    MOE_KERNEL_COUNT = 15
 } moe_kernel_id;
 
 moe_status moe_timing_begin(moe_ctx* ctx, int32_t max_launches);
