@@ -26,4 +26,4 @@ from ._binding import (  # noqa: F401
     MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_SWIGLU, MOE_KERNEL_LAYER,
     MOE_KERNEL_LINEAR, MOE_KERNEL_LINEAR_BWD, MOE_KERNEL_ROUTE, MOE_KERNEL_ROUTE_BWD, MOE_LAYER_MAX_ROWS, MOE_LOGIT_BF16,
     MOE_LOGIT_F32, MOE_MAX_GROUPS, MOE_OUT_BF16, MOE_OUT_F32, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, moe_layer, moe_layer_fp8,
-    moe_linear, moe_linear_backward, moe_linear_backward_workspace, moe_route, moe_route_backward)
+    moe_linear, moe_linear_backward, moe_linear_backward_workspace, moe_linear_workspace, moe_route, moe_route_backward)

@@ -6,6 +6,7 @@ the stream (torch.cuda.current_stream()).  There is no fallback: if the library
 is missing or a call fails, an exception is raised.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -101,7 +102,7 @@ EXPORTS = ("moe_status_str", "moe_size_hint", "moe_ctx_create", "moe_ctx_destroy
            "moe_dispatch_layout_prefetch", "moe_expert_gemm", "moe_expert_gemm_fp8",
            "moe_expert_gemm_backward_rows", "moe_expert_gemm_backward_weights", "moe_swiglu", "moe_swiglu_fp8",
            "moe_swiglu_backward", "moe_route", "moe_route_backward", "moe_linear", "moe_linear_backward",
-           "moe_linear_backward_workspace", "moe_layer", "moe_layer_fp8")
+           "moe_linear_workspace", "moe_linear_backward_workspace", "moe_layer", "moe_layer_fp8")
 
 _lib = None
 
@@ -153,9 +154,10 @@ def load_library(path=LIB_PATH):
         "moe_swiglu_backward": [vp, vp, vp, i32, i32, ctypes.POINTER(moe_handle), vp, vp],
         "moe_route": [vp, vp, i32, ctypes.c_int64, i32, ctypes.POINTER(moe_router), vp, vp, vp, vp],
         "moe_route_backward": [vp, vp, vp, i32, ctypes.c_int64, vp, i32, ctypes.POINTER(moe_router), vp, vp],
-        "moe_linear": [vp, vp, i32, vp, i32, i32, vp, i32, vp, vp, i32, vp, vp],
+        "moe_linear": [vp, vp, i32, vp, i32, i32, vp, i32, vp, vp, i32, vp, vp, vp],
+        "moe_linear_workspace": [i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
         "moe_linear_backward": [vp, vp, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp, i32, i32, vp, vp, vp],
-        "moe_linear_backward_workspace": [i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
+        "moe_linear_backward_workspace": [i32, i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
         "moe_layer": [vp, vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, vp],
         "moe_layer_fp8": [vp, vp, vp, vp, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp],
     }
@@ -705,7 +707,7 @@ def moe_swiglu_backward(ctx, grad_out, gate_up, handle, grad_gate_up=None, order
     po = _expert_rows(ctx, grad_gate_up, torch.bfloat16, 2 * features, order, "grad_gate_up")
     _check(load_library().moe_swiglu_backward(ctx.handle, pd, pg, features, order, ctypes.byref(handle.c), po, _stream()),
            "moe_swiglu_backward", "moe_route", "moe_route_backward", "moe_linear", "moe_linear_backward",
-           "moe_linear_backward_workspace", "moe_layer", "moe_layer_fp8")
+           "moe_linear_workspace", "moe_linear_backward_workspace", "moe_layer", "moe_layer_fp8")
     return grad_gate_up
 
 
@@ -801,10 +803,19 @@ def _linear_sizes(x, weights, act):
     return x.shape[0], K, M // 2 if act == MOE_ACT_SWIGLU else M, M
 
 
-def moe_linear(ctx, x, weights, bias=None, act=MOE_ACT_NONE, residual=None, out=None, out_dtype=torch.bfloat16, pre=None):
+@functools.lru_cache(maxsize=4096)
+def moe_linear_workspace(T, in_features, features, act=MOE_ACT_NONE):
+    """Bytes that moe_linear works in (by sizes alone, so kept)."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_linear_workspace(T, in_features, features, act, ctypes.byref(n)), "moe_linear_workspace")
+    return n.value
+
+
+def moe_linear(ctx, x, weights, bias=None, act=MOE_ACT_NONE, residual=None, out=None, out_dtype=torch.bfloat16, pre=None,
+               workspace=None):
     """act(x weights^T + bias) + residual: x bf16 [T, K], weights bf16 [M, K], bias bf16 [M], residual bf16 [T, F] ->
     [T, F], bf16 or fp32 (out's dtype, or out_dtype), F = M, or M / 2 for MOE_ACT_SWIGLU.  pre: bf16 [T, M], receives
-    what moe_linear_backward needs."""
+    what moe_linear_backward needs.  workspace: moe_linear_workspace bytes."""
     T, K, F, M = _linear_sizes(x, weights, act)
     if out is None:
         out = _empty(ctx, (T, F), out_dtype)
@@ -812,19 +823,21 @@ def moe_linear(ctx, x, weights, bias=None, act=MOE_ACT_NONE, residual=None, out=
     if kind is None:
         raise TypeError("out must be bfloat16 or float32")
     bf16 = torch.bfloat16
+    ps, workspace = _workspace(ctx, workspace, moe_linear_workspace(T, K, F, act))
     _check(load_library().moe_linear(
         ctx.handle, _arg(ctx, x, bf16, (T, K), "x"), T, _arg(ctx, weights, bf16, (M, K), "weights"), K, F,
         _arg(ctx, bias, bf16, (M,), "bias") if bias is not None else None, act,
         _arg(ctx, residual, bf16, (T, F), "residual") if residual is not None else None, _arg(ctx, out, out.dtype, (T, F), "out"),
-        kind, _arg(ctx, pre, bf16, (T, M), "pre") if pre is not None else None, _stream()), "moe_linear")
+        kind, _arg(ctx, pre, bf16, (T, M), "pre") if pre is not None else None, ps, _stream()), "moe_linear")
     return out
 
 
-def moe_linear_backward_workspace(T, features, act=MOE_ACT_NONE, out_dtype=torch.bfloat16, bias=False):
-    """Bytes that moe_linear_backward works in."""
+@functools.lru_cache(maxsize=4096)
+def moe_linear_backward_workspace(T, in_features, features, act=MOE_ACT_NONE, out_dtype=torch.bfloat16, bias=False):
+    """Bytes that moe_linear_backward works in (by sizes and types alone, so kept)."""
     n = ctypes.c_size_t(0)
-    _check(load_library().moe_linear_backward_workspace(T, features, act, _OUT_TYPES[out_dtype], int(bool(bias)), ctypes.byref(n)),
-           "moe_linear_backward_workspace")
+    _check(load_library().moe_linear_backward_workspace(T, in_features, features, act, _OUT_TYPES[out_dtype], int(bool(bias)),
+                                                        ctypes.byref(n)), "moe_linear_backward_workspace")
     return n.value
 
 
@@ -848,7 +861,7 @@ def moe_linear_backward(ctx, grad_out, x, weights, act=MOE_ACT_NONE, pre=None, b
         grad_bias = _empty(ctx, (M,), f32)
     if grad_weights is not None and grad_weights.dtype is not bf16 and grad_weights.dtype is not f32:
         raise TypeError("grad_weights must be bfloat16 or float32")
-    pw, workspace = _workspace(ctx, workspace, moe_linear_backward_workspace(T, F, act, grad_out.dtype, grad_bias is not None))
+    pw, workspace = _workspace(ctx, workspace, moe_linear_backward_workspace(T, K, F, act, grad_out.dtype, grad_bias is not None))
     _check(load_library().moe_linear_backward(
         ctx.handle, _arg(ctx, grad_out, grad_out.dtype, (T, F), "grad_out"), kind, T, _arg(ctx, x, bf16, (T, K), "x"),
         _arg(ctx, weights, bf16, (M, K), "weights"), K, F, act,

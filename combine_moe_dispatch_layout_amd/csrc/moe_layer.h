@@ -56,15 +56,26 @@ struct LinearArgs {
     const uint16_t* residual;  // bf16 [T, F], nullable
     void* out;                 // [T, F]
     uint16_t* pre;             // bf16 [T, M], nullable
+    float* partial;            // workspace: [split, T, M] sums
     int32_t T, K, F;
     int32_t act, out_f32;
+};
+
+// The products of the backward pass: D[r][c] = sum over x of P(c, x) Q(r, x), c along the rows of the output.
+struct LinearBwdArgs {
+    const void* p;             // weights [X, C] (grad_x), x [X, C] (grad_weights)
+    const void* q;             // grad [R, X] (grad_x), grad [X, R] (grad_weights)
+    void* out;                 // [R, C]
+    float* partial;            // workspace: [split, R, C] sums
+    int32_t R, C, X;
+    int32_t out_f32, accumulate;
 };
 
 struct LinearGradArgs {
     const void* grad;          // [T, F]
     const uint16_t* pre;       // bf16 [T, M]; not read without an activation
     uint16_t* grad_pre;        // bf16 [T, M], nullable
-    float* partial;            // [blocks of rows, M] sums of columns, where grad_bias is wanted
+    float* partial;            // [linear_sum_blocks(), M] sums of columns, where grad_bias is wanted; NULL for none
     float* grad_bias;          // [M], nullable
     int32_t T, F;
     int32_t act, grad_f32, accumulate;
@@ -72,8 +83,13 @@ struct LinearGradArgs {
 
 hipError_t launch_layer(const LayerArgs& a, bool fp8, hipStream_t s);
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
+int64_t linear_workspace(int64_t T, int64_t K, int64_t F, bool gated);   // bytes
+// The backward's products where linear_bwd_here() says so; the others are the expert products' gradients.
+bool linear_bwd_here(int64_t R, int64_t C);
+hipError_t launch_linear_bwd(const LinearBwdArgs& a, bool weights, hipStream_t s);
+int64_t linear_bwd_workspace(int64_t R, int64_t C, int64_t X);           // bytes
 // The gradient before the activation, and the bias's from linear_sum_blocks() rows of partial sums.
-int64_t linear_sum_blocks(int64_t T, int64_t M);
+int64_t linear_sum_blocks(int64_t T);   // 0 where one workgroup has all rows
 hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t s);
 hipError_t launch_route(const RouteArgs& a, bool bf16, hipStream_t s);
 hipError_t launch_route_bwd(const RouteBwdArgs& a, bool bf16, hipStream_t s);

@@ -2,6 +2,7 @@
 // argument checks and launches.  Nothing here allocates or blocks.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -52,17 +53,19 @@ moe_status check_linear(int32_t rows, int32_t K, int32_t F, int32_t act, int32_t
     return MOE_OK;
 }
 
-// The backward's workspace: the gradient before the activation, unless grad_out is that already, then the column sums.
+// The backward's workspace: the gradient before the activation, unless grad_out is that already; then sums, of columns and
+// after them of products in parts (one after the other, on one stream).
 struct BackwardPlan {
     bool own_pre;
     size_t sums, total;
 };
-BackwardPlan plan_backward(int32_t rows, int32_t F, int32_t act, int32_t type, bool with_bias) {
+BackwardPlan plan_backward(int32_t rows, int32_t K, int32_t F, int32_t act, int32_t type, bool with_bias) {
     const int64_t M = columns(F, act);
     BackwardPlan p;
     p.own_pre = act != MOE_ACT_NONE || type == MOE_OUT_F32;
     p.sums = p.own_pre ? ((size_t)rows * M * 2 + 255) & ~(size_t)255 : 0;
-    p.total = p.sums + (with_bias ? (size_t)linear_sum_blocks(rows, M) * M * 4 : 0);
+    const int64_t bias = with_bias ? linear_sum_blocks(rows) * M * 4 : 0;
+    p.total = p.sums + (size_t)std::max({bias, linear_bwd_workspace(rows, K, M), linear_bwd_workspace(M, K, rows)});
     return p;
 }
 
@@ -173,14 +176,18 @@ MOE_API moe_status moe_route_backward(moe_ctx* ctx, const float* grad_weights, c
 
 MOE_API moe_status moe_linear(moe_ctx* ctx, const void* x, int32_t num_rows, const void* weights, int32_t in_features,
                               int32_t features, const void* bias, int32_t act, const void* residual, void* out,
-                              int32_t out_type, void* pre, void* stream) {
+                              int32_t out_type, void* pre, void* workspace, void* stream) {
     if (ctx == nullptr || !on_ctx_device(ctx)) return MOE_ERR_INVALID_ARG;
     const moe_status st = check_linear(num_rows, in_features, features, act, out_type);
     if (st != MOE_OK) return st;
     if (num_rows == 0) return MOE_OK;
     for (const void* p : {x, weights, static_cast<const void*>(out)})
         if (p == nullptr || !aligned16(p)) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(bias) || !aligned16(residual) || !aligned16(pre)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(bias) || !aligned16(residual) || !aligned16(pre) || !aligned16(workspace)) return MOE_ERR_INVALID_ARG;
+    if (workspace == nullptr && linear_workspace(num_rows, in_features, features, act == MOE_ACT_SWIGLU) > 0) return MOE_ERR_INVALID_ARG;
+    if (workspace != nullptr)
+        for (const void* p : {x, weights, bias, residual, static_cast<const void*>(out), static_cast<const void*>(pre)})
+            if (workspace == p) return MOE_ERR_INVALID_ARG;
     if (out == x || out == weights || out == bias || (out == residual && out_type != MOE_OUT_BF16)) return MOE_ERR_INVALID_ARG;
     if (pre != nullptr && (pre == x || pre == weights || pre == bias || pre == residual || pre == out)) return MOE_ERR_INVALID_ARG;
     LinearArgs a = {};
@@ -190,6 +197,7 @@ MOE_API moe_status moe_linear(moe_ctx* ctx, const void* x, int32_t num_rows, con
     a.residual = static_cast<const uint16_t*>(residual);
     a.out = out;
     a.pre = static_cast<uint16_t*>(pre);
+    a.partial = static_cast<float*>(workspace);
     a.T = num_rows;
     a.K = in_features;
     a.F = features;
@@ -199,12 +207,20 @@ MOE_API moe_status moe_linear(moe_ctx* ctx, const void* x, int32_t num_rows, con
     return timed(ctx, s, MOE_KERNEL_LINEAR, [&] { return launch_linear(a, s); });
 }
 
-MOE_API moe_status moe_linear_backward_workspace(int32_t num_rows, int32_t features, int32_t act, int32_t out_type,
-                                                 int32_t with_bias, size_t* bytes) {
-    if (bytes == nullptr || (with_bias != 0 && with_bias != 1)) return MOE_ERR_INVALID_ARG;
-    const moe_status st = check_linear(num_rows, 8, features, act, out_type);
+MOE_API moe_status moe_linear_workspace(int32_t num_rows, int32_t in_features, int32_t features, int32_t act, size_t* bytes) {
+    if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+    const moe_status st = check_linear(num_rows, in_features, features, act, MOE_OUT_BF16);
     if (st != MOE_OK) return st;
-    *bytes = plan_backward(num_rows, features, act, out_type, with_bias != 0).total;
+    *bytes = (size_t)linear_workspace(num_rows, in_features, features, act == MOE_ACT_SWIGLU);
+    return MOE_OK;
+}
+
+MOE_API moe_status moe_linear_backward_workspace(int32_t num_rows, int32_t in_features, int32_t features, int32_t act,
+                                                 int32_t out_type, int32_t with_bias, size_t* bytes) {
+    if (bytes == nullptr || (with_bias != 0 && with_bias != 1)) return MOE_ERR_INVALID_ARG;
+    const moe_status st = check_linear(num_rows, in_features, features, act, out_type);
+    if (st != MOE_OK) return st;
+    *bytes = plan_backward(num_rows, in_features, features, act, out_type, with_bias != 0).total;
     return MOE_OK;
 }
 
@@ -216,7 +232,7 @@ MOE_API moe_status moe_linear_backward(moe_ctx* ctx, const void* grad_out, int32
     const moe_status st = check_linear(num_rows, in_features, features, act, out_type);
     if (st != MOE_OK) return st;
     if ((grad_type != MOE_GRAD_BF16 && grad_type != MOE_GRAD_F32) || (accumulate != 0 && accumulate != 1)) return MOE_ERR_INVALID_ARG;
-    const BackwardPlan plan = plan_backward(num_rows, features, act, out_type, grad_bias != nullptr);
+    const BackwardPlan plan = plan_backward(num_rows, in_features, features, act, out_type, grad_bias != nullptr);
     const bool any = num_rows > 0;
     for (const void* p : {grad_out, x, weights, pre, static_cast<const void*>(grad_x), static_cast<const void*>(grad_weights),
                           static_cast<const void*>(grad_bias), static_cast<const void*>(workspace)})
@@ -240,37 +256,41 @@ MOE_API moe_status moe_linear_backward(moe_ctx* ctx, const void* grad_out, int32
     g.pre = static_cast<const uint16_t*>(pre);
     // (the bias alone does not need it)
     if (plan.own_pre && (grad_x != nullptr || grad_weights != nullptr)) g.grad_pre = static_cast<uint16_t*>(workspace);
-    if (grad_bias != nullptr) g.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.sums);
+    float* sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.sums);
+    if (linear_sum_blocks(num_rows) > 0) g.partial = sums;
     g.grad_bias = grad_bias;
     g.T = num_rows;
     g.F = features;
     g.act = act;
     g.grad_f32 = out_type == MOE_OUT_F32;
     g.accumulate = accumulate;
-    ExpertGemmArgs a = {};   // the products of one matrix whose rows are all of them
-    a.seg.E = 1;
-    a.seg.max_rows = num_rows;
-    a.seg.seg_cap = INT32_MAX;
-    a.seg.err = ctx->err();
-    a.q = plan.own_pre ? static_cast<const void*>(g.grad_pre) : grad_out;
-    a.K = in_features;
-    a.N = M;
+    const void* d = plan.own_pre ? static_cast<const void*>(g.grad_pre) : grad_out;
+    ExpertGemmArgs e = {};   // of one matrix that every row belongs to
+    e.seg.E = 1;
+    e.seg.max_rows = num_rows;
+    e.seg.seg_cap = INT32_MAX;
+    e.seg.err = ctx->err();
+    e.q = d;
+    e.K = in_features;
+    e.N = M;
+    // grad_x [rows, K] over M, or grad_weights [M, K] over the rows
+    auto product = [&](const void* p, void* out, int32_t R, int32_t X, bool weights) {
+        if (linear_bwd_here(R, in_features))
+            return launch_linear_bwd(LinearBwdArgs{p, d, out, sums, R, in_features, X, weights && grad_type == MOE_GRAD_F32, weights && accumulate},
+                                     weights, s);
+        e.p = p;
+        e.out = out;
+        if (!weights) return launch_expert_gemm_bwd_rows(e, num_rows, s);
+        e.out_f32 = grad_type == MOE_GRAD_F32;
+        e.accumulate = accumulate;
+        return launch_expert_gemm_bwd_weights(e, s);
+    };
     return timed(ctx, s, MOE_KERNEL_LINEAR_BWD, [&] {
-        hipError_t e = hipSuccess;
-        if (g.grad_pre != nullptr || grad_bias != nullptr) e = launch_linear_grad(g, s);
-        if (e == hipSuccess && grad_x != nullptr && any) {
-            a.p = weights;
-            a.out = grad_x;
-            e = launch_expert_gemm_bwd_rows(a, num_rows, s);
-        }
-        if (e == hipSuccess && grad_weights != nullptr) {
-            a.p = x;
-            a.out = grad_weights;
-            a.out_f32 = grad_type == MOE_GRAD_F32;
-            a.accumulate = accumulate;
-            e = launch_expert_gemm_bwd_weights(a, s);
-        }
-        return e;
+        hipError_t st = hipSuccess;
+        if (g.grad_pre != nullptr || grad_bias != nullptr) st = launch_linear_grad(g, s);
+        if (st == hipSuccess && grad_x != nullptr && any) st = product(weights, grad_x, num_rows, M, false);
+        if (st == hipSuccess && grad_weights != nullptr) st = product(x, grad_weights, M, num_rows, true);
+        return st;
     });
 }
 

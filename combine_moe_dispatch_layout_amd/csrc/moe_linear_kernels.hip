@@ -4,6 +4,8 @@
 //
 // Products are exact and added in binary32; the epilogue works on those sums in binary32 and
 // rounds once.  A gated activation takes a gate's column and its up column in the same tile.
+#include <type_traits>
+
 #include "moe_ep.h"
 #include "moe_internal.h"
 #include "moe_layer.h"
@@ -25,8 +27,29 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
 }
 
 // ---------------------------------------------------------------- activations
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
-constexpr float kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
+// Exponentials and reciprocals are the hardware's (one step each); an exponent's own rounding is what is left, |v| half
+// steps relative.
+__device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504088896341f); }
+__device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-v)); }
+
+// The normal distribution below v: with y = |v| / sqrt(2), erfc(y) = exp(-y^2) t P(t), t = 1 / (1 + 0.3 y), P a minimax
+// polynomial fitted to erfc(y) exp(y^2) / t (2e-7 off at most, relative, in binary32), so that the lower tail keeps its relative
+// precision and the density comes along.  The library's erfc takes twice as many instructions, and made the gradient of gelu
+// bound by them.
+struct Normal {
+    float below, density;   // density times sqrt(2 pi)
+    __device__ __forceinline__ explicit Normal(float v) {
+        constexpr float p[] = {0.16918741f, 0.17072384f, 0.14828606f, 0.215108f, -0.09503003f, 0.5482136f, -0.5126702f, 0.48573738f, -0.12955607f};
+        density = exp_of(-0.5f * v * v);
+        const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(v), 0.3f * 0.70710678118654752f, 1.0f));
+        float q = p[8];
+#pragma unroll
+        for (int i = 7; i >= 0; --i) q = __builtin_fmaf(q, t, p[i]);
+        const float tail = 0.5f * t * q * density;
+        below = v < 0.0f ? tail : 1.0f - tail;
+    }
+};
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhScale = 0.79788456080286536f, kTanhCubic = 0.044715f;   // gelu_tanh: sqrt(2 / pi), and the cube's factor
 
 // (1 + tanh r(v)) / 2 is the sigmoid of 2 r(v)
@@ -36,7 +59,7 @@ __device__ __forceinline__ float activate(int act, float v) {
     switch (act) {
         case MOE_ACT_RELU: return v < 0.0f ? 0.0f : v;   // NaN stays
         case MOE_ACT_SILU: return v * sigmoid(v);
-        case MOE_ACT_GELU: return 0.5f * v * erfcf(-v * kSqrtHalf);   // 1 + erf without cancellation
+        case MOE_ACT_GELU: return v * Normal(v).below;
         case MOE_ACT_GELU_TANH: return v * tanh_gate(v);
         default: return v;
     }
@@ -49,7 +72,10 @@ __device__ __forceinline__ float slope(int act, float v) {
             const float s = sigmoid(v);
             return s * (1.0f + v * (1.0f - s));
         }
-        case MOE_ACT_GELU: return 0.5f * erfcf(-v * kSqrtHalf) + v * expf(-0.5f * v * v) * kInvSqrt2Pi;
+        case MOE_ACT_GELU: {
+            const Normal n(v);
+            return n.below + v * n.density * kInvSqrt2Pi;
+        }
         case MOE_ACT_GELU_TANH: {
             const float s = tanh_gate(v), bend = s * (1.0f - s);   // 0 where the square below may be infinite
             return bend == 0.0f ? s : s + v * bend * (2.0f * kTanhScale) * (1.0f + 3.0f * kTanhCubic * v * v);
@@ -101,20 +127,51 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int row, int col, fl
     }
 }
 
+// A wavefront's 16 rows of PS subtiles side by side (gated: a gate's and an up's in turn) go through LDS, 1 KB a
+// subtile, so that a lane has eight neighbouring columns of one row.  A row's 16-byte chunk c sits at c ^ row.
+template <int PS, bool GATED>
+__device__ __forceinline__ void leave(const LinearArgs& a, char* mine, const f32x4 (&v)[PS], int row, int last_row, int col, int lane) {
+    constexpr int kRow = PS * 64, kMask = PS * 4 - 1, kChunks = PS * 2 / (GATED ? 2 : 1);   // bytes, 16-byte chunks - 1, eights of outputs
+    const int g = lane >> 4, t = lane & 15;
+    auto at = [&](int r, int c) { return reinterpret_cast<f32x4*>(mine + r * kRow + ((c ^ (r & kMask)) << 4)); };
+#pragma unroll
+    for (int p = 0; p < PS; ++p) *at(t, 4 * p + g) = v[p];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+#pragma unroll
+    for (int k = 0; k < 16 * kChunks; k += 64) {
+        const int r = (k + lane) / kChunks, c = lane % kChunks;
+        const int from = GATED ? (c >> 1) * 8 + (c & 1) * 2 : 2 * c;
+        if (row + r < last_row && col + 8 * c < a.F && r < 16) {
+            const f32x4 lo = *at(r, from), hi = *at(r, from + 1);
+            float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}, u[8];
+            if constexpr (GATED) {
+                const f32x4 ul = *at(r, from + 4), uh = *at(r, from + 5);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    u[i] = ul[i];
+                    u[i + 4] = uh[i];
+                }
+            }
+            finish<GATED>(a, row + r, col + 8 * c, x, u);
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+}
+
 // ---------------------------------------------------------------- operands in registers
 // PS x QS subtiles (gated: half of the PS are gates) for a workgroup whose NW wavefronts share out the contraction: every
 // operand byte of the tile is read once, and nothing is waited for but a wavefront's own loads.  Their sums meet in LDS
 // and are added in the order of the wavefronts.
 template <int PS, int QS, bool GATED, int NW, int AHEAD>
-__global__ __launch_bounds__(64 * NW) void k_linear_split(LinearArgs a) {
+__global__ __launch_bounds__(64 * NW) void k_linear_split(LinearArgs a, int run) {
     constexpr int NP = GATED ? 2 : 1, kCols = PS / NP * 16, kRows = QS * 16;
     __shared__ f32x4 part[NW][PS][QS][64];
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, t = lane & 15;
     const int ni = (a.F + kCols - 1) / kCols, nj = (a.T + kRows - 1) / kRows;
-    const int tile = xcd_tile4((int)blockIdx.x);
-    if (tile >= ni * nj) return;
+    const int64_t tile = xcd_run_tile((int)blockIdx.x, run);
+    if (tile >= (int64_t)ni * nj) return;
     int ti, tj;
-    band_order(tile, nj, ni, &tj, &ti);
+    band_order((int)tile, nj, ni, &tj, &ti);
     const int i0 = ti * kCols, j0 = tj * kRows, rows = min(kRows, a.T - j0);
     Direct<false, PS, QS, NP> d;
     d.ld = a.K * 2;
@@ -165,9 +222,9 @@ struct LoadGated {
     int bytes, kbytes;
     uint32_t voff[2], chunk;
     int lds;
-    __device__ __forceinline__ void init(const void* gate, const void* up, int ld, int valid, int w, int lane) {
-        base[0] = static_cast<const char*>(gate);
-        base[1] = static_cast<const char*>(up);
+    __device__ __forceinline__ void init(const char* gate, const char* up, int ld, int valid, int w, int lane) {
+        base[0] = gate;
+        base[1] = up;
         bytes = valid * ld;
         kbytes = ld;
         chunk = ((lane & 7) ^ (lane >> 3)) * 16;
@@ -213,39 +270,14 @@ __device__ __forceinline__ void wide_tile(const LinearArgs& a, int i0, int j0, i
         B::run(st, lp, lq, none, steps, acc, w, lane);
     }
     lds_barrier();   // the epilogue's LDS was a stage
-    // A wavefront's 16 rows of 64 columns at a time go through LDS, so that a lane has eight neighbouring columns of one
-    // row.  A row's 16-byte chunk c sits at c ^ row.
-    const int wp = w % WP, wq = w / WP, g = lane >> 4, t = lane & 15;
-    char* mine = scratch + w * 4096;
-    auto chunk = [&](int r, int c) { return *reinterpret_cast<const f32x4*>(mine + r * 256 + ((c ^ r) << 4)); };
+    const int wp = w % WP, wq = w / WP;
 #pragma unroll
-    for (int q = 0; q < B::QS; ++q) {
+    for (int q = 0; q < B::QS; ++q)
 #pragma unroll
         for (int p0 = 0; p0 < B::PS; p0 += 4) {
-#pragma unroll
-            for (int p = 0; p < 4; ++p) *reinterpret_cast<f32x4*>(mine + t * 256 + (((4 * p + g) ^ t) << 4)) = acc[p0 + p][q];
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-#pragma unroll
-            for (int k = 0; k < (GATED ? 1 : 2); ++k) {
-                const int r = GATED ? lane >> 2 : k * 8 + (lane >> 3), c = GATED ? lane & 3 : lane & 7;
-                const int at = GATED ? (c >> 1) * 8 + (c & 1) * 2 : 2 * c;
-                const int row = wq * B::QS * 16 + q * 16 + r;
-                const int col = i0 + (wp * B::PS + p0) * (GATED ? 8 : 16) + 8 * c;
-                const f32x4 lo = chunk(r, at), hi = chunk(r, at + 1);
-                float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}, u[8];
-                if constexpr (GATED) {
-                    const f32x4 ul = chunk(r, at + 4), uh = chunk(r, at + 5);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        u[i] = ul[i];
-                        u[i + 4] = uh[i];
-                    }
-                }
-                if (row < rows && col < a.F) finish<GATED>(a, j0 + row, col, v, u);
-            }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+            const f32x4 v[4] = {acc[p0][q], acc[p0 + 1][q], acc[p0 + 2][q], acc[p0 + 3][q]};
+            leave<4, GATED>(a, scratch + w * 4096, v, j0 + wq * B::QS * 16 + q * 16, j0 + rows, i0 + (wp * B::PS + p0) * (GATED ? 8 : 16), lane);
         }
-    }
 }
 
 // 256 rows x 256 columns (gated: 128 of each).
@@ -268,10 +300,168 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_linear(LinearArgs a
     else wide_tile<128, 4, 3, GATED>(a, i0, j0, rows, three, lds, w, lane);
 }
 
+// ---------------------------------------------------------------- small tiles
+// Which tile of which part of the contraction a workgroup takes.
+struct Part {
+    int ti, tj, part;
+    int first, last, past;   // steps
+    __device__ __forceinline__ bool init(int ni, int nj, int steps, int split, int run) {
+        const int64_t at = xcd_run_tile((int)blockIdx.x, run), tiles = (int64_t)ni * nj;
+        if (at >= tiles * split) return false;
+        part = (int)(at / tiles);
+        band_order((int)(at - part * tiles), nj, ni, &tj, &ti);
+        past = steps;
+        first = (int)((int64_t)part * steps / split);
+        last = (int)((int64_t)(part + 1) * steps / split);
+        return true;
+    }
+};
+
+// P matrix rows (gated: half of them gates) x Q rows.
+template <int P, int Q, int WP, int WQ, int AHEAD, bool GATED>
+__global__ __launch_bounds__(64 * WP * WQ) void k_linear_tile(LinearArgs a, int split, int run) {
+    using OpP = typename std::conditional<GATED, StageGated<P, WP * WQ>, StageKC<P, WP * WQ>>::type;
+    using OpQ = StageKC<Q, WP * WQ>;
+    using B = StagedBody<P, Q, WP, WQ, AHEAD, OpP, OpQ>;
+    constexpr int NP = GATED ? 2 : 1, kCols = P / NP;
+    __shared__ __align__(1024) char lds[B::kLds];
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, ld = a.K * 2;
+    Part at;
+    if (!at.init((a.F + kCols - 1) / kCols, (a.T + Q - 1) / Q, (ld + kStepBytes - 1) / kStepBytes, split, run)) return;
+    const int i0 = at.ti * kCols, j0 = at.tj * Q, rows = min(Q, a.T - j0);
+    const char* mat = static_cast<const char*>(a.w) + (int64_t)i0 * ld;
+    OpP lp;
+    OpQ lq;
+    if constexpr (GATED) lp.init(mat, mat + (int64_t)a.F * ld, ld, min(kCols, a.F - i0), w, lane);
+    else lp.init(mat, ld, min(kCols, a.F - i0), w, lane);
+    lq.init(static_cast<const char*>(a.x) + (int64_t)j0 * ld, ld, rows, w, lane);
+    B::run(lds, lp, lq, at.first, at.last, at.past, w, lane);
+    for (int item = threadIdx.x; item < Q * kCols / 8; item += 64 * B::kWaves) {
+        const int r = item / (kCols / 8), c = item % (kCols / 8), col = i0 + 8 * c;
+        if (r >= rows || col >= a.F) continue;
+        const int from = GATED ? (c >> 1) * 8 + (c & 1) * 2 : 2 * c;
+        f32x4 v[NP][2];
+#pragma unroll
+        for (int h = 0; h < NP; ++h) {
+            v[h][0] = B::sum(lds, r, from + 4 * h);
+            v[h][1] = B::sum(lds, r, from + 4 * h + 1);
+        }
+        if (split > 1) {
+            f32x4* to = reinterpret_cast<f32x4*>(a.partial + ((int64_t)at.part * a.T + j0 + r) * (NP * a.F) + col);
+#pragma unroll
+            for (int h = 0; h < NP; ++h) {
+                to[h * (a.F / 4)] = v[h][0];
+                to[h * (a.F / 4) + 1] = v[h][1];
+            }
+        } else {
+            float x[NP][8];
+#pragma unroll
+            for (int h = 0; h < NP; ++h)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[h][i] = v[h][i >> 2][i & 3];
+            finish<GATED>(a, j0 + r, col, x[0], x[NP - 1]);
+        }
+    }
+}
+
+// Eight sums of partial results, added in the order of the parts.
+__device__ __forceinline__ void add_parts(const float* from, int64_t stride, int split, float (&v)[8]) {
+    f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+    for (int s = 0; s < split; ++s) {
+        const f32x4* p = reinterpret_cast<const f32x4*>(from + s * stride);
+        lo += p[0];
+        hi += p[1];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = lo[i];
+        v[i + 4] = hi[i];
+    }
+}
+
+template <bool GATED>
+__global__ __launch_bounds__(256) void k_linear_join(LinearArgs a, int split) {
+    const int64_t eights = a.F / 8, item = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (item >= a.T * eights) return;
+    const int row = (int)(item / eights), col = (int)(item - row * eights) * 8, M = GATED ? 2 * a.F : a.F;
+    const float* from = a.partial + (int64_t)row * M + col;
+    float v[8], u[8];
+    add_parts(from, (int64_t)a.T * M, split, v);
+    if constexpr (GATED) add_parts(from + a.F, (int64_t)a.T * M, split, u);
+    finish<GATED>(a, row, col, v, u);
+}
+
+// ---------------------------------------------------------------- products of the backward pass
+// Eight neighbouring results at element o of the output.
+__device__ __forceinline__ void put8(const LinearBwdArgs& a, int64_t o, float (&v)[8]) {
+    if (a.out_f32) {
+        f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o);
+        f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+        if (a.accumulate) {
+            lo += d[0];
+            hi += d[1];
+        }
+        d[0] = lo;
+        d[1] = hi;
+    } else {
+        u32x4* d = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + o);
+        if (a.accumulate) {
+            float old[8];
+            unpack8(*d, old);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += old[i];
+        }
+        *d = pack8(v);
+    }
+}
+
+// WEIGHTS: the contraction runs over rows of both operands; else along the gradient's rows.
+template <int P, int Q, int WP, int WQ, int AHEAD, bool WEIGHTS>
+__global__ __launch_bounds__(64 * WP * WQ) void k_linear_bwd(LinearBwdArgs a, int split, int run) {
+    using OpP = StageMC<P, WP * WQ>;
+    using OpQ = typename std::conditional<WEIGHTS, StageMC<Q, WP * WQ>, StageKC<Q, WP * WQ>>::type;
+    using B = StagedBody<P, Q, WP, WQ, AHEAD, OpP, OpQ>;
+    __shared__ __align__(1024) char lds[B::kLds];
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    Part at;
+    if (!at.init((a.C + P - 1) / P, (a.R + Q - 1) / Q, (a.X + kStepC - 1) / kStepC, split, run)) return;
+    const int i0 = at.ti * P, j0 = at.tj * Q, rows = min(Q, a.R - j0);
+    OpP lp;
+    OpQ lq;
+    lp.init(a.p, a.C * 2, a.X, i0, w, lane);
+    if constexpr (WEIGHTS) lq.init(a.q, a.R * 2, a.X, j0, w, lane);
+    else lq.init(static_cast<const char*>(a.q) + (int64_t)j0 * a.X * 2, a.X * 2, rows, w, lane);
+    B::run(lds, lp, lq, at.first, at.last, at.past, w, lane);
+    for (int item = threadIdx.x; item < Q * P / 8; item += 64 * B::kWaves) {
+        const int r = item / (P / 8), c = item % (P / 8), col = i0 + 8 * c;
+        if (r >= rows || col >= a.C) continue;
+        const f32x4 lo = B::sum(lds, r, 2 * c), hi = B::sum(lds, r, 2 * c + 1);
+        if (split > 1) {
+            f32x4* to = reinterpret_cast<f32x4*>(a.partial + ((int64_t)at.part * a.R + j0 + r) * a.C + col);
+            to[0] = lo;
+            to[1] = hi;
+        } else {
+            float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            put8(a, (int64_t)(j0 + r) * a.C + col, v);
+        }
+    }
+}
+
+__global__ __launch_bounds__(256) void k_linear_bwd_join(LinearBwdArgs a, int split) {
+    const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x, n = (int64_t)a.R * a.C;
+    if (item * 8 >= n) return;
+    float v[8];
+    add_parts(a.partial + item * 8, n, split, v);
+    put8(a, item * 8, v);
+}
+
 // ---------------------------------------------------------------- gradient before the activation
-// grad_pre = grad act'(pre), and the sums of its columns over a block of rows (of the binary32 values).  A wavefront
-// takes 512 columns of kGradRows rows, eight a lane.
-constexpr int kGradRows = 32, kGradSlice = 512;
+// grad_pre = grad act'(pre), and the sums of its columns (of the binary32 values): a workgroup takes 512 columns, eight a
+// lane, of its wavefronts' share of rows, whose sums meet in LDS.  Bound by memory.
+constexpr int kGradWaves = 16, kGradSlice = 512;
+// Rows of a wavefront: all of a few, so that one workgroup has every row of its columns and writes their sums itself;
+// else 8 (the sums of 128 rows are 1/64 of what a bf16 gradient takes).
+__host__ __device__ inline int grad_rows(int T) { return T <= 8 * kGradWaves ? (T + kGradWaves - 1) / kGradWaves : 8; }
 
 __device__ __forceinline__ void load_grad(const LinearGradArgs& a, int64_t at, float (&d)[8]) {
     if (a.grad_f32) {
@@ -288,107 +478,231 @@ __device__ __forceinline__ void load_grad(const LinearGradArgs& a, int64_t at, f
 }
 
 template <bool GATED>
-__global__ __launch_bounds__(64) void k_linear_grad(LinearGradArgs a) {
-    const int slices = (a.F + kGradSlice - 1) / kGradSlice;
-    const int block = (int)(blockIdx.x / slices), col = (int)(blockIdx.x - (unsigned)block * slices) * kGradSlice + threadIdx.x * 8;
-    if (col >= a.F) return;
-    const int first = block * kGradRows, last = min(a.T, first + kGradRows), M = GATED ? 2 * a.F : a.F;
-    float sum[GATED ? 2 : 1][8] = {};
-    for (int r = first; r < last; ++r) {
-        float d[8], v[8];
-        load_grad(a, (int64_t)r * a.F + col, d);
-        const int64_t at = (int64_t)r * M + col;
-        if constexpr (GATED) {
-            float u[8];
-            unpack8(*reinterpret_cast<const u32x4*>(a.pre + at), v);
-            unpack8(*reinterpret_cast<const u32x4*>(a.pre + at + a.F), u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float s = sigmoid(v[i]);
-                const float dg = d[i] * u[i] * (s * (1.0f + v[i] * (1.0f - s))), du = d[i] * (v[i] * s);
-                v[i] = dg;
-                u[i] = du;
-                sum[0][i] += dg;
-                sum[1][i] += du;
-            }
-            if (a.grad_pre != nullptr) {
-                *reinterpret_cast<u32x4*>(a.grad_pre + at) = pack8(v);
-                *reinterpret_cast<u32x4*>(a.grad_pre + at + a.F) = pack8(u);
-            }
-        } else {
-            if (a.act != MOE_ACT_NONE) {
+__global__ __launch_bounds__(64 * kGradWaves) void k_linear_grad(LinearGradArgs a, int per) {
+    constexpr int NP = GATED ? 2 : 1;
+    __shared__ f32x4 part[kGradWaves][2][64];
+    const int slices = (a.F + kGradSlice - 1) / kGradSlice, w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int block = (int)(blockIdx.x / slices), col = (int)(blockIdx.x - (unsigned)block * slices) * kGradSlice + lane * 8;
+    const int M = NP * a.F;
+    float sum[NP][8] = {};
+    if (col < a.F) {
+        for (int i = 0; i < per; ++i) {
+            const int r = (block * per + i) * kGradWaves + w;
+            if (r >= a.T) break;
+            float d[8], v[8];
+            load_grad(a, (int64_t)r * a.F + col, d);
+            const int64_t at = (int64_t)r * M + col;
+            if constexpr (GATED) {
+                float u[8];
                 unpack8(*reinterpret_cast<const u32x4*>(a.pre + at), v);
+                unpack8(*reinterpret_cast<const u32x4*>(a.pre + at + a.F), u);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) d[i] *= slope(a.act, v[i]);
+                for (int k = 0; k < 8; ++k) {
+                    const float s = sigmoid(v[k]);
+                    const float dg = d[k] * u[k] * (s * (1.0f + v[k] * (1.0f - s))), du = d[k] * (v[k] * s);
+                    v[k] = dg;
+                    u[k] = du;
+                    sum[0][k] += dg;
+                    sum[1][k] += du;
+                }
+                if (a.grad_pre != nullptr) {
+                    *reinterpret_cast<u32x4*>(a.grad_pre + at) = pack8(v);
+                    *reinterpret_cast<u32x4*>(a.grad_pre + at + a.F) = pack8(u);
+                }
+            } else {
+                if (a.act != MOE_ACT_NONE) {
+                    unpack8(*reinterpret_cast<const u32x4*>(a.pre + at), v);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) d[k] *= slope(a.act, v[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[0][k] += d[k];
+                if (a.grad_pre != nullptr) *reinterpret_cast<u32x4*>(a.grad_pre + at) = pack8(d);
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum[0][i] += d[i];
-            if (a.grad_pre != nullptr) *reinterpret_cast<u32x4*>(a.grad_pre + at) = pack8(d);
         }
     }
     if (a.grad_bias == nullptr) return;
 #pragma unroll
-    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-        f32x4* to = reinterpret_cast<f32x4*>(a.partial + (int64_t)block * M + h * a.F + col);
-        to[0] = f32x4{sum[h][0], sum[h][1], sum[h][2], sum[h][3]};
-        to[1] = f32x4{sum[h][4], sum[h][5], sum[h][6], sum[h][7]};
+    for (int h = 0; h < NP; ++h) {
+        if (h > 0) __syncthreads();
+        part[w][0][lane] = f32x4{sum[h][0], sum[h][1], sum[h][2], sum[h][3]};
+        part[w][1][lane] = f32x4{sum[h][4], sum[h][5], sum[h][6], sum[h][7]};
+        __syncthreads();
+        if (w < 2 && col < a.F) {   // each of two wavefronts half of a lane's eight
+            f32x4 v = part[0][w][lane];
+#pragma unroll
+            for (int i = 1; i < kGradWaves; ++i) v += part[i][w][lane];
+            const int64_t at = h * a.F + col + w * 4;
+            if (a.partial != nullptr) {
+                *reinterpret_cast<f32x4*>(a.partial + (int64_t)block * M + at) = v;
+            } else {
+                f32x4* out = reinterpret_cast<f32x4*>(a.grad_bias + at);
+                *out = a.accumulate ? *out + v : v;
+            }
+        }
     }
 }
 
-// The blocks' sums, added in their order (in binary64: a column may have any number of rows).
-__global__ __launch_bounds__(256) void k_linear_bias(const float* partial, int64_t blocks, int M, float* out, int accumulate) {
-    __shared__ double part[4][64];
+// The workgroups' sums, added in their order (in binary64: a column may have any number of rows).
+__global__ __launch_bounds__(1024) void k_linear_bias(const float* partial, int blocks, int M, float* out, int accumulate) {
+    __shared__ double part[16][64];
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, c = (int)blockIdx.x * 64 + lane;
     double sum = 0.0;
     if (c < M)
-        for (int64_t b = w; b < blocks; b += 4) sum += partial[b * M + c];
+        for (int b = w; b < blocks; b += 16) sum += partial[(int64_t)b * M + c];
     part[w][lane] = sum;
     __syncthreads();
     if (w != 0 || c >= M) return;
-    sum = part[0][lane] + part[1][lane] + part[2][lane] + part[3][lane];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) sum += part[i][lane];
     out[c] = (float)(accumulate ? sum + out[c] : sum);
+}
+
+template <bool GATED, int PS, int QS, int NW, int AHEAD>
+hipError_t launch_split(const LinearArgs& a, hipStream_t s) {
+    constexpr int kCols = PS * 16 / (GATED ? 2 : 1), kRows = QS * 16;
+    const int64_t tiles = (int64_t)((a.F + kCols - 1) / kCols) * ((a.T + kRows - 1) / kRows);
+    k_linear_split<PS, QS, GATED, NW, AHEAD><<<dim3((unsigned)xcd_grid(tiles, xcd_run(tiles))), dim3(64 * NW), 0, s>>>(a, xcd_run(tiles));
+    return hipGetLastError();
+}
+
+template <bool GATED, int P, int Q, int WP, int WQ, int AHEAD>
+hipError_t launch_tile(const LinearArgs& a, int split, hipStream_t s) {
+    constexpr int kCols = GATED ? P / 2 : P;
+    const int64_t tiles = (int64_t)((a.F + kCols - 1) / kCols) * ((a.T + Q - 1) / Q) * split;
+    const int run = xcd_run(tiles);
+    k_linear_tile<P, Q, WP, WQ, AHEAD, GATED><<<dim3((unsigned)xcd_grid(tiles, run)), dim3(64 * WP * WQ), 0, s>>>(a, split, run);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || split == 1) return e;
+    k_linear_join<GATED><<<dim3((unsigned)(((int64_t)a.T * (a.F / 8) + 255) / 256)), dim3(256), 0, s>>>(a, split);
+    return hipGetLastError();
+}
+
+template <bool WEIGHTS, int P, int Q, int WP, int WQ, int AHEAD>
+hipError_t launch_bwd(const LinearBwdArgs& a, int split, hipStream_t s) {
+    const int64_t tiles = (int64_t)((a.C + P - 1) / P) * ((a.R + Q - 1) / Q) * split;
+    const int run = xcd_run(tiles);
+    k_linear_bwd<P, Q, WP, WQ, AHEAD, WEIGHTS><<<dim3((unsigned)xcd_grid(tiles, run)), dim3(64 * WP * WQ), 0, s>>>(a, split, run);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || split == 1) return e;
+    k_linear_bwd_join<<<dim3((unsigned)(((int64_t)a.R * a.C / 8 + 255) / 256)), dim3(256), 0, s>>>(a, split);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- which kernel
+// How a product of `rows` x `cols` results over `steps` steps is shared out: tiles of kTileRows x kTileCols, the contraction
+// in `split` parts.  The shortest of what they are expected to take, us: the operands' way from L2, or the latency of a
+// workgroup's steps; and the partial sums' way to memory and back with a second launch.  Measured, cold matrices, us (tile
+// rows x columns / parts; the choice first):
+//   4096 x 7168 -> 256     128 x 128 / 4  31   / 1 90    64 x 64 / 1 38
+//   8192 x 4096 -> 64      32 x 64 / 1    19             64 x 64 / 1 24
+//   1024 x 4096 -> 4096    128 x 128 / 1  44   / 2 54    64 x 64 / 1 67   256 x 256 105
+//   512 x 4096 -> 4096     128 x 128 / 2  32   / 1 41    64 x 64 / 1 37
+//   333 x 1000 -> 2056     64 x 64 / 1    10   / 2 15    128 x 128 / 1 17
+//   64 x 4096 -> 4096      64 x 64 / 4    13   / 1 23    32 x 64 / 2 13.5
+//   32 x 4096 -> 4096      32 x 64 / 4    12   / 1 17    64 x 64 / 4 12
+//   24 x 7168 -> 256       32 x 64 / 8    10   / 2 16
+//   3000 x 4096 -> 4096    256 x 256      104            128 x 128 / 1 111
+//   2048 x 4096 -> 4096    128 x 128 / 1  75             256 x 256 105
+struct Plan {
+    int tile, split;   // kTile128 .., or kWide
+    float us;
+};
+enum { kTile128, kTile64, kTile32, kTiles, kWide };
+constexpr int kTileCols[kTiles] = {128, 64, 64}, kTileRows[kTiles] = {128, 64, 32};
+constexpr float kStepUs[kTiles] = {0.65f, 0.33f, 0.2f}, kL2Us = 1.0f / 12e6f, kPartUs = 8.0f / 5e6f, kJoinUs = 4.0f, kWideUs = 1.6f;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// tiles: how many kinds there are.  cols counts matrix rows (a gated product's are twice its results).
+Plan plan_tiles(int64_t rows, int64_t cols, int64_t steps, int tiles) {
+    Plan best = {kTile64, 1, 1e30f};
+    for (int t = 0; t < tiles; ++t) {
+        const int64_t n = ceil_div(rows, kTileRows[t]) * ceil_div(cols, kTileCols[t]);
+        for (int split = 1; split <= 16 && (split == 1 || steps >= 4 * split); split *= 2) {
+            const float traffic = (float)n * steps * (kTileCols[t] + kTileRows[t]) * kStepBytes * kL2Us;
+            const float latency = (float)ceil_div(steps, split) * ceil_div(n * split, 512) * kStepUs[t];
+            const float us = (traffic > latency ? traffic : latency) + (split > 1 ? kJoinUs + (float)split * rows * cols * kPartUs : 0.0f);
+            if (us < best.us) best = Plan{t, split, us};
+        }
+    }
+    return best;
+}
+
+// Up to 12 rows whose matrix a workgroup for each 16 columns reads well (1 x 7168 -> 4096 13.2, in tiles 15.2; 12 x 4096 -> 4096 10.4
+// and 11.3), or is short (8 x 1024 -> 1024 5.1 and 6.4); not so 4 x 7168 -> 2048 gated (21.6 and 16.1), 8 x 7168 -> 256 (13.4 and
+// 9.7) or 16 x 4096 -> 4096.
+bool few_rows(int64_t T, int64_t K, int64_t F) { return T <= 12 && (F >= 192 * 16 || K <= 1024); }
+
+Plan plan_linear(int64_t T, int64_t K, int64_t M) {
+    const int64_t steps = ceil_div(K * 2, kStepBytes);
+    const Plan p = plan_tiles(T, M, steps, kTiles);
+    const float wide = (float)ceil_div(ceil_div(M, kTileP) * ceil_div(T, 256), 256) * steps * kWideUs;
+    return wide < p.us ? Plan{kWide, 1, wide} : p;
 }
 
 template <bool GATED>
 hipError_t linear(const LinearArgs& a, hipStream_t s) {
-    constexpr int NP = GATED ? 2 : 1;
-    auto split = [&](auto ps, auto qs, auto nw, auto ahead) {
-        constexpr int PS = decltype(ps)::value * NP, QS = decltype(qs)::value, NW = decltype(nw)::value, A = decltype(ahead)::value;
-        const int64_t tiles = (int64_t)((a.F + PS / NP * 16 - 1) / (PS / NP * 16)) * ((a.T + QS * 16 - 1) / (QS * 16));
-        k_linear_split<PS, QS, GATED, NW, A><<<dim3((unsigned)((tiles + 31) / 32 * 32)), dim3(64 * NW), 0, s>>>(a);
-        return hipGetLastError();
-    };
-    using std::integral_constant;
-    const int cols = kTileP / NP;
-    const int64_t wide = (int64_t)((a.F + cols - 1) / cols) * ((a.T + 255) / 256);
-    if (wide < 128) {
-        if (a.T <= 16) return split(integral_constant<int, 1>(), integral_constant<int, 1>(), integral_constant<int, 8>(), integral_constant<int, 4>());
-        return split(integral_constant<int, 4 / NP>(), integral_constant<int, 4>(), integral_constant<int, 8>(), integral_constant<int, 2>());
-    }
-    const int64_t blocks = (wide + 255) / 256 * 256;
+    const int64_t M = GATED ? 2 * (int64_t)a.F : a.F;
+    if (few_rows(a.T, a.K, a.F)) return launch_split<GATED, GATED ? 2 : 1, 1, 4, 8>(a, s);
+    const Plan p = plan_linear(a.T, a.K, M);
+    if (p.tile == kTile128) return launch_tile<GATED, 128, 128, 2, 4, 2>(a, p.split, s);
+    if (p.tile == kTile64) return launch_tile<GATED, 64, 64, 2, 2, 4>(a, p.split, s);
+    if (p.tile == kTile32) return launch_tile<GATED, 64, 32, 2, 2, 4>(a, p.split, s);
+    const int64_t blocks = ceil_div(ceil_div(M, kTileP) * ceil_div(a.T, 256), 256) * 256;
     if (blocks * 64 * kWaves >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
     k_linear<GATED><<<dim3((unsigned)blocks), dim3(64 * kWaves), 0, s>>>(a);
     return hipGetLastError();
+}
+
+template <bool WEIGHTS>
+hipError_t linear_bwd(const LinearBwdArgs& a, hipStream_t s) {
+    const Plan p = plan_tiles(a.R, a.C, ceil_div(a.X, kStepC), kTile32);
+    if (p.tile == kTile128) return launch_bwd<WEIGHTS, 128, 128, 2, 4, 2>(a, p.split, s);
+    return launch_bwd<WEIGHTS, 64, 64, 2, 2, 4>(a, p.split, s);
 }
 
 }  // namespace
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) { return a.act == MOE_ACT_SWIGLU ? linear<true>(a, s) : linear<false>(a, s); }
 
-int64_t linear_sum_blocks(int64_t T, int64_t) { return (T + kGradRows - 1) / kGradRows; }
+int64_t linear_workspace(int64_t T, int64_t K, int64_t F, bool gated) {
+    if (T == 0 || few_rows(T, K, F)) return 0;
+    const int64_t M = gated ? 2 * F : F;
+    const Plan p = plan_linear(T, K, M);
+    return p.split > 1 ? p.split * T * M * 4 : 0;
+}
+
+// Up to 320 tiles of 128 x 128; more fill the chip in the expert products' kernels.  grad_x, us, here and there: 1024 rows, 4096 x
+// 4096, 43 and 66, 519 rows, 5120 -> 1368 24 and 71, 77 rows, 528 -> 256 6.6 and 9.3; grad_W of 256 x 7168 over 4096 rows 32 and 45, of
+// 4096 x 4096 over 1024 44 and 33, over 1 15 and 11, of 5120 x 1368 over 519 19 and 17.
+bool linear_bwd_here(int64_t R, int64_t C) { return ceil_div(R, 128) * ceil_div(C, 128) <= 320; }
+
+int64_t linear_bwd_workspace(int64_t R, int64_t C, int64_t X) {
+    if (!linear_bwd_here(R, C)) return 0;
+    const Plan p = plan_tiles(R, C, ceil_div(X, kStepC), kTile32);
+    return p.split > 1 ? p.split * R * C * 4 : 0;
+}
+
+hipError_t launch_linear_bwd(const LinearBwdArgs& a, bool weights, hipStream_t s) { return weights ? linear_bwd<true>(a, s) : linear_bwd<false>(a, s); }
+
+int64_t linear_sum_blocks(int64_t T) {
+    const int64_t rows = (int64_t)kGradWaves * grad_rows((int)T);
+    return T <= rows ? 0 : (T + rows - 1) / rows;
+}
 
 hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t s) {
     const bool gated = a.act == MOE_ACT_SWIGLU;
-    const int M = gated ? 2 * a.F : a.F;
-    const int64_t rows = linear_sum_blocks(a.T, M), blocks = rows * ((a.F + kGradSlice - 1) / kGradSlice);
-    if (blocks * 64 >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
+    const int M = gated ? 2 * a.F : a.F, per = grad_rows(a.T);
+    const int64_t sums = linear_sum_blocks(a.T), blocks = (a.T > 0 ? sums > 0 ? sums : 1 : 0) * ((a.F + kGradSlice - 1) / kGradSlice);
+    if (blocks * 64 * kGradWaves >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
     if (blocks > 0) {
-        if (gated) k_linear_grad<true><<<dim3((unsigned)blocks), dim3(64), 0, s>>>(a);
-        else k_linear_grad<false><<<dim3((unsigned)blocks), dim3(64), 0, s>>>(a);
+        if (gated) k_linear_grad<true><<<dim3((unsigned)blocks), dim3(64 * kGradWaves), 0, s>>>(a, per);
+        else k_linear_grad<false><<<dim3((unsigned)blocks), dim3(64 * kGradWaves), 0, s>>>(a, per);
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.grad_bias == nullptr) return e;
-    k_linear_bias<<<dim3((unsigned)((M + 63) / 64)), dim3(256), 0, s>>>(a.partial, rows, M, a.grad_bias, a.accumulate);
+    if (e != hipSuccess || a.grad_bias == nullptr || (a.T > 0 && sums == 0)) return e;
+    k_linear_bias<<<dim3((unsigned)((M + 63) / 64)), dim3(1024), 0, s>>>(a.partial, (int)sums, M, a.grad_bias, a.accumulate);
     return hipGetLastError();
 }
 

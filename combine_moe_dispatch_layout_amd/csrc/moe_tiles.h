@@ -56,6 +56,17 @@ __device__ __forceinline__ int64_t xcd_tile(int b) {
 // that share lines of the output.
 __device__ __forceinline__ int xcd_tile4(int b) { return (b & ~31) | ((b & 7) << 2) | ((b >> 3) & 3); }
 
+// The same where the tiles are known on the host: each XCD takes `run` consecutive ones at a time.  What the tiles of an XCD
+// share is read from memory once: 4096 rows of 7168 against 256 columns in tiles of 64 x 64, 8 rows of tiles an XCD, 36 us,
+// 40 with 4 neighbours an XCD.
+constexpr int kMostRun = 32;
+inline int xcd_run(int64_t tiles) { return tiles >= 8 * kMostRun ? kMostRun : (int)((tiles + 7) / 8); }
+inline int64_t xcd_grid(int64_t tiles, int run) { return (tiles + 8 * run - 1) / (8 * run) * (8 * run); }
+__device__ __forceinline__ int64_t xcd_run_tile(int b, int run) {
+    const int i = b >> 3;
+    return (int64_t)(i / run) * (8 * run) + (b & 7) * run + i % run;
+}
+
 // Order of the tiles of one matrix with `nj` row tiles and `ni` column tiles: bands of kBand row
 // tiles, column by column, so that 32 consecutive tiles touch about 4 + 8 panels.
 constexpr int kBand = 4;
@@ -564,6 +575,188 @@ struct Direct {
             }
         }
     }
+};
+
+// ---------------------------------------------------------------- operands through registers into LDS
+// For tiles that are too few, or too small, to hide a step's latency: operands are loaded into registers several steps
+// ahead (each use waits for its own loads alone) and stored to LDS, which holds two steps.  What bounds many of them
+// is the way from L2: about 12 TB/s of operands, 0.75 PFLOP/s in tiles of 128 x 128.  A third step in LDS, so that fragments
+// are read a barrier ahead, made no difference but for fewer workgroups a compute unit.
+
+// R rows of 128 contraction bytes a step for NW wavefronts, in LoadKC's order.
+template <int R, int NW>
+struct StageKC {
+    static constexpr int kN = R / 8 / NW, kBytes = R * kStepBytes;
+    static_assert(kN >= 1 && kN * 8 * NW == R, "");
+    const char* base;
+    int bytes, kbytes;
+    uint32_t voff[kN], chunk, at;
+    __device__ __forceinline__ void init(const void* b, int ld, int valid, int w, int lane) {
+        base = static_cast<const char*>(b);
+        bytes = valid * ld;
+        kbytes = ld;
+        chunk = (lane & 7) * 16;
+        at = w * kN * 1024 + (lane >> 3) * kStepBytes + (((lane & 7) ^ (lane >> 3)) << 4);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) voff[i] = (uint32_t)(((w * kN + i) * 8 + (lane >> 3)) * ld) + chunk;
+    }
+    __device__ __forceinline__ void load(i32x4 (&r)[kN], int step) const {
+        const int from = step * kStepBytes;
+        const auto rsrc = descriptor(base + from, from < kbytes ? bytes - from : 0);
+        const bool in = (int)chunk < kbytes - from;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) r[i] = load16(rsrc, in ? voff[i] : kOob);
+    }
+    __device__ __forceinline__ void store(char* to, const i32x4 (&r)[kN]) const {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) *reinterpret_cast<i32x4*>(to + at + i * 1024) = r[i];
+    }
+    __device__ __forceinline__ static bf16x8 frag(const char* stage, int sub, int half, int lane) {
+        const int row = sub * 16 + (lane & 15);
+        return *reinterpret_cast<const bf16x8*>(stage + (row * kStepBytes + (((half * 4 + (lane >> 4)) ^ (row & 7)) << 4)));
+    }
+};
+
+// The same of R matrix rows whose subtiles of 16 are a gate's and an up's in turn, each from a panel of its own.
+template <int R, int NW>
+struct StageGated {
+    using KC = StageKC<R, NW>;
+    static constexpr int kN = KC::kN, kBytes = KC::kBytes;
+    static_assert(kN == 2 || kN == 4, "");   // a wavefront's first two loads are of one subtile
+    const char* base[2];                     // of its first pair of loads, and of its second
+    int bytes, kbytes;
+    uint32_t voff[2], chunk, at;
+    __device__ __forceinline__ void init(const char* gate, const char* up, int ld, int valid, int w, int lane) {
+        base[0] = kN == 2 && (w & 1) ? up : gate;
+        base[1] = up;
+        bytes = valid * ld;
+        kbytes = ld;
+        chunk = (lane & 7) * 16;
+        at = w * kN * 1024 + (lane >> 3) * kStepBytes + (((lane & 7) ^ (lane >> 3)) << 4);
+        const int row = (kN == 2 ? w >> 1 : w) * 16 + (lane >> 3);
+        voff[0] = (uint32_t)(row * ld) + chunk;
+        voff[1] = (uint32_t)((row + 8) * ld) + chunk;
+    }
+    __device__ __forceinline__ void load(i32x4 (&r)[kN], int step) const {
+        const int from = step * kStepBytes, n = from < kbytes ? bytes - from : 0;
+        const bool in = (int)chunk < kbytes - from;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) r[i] = load16(descriptor(base[i >> 1] + from, n), in ? voff[i & 1] : kOob);
+    }
+    __device__ __forceinline__ void store(char* to, const i32x4 (&r)[kN]) const {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) *reinterpret_cast<i32x4*>(to + at + i * 1024) = r[i];
+    }
+    __device__ __forceinline__ static bf16x8 frag(const char* stage, int sub, int half, int lane) { return KC::frag(stage, sub, half, lane); }
+};
+
+// 64 contraction rows of W columns a step.  Contraction row c's 32-byte unit u (16 columns) sits at u ^ key(c), so that the
+// eight rows that a transposing load's 32 lanes read lie in different banks (rows of 256 bytes all begin in the same, of 128
+// in two).
+template <int W, int NW>
+struct StageMC {
+    static_assert(W == 64 || W == 128, "");
+    static constexpr int kRow = W * 2, kLanes = kRow / 16, kBytes = kStepC * kRow, kN = kBytes / 1024 / NW;
+    static_assert(kN >= 1 && kN * 1024 * NW == kBytes, "");
+    const char* base;
+    int ld, crows, before;   // bytes of a contraction row, contraction rows, bytes of a row before the tile
+    uint32_t voff[kN], at[kN];
+    __device__ __forceinline__ static int key(int c) { return W == 64 ? (c >> 1 & 1) | (c >> 2 & 2) : (c & 3) | (c >> 1 & 4); }
+    __device__ __forceinline__ void init(const void* b, int row_bytes, int n, int col0, int w, int lane) {
+        before = col0 * 2;
+        base = static_cast<const char*>(b) + before;
+        ld = row_bytes;
+        crows = n;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int c = (w * kN + i) * (64 / kLanes) + lane / kLanes, p = lane % kLanes;
+            voff[i] = before + p * 16 < row_bytes ? (uint32_t)(c * row_bytes) + p * 16 : kOob;
+            at[i] = c * kRow + (((p >> 1) ^ key(c)) << 5) + (p & 1) * 16;
+        }
+    }
+    __device__ __forceinline__ void load(i32x4 (&r)[kN], int step) const {
+        const int c0 = step * kStepC;
+        const auto rsrc = descriptor(base + (int64_t)c0 * ld, min(crows - c0, kStepC) * ld - before);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) r[i] = load16(rsrc, voff[i]);
+    }
+    __device__ __forceinline__ void store(char* to, const i32x4 (&r)[kN]) const {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) *reinterpret_cast<i32x4*>(to + at[i]) = r[i];
+    }
+    __device__ __forceinline__ static bf16x8 frag(const char* stage, int sub, int half, int lane) {
+        const int g = lane >> 4, t = lane & 15, c = half * 32 + 8 * g + (t >> 2);
+        const int from = c * kRow + ((sub ^ key(c)) << 5) + (t & 3) * 8;
+        const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(LDS_PTR(bf16x4, const_cast<char*>(stage) + from));
+        const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(LDS_PTR(bf16x4, const_cast<char*>(stage) + (from + 4 * kRow)));
+        return bf16x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    }
+};
+
+// A tile of P x Q outputs by WP x WQ wavefronts, AHEAD steps of loads on their way.
+template <int P, int Q, int WP, int WQ, int AHEAD, class OpP, class OpQ>
+struct StagedBody {
+    static constexpr int kWaves = WP * WQ, PS = P / WP / 16, QS = Q / WQ / 16;
+    static constexpr int kStage = OpP::kBytes + OpQ::kBytes, kSums = P * Q * 4;
+    static constexpr int kLds = 2 * kStage > kSums ? 2 * kStage : kSums;
+    static_assert(PS >= 1 && QS >= 1 && AHEAD % 2 == 0, "");
+
+    // Steps [first, last) of the contraction; afterwards the tile's sums are in LDS.
+    __device__ __forceinline__ static void run(char* lds, const OpP& lp, const OpQ& lq, int first, int last, int past, int w, int lane) {
+        const int wp = w % WP, wq = w / WP;
+        f32x4 acc[PS][QS];
+#pragma unroll
+        for (int p = 0; p < PS; ++p)
+#pragma unroll
+            for (int q = 0; q < QS; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        i32x4 rp[AHEAD][OpP::kN], rq[AHEAD][OpQ::kN];
+        auto fetch = [&](int slot, int step) {   // past the end zeros
+            step = step < last ? step : past;
+            lp.load(rp[slot], step);
+            lq.load(rq[slot], step);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+#pragma unroll
+        for (int s = 0; s < AHEAD; ++s) fetch(s, first + s);
+        lp.store(lds, rp[0]);
+        lq.store(lds + OpP::kBytes, rq[0]);
+        fetch(0, first + AHEAD);
+        lds_barrier();
+        for (int step = first; step < last; step += AHEAD) {   // whole rounds of both buffers and of the registers
+#pragma unroll
+            for (int s = 0; s < AHEAD; ++s) {
+                const char* cur = lds + (s & 1) * kStage;
+                char* nxt = lds + ((s + 1) & 1) * kStage;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    bf16x8 pf[PS], qf[QS];
+#pragma unroll
+                    for (int p = 0; p < PS; ++p) pf[p] = OpP::frag(cur, wp * PS + p, h, lane);
+#pragma unroll
+                    for (int q = 0; q < QS; ++q) qf[q] = OpQ::frag(cur + OpP::kBytes, wq * QS + q, h, lane);
+#pragma unroll
+                    for (int p = 0; p < PS; ++p)
+#pragma unroll
+                        for (int q = 0; q < QS; ++q) acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[p], qf[q], acc[p][q], 0, 0, 0);
+                    if (h == 0) {   // the next step goes into the other buffer, which everyone left at the last barrier
+                        lp.store(nxt, rp[(s + 1) % AHEAD]);
+                        lq.store(nxt + OpP::kBytes, rq[(s + 1) % AHEAD]);
+                        fetch((s + 1) % AHEAD, step + s + 1 + AHEAD);
+                    }
+                }
+                lds_barrier();
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < PS; ++p)
+#pragma unroll
+            for (int q = 0; q < QS; ++q)
+                *reinterpret_cast<f32x4*>(lds + sum_at((wq * QS + q) * 16 + (lane & 15), (wp * PS + p) * 4 + (lane >> 4))) = acc[p][q];
+        lds_barrier();
+    }
+    // Of row j's sums, 16-byte chunk c (of row j's first 16 chunks, c ^ j).
+    __device__ __forceinline__ static int sum_at(int j, int c) { return j * P * 4 + ((c ^ (j & 15)) << 4); }
+    __device__ __forceinline__ static f32x4 sum(const char* lds, int j, int c) { return *reinterpret_cast<const f32x4*>(lds + sum_at(j, c)); }
 };
 
 }  // namespace

@@ -537,12 +537,18 @@ typedef enum moe_out_type {
  *   out        [num_rows, F] of out_type
  *   pre        bf16 [num_rows, M], nullable: receives the sums with their bias, for
  *              moe_linear_backward
+ *   workspace  moe_linear_workspace bytes, 16-byte aligned: partial sums of products whose contraction
+ *              is shared out; may be NULL if that is 0
  * F is `features`, in_features and F multiples of 8, M and in_features at most MOE_MAX_FEATURES, else
  * MOE_ERR_UNSUPPORTED (as are more tiles of 256 x 256 than 2^23 - 256); buffers 16-byte aligned; only residual and out
  * may overlap.  Sums and epilogue are binary32, each output is rounded once, in an order that the sizes decide. */
 moe_status moe_linear(moe_ctx* ctx, const void* x, int32_t num_rows, const void* weights,
                       int32_t in_features, int32_t features, const void* bias, int32_t act,
-                      const void* residual, void* out, int32_t out_type, void* pre, void* stream);
+                      const void* residual, void* out, int32_t out_type, void* pre, void* workspace,
+                      void* stream);
+/* Bytes of its workspace (host; needs no GPU). */
+moe_status moe_linear_workspace(int32_t num_rows, int32_t in_features, int32_t features, int32_t act,
+                                size_t* bytes);
 
 /* Gradients of moe_linear.  With d[r, m] the gradient before the activation (grad_out * act'(pre)):
  *   grad_x[r, c] = sum over m of d[r, m] * W[m, c]        bf16 [num_rows, in_features], nullable
@@ -562,8 +568,9 @@ moe_status moe_linear_backward(moe_ctx* ctx, const void* grad_out, int32_t out_t
                                void* grad_weights, int32_t grad_type, int32_t accumulate,
                                float* grad_bias, void* workspace, void* stream);
 /* Bytes of its workspace (host; needs no GPU). */
-moe_status moe_linear_backward_workspace(int32_t num_rows, int32_t features, int32_t act,
-                                         int32_t out_type, int32_t with_bias, size_t* bytes);
+moe_status moe_linear_backward_workspace(int32_t num_rows, int32_t in_features, int32_t features,
+                                         int32_t act, int32_t out_type, int32_t with_bias,
+                                         size_t* bytes);
 
 /* ---------------------------------------------------------------- a few tokens */
 /* Everything between the router and the layer's output, for decode-sized

@@ -94,6 +94,17 @@ def test_linear(gpu, T, K, N, act):
     ctx.close()
 
 
+# products whose contraction is shared out, in each kind of tile, and tiles of 128 x 128 that are not
+@gpu_only
+@pytest.mark.parametrize("act", [NONE, SILU, SWIGLU])
+@pytest.mark.parametrize("T,K,N", [(24, 7168, 256), (3, 5000, 72), (13, 1032, 264), (64, 4096, 1032), (100, 2056, 520), (520, 4104, 4096), (700, 72, 3000), (2000, 4160, 264)])
+def test_linear_in_parts(gpu, T, K, N, act):
+    ctx = context(gpu)
+    for bias, residual, dtype in ((True, True, torch.bfloat16), (False, False, torch.float32)):
+        check_forward(gpu, ctx, T, K, N, act, bias, residual, dtype)
+    ctx.close()
+
+
 # rows and columns around whole tiles of the large kernel, and lengths of a step's ends
 @gpu_only
 @pytest.mark.parametrize("act", [GELU, SWIGLU])
@@ -184,7 +195,7 @@ def check_backward(moe, ctx, T, K, N, act, grad_dtype, weights_dtype, accumulate
     gx = torch.full((T + 1, K), 7.0, dtype=torch.bfloat16, device="cuda")
     held_w, held_b = randn(g, M, K, dtype=weights_dtype), randn(g, M, dtype=torch.float32)
     gw, gb = held_w.clone(), held_b.clone()
-    ws = torch.full((moe.moe_linear_backward_workspace(T, N, act, grad_dtype, True) + 16,), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((moe.moe_linear_backward_workspace(T, K, N, act, grad_dtype, True) + 16,), 255, dtype=torch.uint8, device="cuda")
     got = moe.moe_linear_backward(ctx, d, x, w, act=act, pre=pre, bias=True, grad_x=gx[:T], grad_weights=gw, grad_bias=gb, accumulate=accumulate, workspace=ws)
     assert got[1] is gw and got[2] is gb and (ws[-16:] == 255).all()
     d64 = d.double()
@@ -232,6 +243,16 @@ def test_backward(gpu, T, K, N, act):
                                                   (torch.float32, torch.float32, False), (torch.bfloat16, torch.float32, True)):
         check_backward(gpu, ctx, T, K, N, act, grad_dtype, weights_dtype, accumulate)
     assert gpu.moe_poll_error(ctx) == (gpu.MOE_OK, 0)
+    ctx.close()
+
+
+@gpu_only
+@pytest.mark.parametrize("act,T,K,N", [(GELU, 100, 72, 8192), (RELU, 4100, 264, 136), (SWIGLU, 520, 1368, 2560), (NONE, 4000, 1024, 1032), (SILU, 1, 4096, 4096), (NONE, 3000, 40, 24)])
+def test_backward_in_parts(gpu, act, T, K, N):
+    ctx = context(gpu)
+    check_backward(gpu, ctx, T, K, N, act, torch.bfloat16, torch.bfloat16, False)
+    check_backward(gpu, ctx, T, K, N, act, torch.float32, torch.float32, True)
+    check_backward(gpu, ctx, T, K, N, act, torch.bfloat16, torch.bfloat16, True)
     ctx.close()
 
 
@@ -330,22 +351,34 @@ def test_null_arguments_rejected():
     import combine_moe_dispatch_layout_amd as moe
     lib, n = moe.load_library(), ctypes.c_size_t(0)
     bad = moe.MOE_ERR_INVALID_ARG
-    assert lib.moe_linear(None, None, 1, None, 8, 8, None, 0, None, None, 0, None, None) == bad
+    assert lib.moe_linear(None, None, 1, None, 8, 8, None, 0, None, None, 0, None, None, None) == bad
     assert lib.moe_linear_backward(None, None, 0, 1, None, None, 8, 8, 0, None, None, None, 0, 0, None, None, None) == bad
-    assert lib.moe_linear_backward_workspace(4, 8, 0, 0, 1, None) == bad
-    for args, status in [((-1, 8, 0, 0, 0), 1), ((4, 0, 0, 0, 0), 1), ((4, 8, 6, 0, 0), 1), ((4, 8, -1, 0, 0), 1), ((4, 8, 0, 2, 0), 1), ((4, 8, 0, 0, 2), 1),
-                         ((4, 12, 0, 0, 0), 2), ((4, 65536, 5, 0, 0), 2), ((4, 65536, 0, 0, 0), 0)]:
+    assert lib.moe_linear_backward_workspace(4, 8, 8, 0, 0, 1, None) == bad
+    assert lib.moe_linear_workspace(4, 8, 8, 0, None) == bad
+    for args, status in [((-1, 8, 8, 0, 0, 0), 1), ((4, 8, 0, 0, 0, 0), 1), ((4, 0, 8, 0, 0, 0), 1), ((4, 8, 8, 6, 0, 0), 1), ((4, 8, 8, -1, 0, 0), 1),
+                         ((4, 8, 8, 0, 2, 0), 1), ((4, 8, 8, 0, 0, 2), 1), ((4, 8, 12, 0, 0, 0), 2), ((4, 12, 8, 0, 0, 0), 2), ((4, 8, 65536, 5, 0, 0), 2),
+                         ((4, 8, 65536, 0, 0, 0), 0)]:
         assert lib.moe_linear_backward_workspace(*args, ctypes.byref(n)) == status, args
+        if args[4:] == (0, 0):
+            assert lib.moe_linear_workspace(*args[:4], ctypes.byref(n)) == status, args
 
 
 def test_workspace_sizes():
     import combine_moe_dispatch_layout_amd as moe
-    assert moe.moe_linear_backward_workspace(100, 64) == 0
-    assert moe.moe_linear_backward_workspace(100, 64, act=GELU) >= 100 * 64 * 2
-    assert moe.moe_linear_backward_workspace(100, 64, act=SWIGLU) >= 100 * 128 * 2
-    assert moe.moe_linear_backward_workspace(100, 64, out_dtype=torch.float32) >= 100 * 64 * 2
-    assert moe.moe_linear_backward_workspace(100, 64, bias=True) >= 64 * 4
-    assert moe.moe_linear_backward_workspace(0, 64, act=GELU, bias=True) == 0
+    back = moe.moe_linear_backward_workspace
+    assert back(100, 64, 64) == 0
+    assert back(100, 64, 64, act=GELU) >= 100 * 64 * 2
+    assert back(100, 64, 64, act=SWIGLU) >= 100 * 128 * 2
+    assert back(100, 64, 64, out_dtype=torch.float32) >= 100 * 64 * 2
+    assert back(1000, 64, 64, bias=True) >= 64 * 4
+    assert back(100, 64, 8192) >= 2 * 100 * 64 * 4   # a long contraction for few results is shared out
+    assert back(0, 64, 64, act=GELU, bias=True) == 0
+    assert moe.moe_linear_workspace(0, 64, 64) == moe.moe_linear_workspace(1, 512, 64) == moe.moe_linear_workspace(8192, 4096, 4096) == 0
+    assert moe.moe_linear_workspace(24, 7168, 256) >= 2 * 24 * 256 * 4
+
+
+def moe_bytes(moe):
+    return moe.moe_linear_workspace(24, 7168, 256)
 
 
 @gpu_only
@@ -377,7 +410,13 @@ def test_refusals(gpu):
            (p(x), p(w), None, None, p(x), 0, None), (p(x), p(w), None, None, p(w), 0, None), (p(x), p(w), None, p(f32), p(f32), 1, None),
            (p(x), p(w), None, None, p(out), 0, p(out)), (p(x), p(w), None, None, p(out), 2, None)]
     for a in bad:
-        assert lib.moe_linear(ctx.handle, a[0], 4, a[1], 16, 24, a[2], 0, a[3], a[4], a[5], a[6], None) == gpu.MOE_ERR_INVALID_ARG, a
+        assert lib.moe_linear(ctx.handle, a[0], 4, a[1], 16, 24, a[2], 0, a[3], a[4], a[5], a[6], None, None) == gpu.MOE_ERR_INVALID_ARG, a
+    lx, lw = torch.zeros(24, 7168, **bf), torch.zeros(256, 7168, **bf)   # a product that needs its workspace
+    lo, ls = torch.zeros(24, 256, **bf), torch.zeros(moe_bytes(gpu), dtype=torch.uint8, device="cuda")
+    long = lambda ws: lib.moe_linear(ctx.handle, p(lx), 24, p(lw), 7168, 256, None, 0, None, p(lo), 0, None, ws, None)
+    assert [long(ws) for ws in (None, p(ls) + 8, p(lx), p(lo))] == [gpu.MOE_ERR_INVALID_ARG] * 4 and long(p(ls)) == gpu.MOE_OK
+    with pytest.raises(ValueError):
+        gpu.moe_linear(ctx, lx, lw, workspace=ls[:-16])
     d = torch.zeros(4, 24, **bf)
     gx, gw, gb = torch.zeros(4, 16, **bf), torch.zeros(24, 16, **bf), torch.zeros(24, device="cuda")
     ws = torch.zeros(4096, dtype=torch.uint8, device="cuda")
