@@ -189,14 +189,23 @@ struct ManyTiles {
 
 __device__ __forceinline__ float silu(float g) { return g * (1.0f / (1.0f + __expf(-g))); }
 
-// One tile against 16 gate columns and the 16 up columns that belong to them.
+// One tile against `cols` times 16 gate columns and the up columns that belong to them, the contraction shared out over the
+// wavefronts.
 template <bool FP8, int NW, int AHEAD>
-__global__ __launch_bounds__(64 * NW) void k_layer_up(LayerArgs a) {
+__global__ __launch_bounds__(64 * NW) void k_layer_up(LayerArgs a, int cols) {
     constexpr int kSize = FP8 ? 1 : 2;
-    __shared__ f32x4 part[NW][2][64];
-    __shared__ Counts counts;
+    using D = Direct<FP8, 2, 2>;
+    union Shared {
+        Counts counts;
+        f32x4 part[2][NW][2][64];
+        __device__ Shared() {}
+    };
+    __shared__ Shared sh;
+    __shared__ __align__(16) char corners[NW][D::kLds];
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int cols = (a.I + 15) / 16, tile = (int)blockIdx.x / cols, i0 = ((int)blockIdx.x - tile * cols) * 16;
+    const int all = (a.I + 15) / 16, runs = (all + cols - 1) / cols, tile = (int)blockIdx.x / runs;
+    int col = ((int)blockIdx.x - tile * runs) * cols;
+    const int last_col = min(col + cols, all);
     Found f;
     if (a.T * a.k <= kFewSlots) {
         FewTiles few;
@@ -205,79 +214,107 @@ __global__ __launch_bounds__(64 * NW) void k_layer_up(LayerArgs a) {
         for (int i = 0; i < tile && f.e >= 0; ++i) f = few.next(lane);
     } else {
         int ex[MOE_LAYER_MAX_ROWS / (64 * NW)], rank[MOE_LAYER_MAX_ROWS / (64 * NW)];
-        counts.init<64 * NW>(a, ex, rank);
-        f = counts.tile(a, tile, lane);
+        sh.counts.template init<64 * NW>(a, ex, rank);
+        f = sh.counts.tile(a, tile, lane);
+        __syncthreads();   // the sums go where the counts are
     }
     const int e = __builtin_amdgcn_readfirstlane(f.e), n = __builtin_amdgcn_readfirstlane(f.n);
     if (e < 0) return;
     const int g = lane >> 4, t = lane & 15;
-    Direct<FP8, 2, 1, 2> d;
+    D d;
+    d.corner = corners[w];
     d.ld = a.H * kSize;
     const char* mat = static_cast<const char*>(a.w1) + (int64_t)e * 2 * a.I * d.ld;
     d.rq = descriptor(a.x, a.T * a.H * 2);
-    d.row[0] = t < n ? (uint32_t)(f.slot / a.k) * (uint32_t)(a.H * 2) : kOob;
+    d.set_rows(n, (uint32_t)(f.slot / a.k) * (uint32_t)(a.H * 2), lane);
+    int done_col = col, side = 0;
+    d.template stream<AHEAD>(
+        [&](int* first, int* stride, int* end) {
+            *first = w;
+            *stride = NW;
+            *end = (d.ld + kStepBytes - 1) / kStepBytes;
+            if (col >= last_col) return false;
+            const int i0 = col++ * 16;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        d.rp[h] = descriptor(mat + (int64_t)(h * a.I + i0) * d.ld, min(16, a.I - i0) * d.ld);
-        if constexpr (FP8)
-            d.rm[h] = descriptor(a.s1 + ((int64_t)e * (2 * a.I / 128) + (h * a.I + i0) / 128) * (a.H / 128), a.H / 128 * 4);
-    }
-    f32x4 acc[2][1];
-    d.template run<AHEAD>(acc, w, NW, (d.ld + kStepBytes - 1) / kStepBytes, lane);
-    part[w][0][lane] = acc[0][0];
-    part[w][1][lane] = acc[1][0];
-    __syncthreads();
-    if (w != 0) return;
-    f32x4 gate = part[0][0][lane], up = part[0][1][lane];
+            for (int h = 0; h < 2; ++h) {
+                d.rp[h] = descriptor(mat + (int64_t)(h * a.I + i0) * d.ld, min(16, a.I - i0) * d.ld);
+                if constexpr (FP8) d.set_scales(h, a.s1 + ((int64_t)e * (2 * a.I / 128) + (h * a.I + i0) / 128) * (a.H / 128));
+            }
+            return true;
+        },
+        [&](const f32x4 (&acc)[2]) {
+            sh.part[side][w][0][lane] = acc[0];
+            sh.part[side][w][1][lane] = acc[1];
+            __syncthreads();   // the next item's go to the other side, so one barrier an item is enough
+            const int i = done_col * 16 + 4 * g;
+            if (done_col % NW == w && t < n && i < a.I) {   // the wavefronts take turns to join
+                f32x4 gate = sh.part[side][0][0][lane], up = sh.part[side][0][1][lane];
 #pragma unroll
-    for (int i = 1; i < NW; ++i) {
-        gate += part[i][0][lane];
-        up += part[i][1][lane];
-    }
-    const int i = i0 + 4 * g;
-    if (t < n && i < a.I) {
-        f32x4 v;
+                for (int j = 1; j < NW; ++j) {
+                    gate += sh.part[side][j][0][lane];
+                    up += sh.part[side][j][1][lane];
+                }
+                f32x4 v;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = silu(gate[r]) * up[r];
-        *reinterpret_cast<u32x2*>(a.act + (int64_t)f.slot * a.I + i) = bf16_pack(v);
-    }
+                for (int r = 0; r < 4; ++r) v[r] = silu(gate[r]) * up[r];
+                *reinterpret_cast<u32x2*>(a.act + (int64_t)f.slot * a.I + i) = bf16_pack(v);
+            }
+            ++done_col;
+            side ^= 1;
+        },
+        lane);
 }
 
 // 16 output columns of every token.  The tiles (times `split` parts of their contraction) go round the
 // wavefronts; what a slot contributes stays in LDS until all are done, and each token adds its own in the order of its slots.
 template <bool FP8, int NW, int AHEAD>
-__global__ __launch_bounds__(64 * NW) void k_layer_down(LayerArgs a) {
+__global__ __launch_bounds__(64 * NW, 4) void k_layer_down(LayerArgs a) {
+    using D = Direct<FP8, 1>;
     constexpr int kSize = FP8 ? 1 : 2, NT = 64 * NW;
     extern __shared__ f32x4 slots[];   // [split][slots][4]
     __shared__ ManyTiles many;
+    __shared__ __align__(16) char corners[NW][D::kLds];
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int P = a.T * a.k, h0 = (int)blockIdx.x * 16, g = lane >> 4, t = lane & 15;
     const bool small = P <= kFewSlots;
     FewTiles few;
     if (small) few.init(a, lane);
     else many.init<NT>(a);
-    Direct<FP8, 1, 1> d;
+    D d;
+    d.corner = corners[w];
     d.ld = a.I * kSize;
     d.rq = descriptor(a.act, P * a.I * 2);
     const int steps = (d.ld + kStepBytes - 1) / kStepBytes;
     Found f = {-1, 0, 0};
-    int have = -1;   // tile that f is
-    for (int item = w;; item += NW) {
-        const int tile = item / a.split, part = item - tile * a.split;
-        if (small) {
-            for (; have < tile && (have < 0 || f.e >= 0); ++have) f = few.next(lane);
-        } else {
-            f = many.at(tile, lane);
-        }
-        const int e = __builtin_amdgcn_readfirstlane(f.e), n = __builtin_amdgcn_readfirstlane(f.n);
-        if (e < 0) break;
-        d.row[0] = t < n ? (uint32_t)f.slot * (uint32_t)(a.I * 2) : kOob;
-        d.rp[0] = descriptor(static_cast<const char*>(a.w2) + ((int64_t)e * a.H + h0) * d.ld, min(16, a.H - h0) * d.ld);
-        if constexpr (FP8) d.rm[0] = descriptor(a.s2 + ((int64_t)e * (a.H / 128) + h0 / 128) * (a.I / 128), a.I / 128 * 4);
-        f32x4 acc[1][1];
-        d.template run<AHEAD>(acc, part * steps / a.split, 1, (part + 1) * steps / a.split, lane);
-        if (t < n) slots[(part * P + f.slot) * 4 + g] = acc[0][0];
-    }
+    int have = -1, item = w;                       // tile that f is; next item
+    int put_n = 0, put_at = 0, next_n = 0, next_at = 0;   // slots of the item whose sums come next, and of the one loaded after it
+    d.template stream<AHEAD>(
+        [&](int* first, int* stride, int* end) {
+            const int tile = item / a.split, part = item - tile * a.split;
+            item += NW;
+            if (small) {
+                for (; have < tile && (have < 0 || f.e >= 0); ++have) f = few.next(lane);
+            } else {
+                f = many.at(tile, lane);
+            }
+            put_n = next_n;
+            put_at = next_at;
+            *first = part * steps / a.split;
+            *stride = 1;
+            *end = (part + 1) * steps / a.split;
+            const int e = __builtin_amdgcn_readfirstlane(f.e), n = __builtin_amdgcn_readfirstlane(f.n);
+            if (e < 0) return false;
+            next_n = n;
+            next_at = (part * P + f.slot) * 4 + g;
+            d.set_rows(n, (uint32_t)f.slot * (uint32_t)(a.I * 2), lane);
+            d.rp[0] = descriptor(static_cast<const char*>(a.w2) + ((int64_t)e * a.H + h0) * d.ld, min(16, a.H - h0) * d.ld);
+            if constexpr (FP8) d.set_scales(0, a.s2 + ((int64_t)e * (a.H / 128) + h0 / 128) * (a.I / 128));
+            return true;
+        },
+        [&](const f32x4 (&acc)[1]) {
+            if (t < put_n) slots[put_at] = acc[0];
+        },
+        lane);
     __syncthreads();
     for (int i = threadIdx.x; i < a.T * 4; i += NT) {
         const int tok = i >> 2, c = i & 3, h = h0 + 4 * c;
@@ -303,17 +340,26 @@ __global__ __launch_bounds__(64 * NW) void k_layer_down(LayerArgs a) {
 
 template <bool FP8>
 hipError_t launch(const LayerArgs& args, hipStream_t s) {
-    constexpr int kUp = 4, kDown = 8;
     LayerArgs a = args;
     const int P = a.T * a.k;
     const int tiles = (P < a.E ? P : a.E) + P / kRows;   // at most
     const int up = (a.I + 15) / 16, down = (a.H + 15) / 16;   // at most 2048 each
-    a.split = 1;
-    while (a.split < kDown && tiles * a.split < kDown) a.split *= 2;
-    k_layer_up<FP8, kUp, FP8 ? 2 : 4><<<dim3((unsigned)(tiles * up)), dim3(64 * kUp), 0, s>>>(a);
+    // Column tiles of a workgroup: enough workgroups for four rounds of four a compute unit, so that finding its slots does not
+    // count (128 tokens x 8 of 256 experts, E4M3: 1.32 ms with 8, 1.51 with one).
+    int cols = 1;
+    while (cols < 16 && (int64_t)tiles * up >= 4096 * cols) cols *= 2;
+    k_layer_up<FP8, 4, FP8 ? 2 : 4><<<dim3((unsigned)(tiles * ((up + cols - 1) / cols))), dim3(256), 0, s>>>(a, cols);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    k_layer_down<FP8, kDown, FP8 ? 4 : 8><<<dim3((unsigned)down), dim3(64 * kDown), (size_t)a.split * P * 64, s>>>(a);
+    // 64 slots take little LDS, so two workgroups of eight wavefronts share a compute unit; the sums of 1024 slots are 64 KB,
+    // and one of sixteen takes it.
+    const bool few = P <= kFewSlots;
+    const int waves = few ? 8 : 16;
+    a.split = 1;   // every wavefront has work
+    while (a.split < waves && tiles * a.split < waves) a.split *= 2;
+    const size_t lds = (size_t)a.split * P * 64;
+    if (few) k_layer_down<FP8, 8, FP8 ? 2 : 4><<<dim3((unsigned)down), dim3(512), lds, s>>>(a);
+    else k_layer_down<FP8, 16, FP8 ? 2 : 4><<<dim3((unsigned)down), dim3(1024), lds, s>>>(a);
     return hipGetLastError();
 }
 

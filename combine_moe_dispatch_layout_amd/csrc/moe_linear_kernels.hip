@@ -158,57 +158,59 @@ __device__ __forceinline__ void leave(const LinearArgs& a, char* mine, const f32
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
 }
 
-// ---------------------------------------------------------------- operands in registers
-// PS x QS subtiles (gated: half of the PS are gates) for a workgroup whose NW wavefronts share out the contraction: every
-// operand byte of the tile is read once, and nothing is waited for but a wavefront's own loads.  Their sums meet in LDS
-// and are added in the order of the wavefronts.
-template <int PS, int QS, bool GATED, int NW, int AHEAD>
-__global__ __launch_bounds__(64 * NW) void k_linear_split(LinearArgs a, int run) {
-    constexpr int NP = GATED ? 2 : 1, kCols = PS / NP * 16, kRows = QS * 16;
-    __shared__ f32x4 part[NW][PS][QS][64];
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, t = lane & 15;
-    const int ni = (a.F + kCols - 1) / kCols, nj = (a.T + kRows - 1) / kRows;
-    const int64_t tile = xcd_run_tile((int)blockIdx.x, run);
-    if (tile >= (int64_t)ni * nj) return;
-    int ti, tj;
-    band_order((int)tile, nj, ni, &tj, &ti);
-    const int i0 = ti * kCols, j0 = tj * kRows, rows = min(kRows, a.T - j0);
-    Direct<false, PS, QS, NP> d;
+// ---------------------------------------------------------------- few rows
+// 16 columns and up to 16 rows for a workgroup whose NW wavefronts share out the contraction: the matrix goes straight into
+// registers, and nothing is waited for but a wavefront's own loads.  Their sums meet in LDS and are added in the order of the
+// wavefronts.
+template <bool GATED, int NW, int AHEAD>
+__global__ __launch_bounds__(64 * NW) void k_linear_few(LinearArgs a) {
+    constexpr int NP = GATED ? 2 : 1;
+    using D = Direct<false, NP, NP>;
+    __shared__ f32x4 part[NW][NP][64];
+    __shared__ __align__(16) char corners[NW][D::kLds];
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i0 = (int)blockIdx.x * 16;
+    D d;
+    d.corner = corners[w];
     d.ld = a.K * 2;
 #pragma unroll
     for (int h = 0; h < NP; ++h)
-        d.rp[h] = descriptor(static_cast<const char*>(a.w) + (int64_t)(h * a.F + i0) * d.ld, min(kCols, a.F - i0) * d.ld);
-    d.rq = descriptor(static_cast<const char*>(a.x) + (int64_t)j0 * d.ld, rows * d.ld);
+        d.rp[h] = descriptor(static_cast<const char*>(a.w) + (int64_t)(h * a.F + i0) * d.ld, min(16, a.F - i0) * d.ld);
+    d.rq = descriptor(a.x, a.T * d.ld);
+    d.set_rows(a.T, (uint32_t)((lane & 15) * d.ld), lane);
+    bool todo = true;
+    d.template stream<AHEAD>(
+        [&](int* first, int* stride, int* end) {
+            *first = w;
+            *stride = NW;
+            *end = (d.ld + kStepBytes - 1) / kStepBytes;
+            const bool more = todo;
+            todo = false;
+            return more;
+        },
+        [&](const f32x4 (&acc)[NP]) {
 #pragma unroll
-    for (int q = 0; q < QS; ++q) d.row[q] = (uint32_t)((q * 16 + t) * d.ld);   // past the last row: past the descriptor
-    f32x4 acc[PS][QS];
-    d.template run<AHEAD>(acc, w, NW, (d.ld + kStepBytes - 1) / kStepBytes, lane);
-#pragma unroll
-    for (int p = 0; p < PS; ++p)
-#pragma unroll
-        for (int q = 0; q < QS; ++q) part[w][p][q][lane] = acc[p][q];
+            for (int p = 0; p < NP; ++p) part[w][p][lane] = acc[p];
+        },
+        lane);
     __syncthreads();
-    for (int item = threadIdx.x; item < kRows * kCols / 8; item += 64 * NW) {
-        const int r = item / (kCols / 8), c = item % (kCols / 8);
-        if (r >= rows || i0 + 8 * c >= a.F) continue;
-        float v[NP][8];
+    const int r = threadIdx.x >> 1, c = threadIdx.x & 1;
+    if (r >= a.T || i0 + 8 * c >= a.F) return;
+    float v[NP][8];
 #pragma unroll
-        for (int h = 0; h < NP; ++h) {
-            const f32x4* from = &part[0][h * (PS / NP) + c / 2][r / 16][(c & 1) * 32 + (r & 15)];
-            f32x4 lo = from[0], hi = from[16];
+    for (int h = 0; h < NP; ++h) {
+        f32x4 lo = part[0][h][c * 32 + r], hi = part[0][h][c * 32 + 16 + r];
 #pragma unroll
-            for (int k = 1; k < NW; ++k) {
-                lo += from[k * PS * QS * 64];
-                hi += from[k * PS * QS * 64 + 16];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[h][i] = lo[i];
-                v[h][i + 4] = hi[i];
-            }
+        for (int k = 1; k < NW; ++k) {
+            lo += part[k][h][c * 32 + r];
+            hi += part[k][h][c * 32 + 16 + r];
         }
-        finish<GATED>(a, j0 + r, i0 + 8 * c, v[0], v[NP - 1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[h][i] = lo[i];
+            v[h][i + 4] = hi[i];
+        }
     }
+    finish<GATED>(a, r, i0 + 8 * c, v[0], v[NP - 1]);
 }
 
 // ---------------------------------------------------------------- large tiles
@@ -558,14 +560,6 @@ __global__ __launch_bounds__(1024) void k_linear_bias(const float* partial, int 
     out[c] = (float)(accumulate ? sum + out[c] : sum);
 }
 
-template <bool GATED, int PS, int QS, int NW, int AHEAD>
-hipError_t launch_split(const LinearArgs& a, hipStream_t s) {
-    constexpr int kCols = PS * 16 / (GATED ? 2 : 1), kRows = QS * 16;
-    const int64_t tiles = (int64_t)((a.F + kCols - 1) / kCols) * ((a.T + kRows - 1) / kRows);
-    k_linear_split<PS, QS, GATED, NW, AHEAD><<<dim3((unsigned)xcd_grid(tiles, xcd_run(tiles))), dim3(64 * NW), 0, s>>>(a, xcd_run(tiles));
-    return hipGetLastError();
-}
-
 template <bool GATED, int P, int Q, int WP, int WQ, int AHEAD>
 hipError_t launch_tile(const LinearArgs& a, int split, hipStream_t s) {
     constexpr int kCols = GATED ? P / 2 : P;
@@ -644,7 +638,10 @@ Plan plan_linear(int64_t T, int64_t K, int64_t M) {
 template <bool GATED>
 hipError_t linear(const LinearArgs& a, hipStream_t s) {
     const int64_t M = GATED ? 2 * (int64_t)a.F : a.F;
-    if (few_rows(a.T, a.K, a.F)) return launch_split<GATED, GATED ? 2 : 1, 1, 4, 8>(a, s);
+    if (few_rows(a.T, a.K, a.F)) {
+        k_linear_few<GATED, 4, 8><<<dim3((unsigned)ceil_div(a.F, 16)), dim3(256), 0, s>>>(a);
+        return hipGetLastError();
+    }
     const Plan p = plan_linear(a.T, a.K, M);
     if (p.tile == kTile128) return launch_tile<GATED, 128, 128, 2, 4, 2>(a, p.split, s);
     if (p.tile == kTile64) return launch_tile<GATED, 64, 64, 2, 2, 4>(a, p.split, s);

@@ -474,49 +474,70 @@ __device__ __forceinline__ float load4(__amdgpu_buffer_rsrc_t rsrc, uint32_t off
     return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rsrc, (int)off, 0, 0));
 }
 
-// ---------------------------------------------------------------- operands straight into registers
-// PS x QS subtiles of 16 x 16 for one wavefront whose operands do not pass through LDS: a step is 128 bytes of
-// each matrix row, in bf16 (64 channels) or E4M3 codes (128, widened to bf16, which holds every code exactly), against as
-// many channels of bf16 rows.  NP panels of the matrix (a gate's and an up's) take PS / NP subtiles each.  E4M3: a
-// step's sums are multiplied by the scale of its 128 x 128 block before they are added.
-template <bool FP8, int PS, int QS, int NP = 1>
+// ---------------------------------------------------------------- matrices straight into registers
+// PS subtiles of 16 matrix rows against up to 16 bf16 rows for one wavefront: a step is 128 bytes of each matrix row, in bf16
+// (64 channels) or E4M3 codes (128, widened to bf16, which holds every code exactly).  NP panels of the matrix (a gate's and
+// an up's) take PS / NP subtiles each.  E4M3: a step's sums are multiplied by the scale of its 128 x 128 block before they are
+// added.
+//
+// What bounds reading a matrix this way is how much a compute unit's vector cache has on its way: some 700 requests of 64
+// bytes, those that hit or read nothing among them.  So the rows, of which there are few, are not read as the matrix
+// instruction wants them (four or two loads for 16 rows, whether they are there or not): a load brings the step of four
+// (bf16: eight) rows, and a wavefront's corner of LDS, which no one else uses and nobody waits for, turns it into fragments.
+template <bool FP8, int PS, int NP = 1>
 struct Direct {
     static_assert(PS % NP == 0, "");
     static constexpr int kPer = PS / NP;
-    static constexpr int kQ = FP8 ? 4 : 2;   // 16-byte loads of a row a lane and step
+    static constexpr int kRowBytes = FP8 ? 256 : 128, kGroup = 1024 / kRowBytes, kGroups = 16 / kGroup;   // a row's step; rows of a load, loads
+    static constexpr int kLds = 16 * kRowBytes;   // bytes of a wavefront's corner
     struct Step {
-        i32x4 p[PS][2], q[QS][kQ];
+        i32x4 p[PS][2], q[kGroups];
         float m[NP];
     };
-    __amdgpu_buffer_rsrc_t rp[NP], rq, rm[NP];
-    uint32_t row[QS];   // byte offset of the lane's row of each subtile, kOob for none
-    int ld;             // bytes of a matrix row
+    __amdgpu_buffer_rsrc_t rp[NP], rq;
+    // E4M3: the panels' scales, one a step, in scalar loads (as vector loads they took a tenth of the time)
+    const __attribute__((address_space(4))) float* scales[NP];
+    uint32_t row[kGroups];   // byte offset of the rows that the lane loads, with its place in them
+    int groups;              // loads that the rows take
+    int ld;                  // bytes of a matrix row
+    char* corner;
 
+    // n rows; from: byte offset of row lane & 15, anything from n on.
+    __device__ __forceinline__ void set_rows(int n, uint32_t from, int lane) {
+        groups = (n + kGroup - 1) / kGroup;
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+            const int r = j * kGroup + lane * 16 / kRowBytes;
+            const uint32_t of = __shfl(from, r, 64);
+            row[j] = r < n ? of + lane * 16 % kRowBytes : kOob;
+        }
+    }
+    __device__ __forceinline__ void set_scales(int panel, const float* of) {
+        scales[panel] = (const __attribute__((address_space(4))) float*)of;
+    }
     // Past the end of a row a step's lanes load zeros, for both operands.
     __device__ __forceinline__ void load(Step& x, int step, int lane) const {
         const int g = lane >> 4, t = lane & 15;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int at = step * kStepBytes + g * 16 + c * 64;
-            const bool in = at < ld;
-            const uint32_t off = in ? (uint32_t)(t * ld + at) : kOob;
+            const uint32_t off = at < ld ? (uint32_t)(t * ld + at) : kOob;
 #pragma unroll
             for (int p = 0; p < PS; ++p) x.p[p][c] = load16(rp[p / kPer], off + (uint32_t)(p % kPer * 16 * ld));
-#pragma unroll
-            for (int q = 0; q < QS; ++q) {
-                const uint32_t from = in ? row[q] + (FP8 ? 2 * at : at) : kOob;
-                if constexpr (FP8) {
-                    x.q[q][2 * c] = load16(rq, from);
-                    x.q[q][2 * c + 1] = load16(rq, from + 16);
-                } else {
-                    x.q[q][c] = load16(rq, from);
-                }
-            }
         }
         if constexpr (FP8) {
 #pragma unroll
-            for (int n = 0; n < NP; ++n) x.m[n] = load4(rm[n], (uint32_t)step * 4);
+            for (int n = 0; n < NP; ++n) x.m[n] = scales[n][min(step, ld / kStepBytes - 1)];
         }
+        const int at = step * kRowBytes;
+        const bool in = at + lane * 16 % kRowBytes < (FP8 ? 2 * ld : ld);
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j)
+            if (j == 0 || j < groups) x.q[j] = load16(rq, in ? row[j] + at : kOob);
+    }
+    // Row r's 16-byte chunk c sits at c ^ r of the row's.
+    __device__ __forceinline__ char* place(int r, int c) const {
+        return corner + r * kRowBytes + (((c ^ r) & (kRowBytes / 16 - 1)) << 4);
     }
     // eight E4M3 codes as bf16
     __device__ __forceinline__ static bf16x8 widen(int lo, int hi) {
@@ -525,54 +546,68 @@ struct Direct {
         const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
         return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
     }
-    __device__ __forceinline__ static void multiply(const Step& x, f32x4 (&acc)[PS][QS]) {
+    __device__ __forceinline__ void multiply(const Step& x, f32x4 (&acc)[PS], int loaded, int lane) const {
+        constexpr int kFrags = FP8 ? 4 : 2;
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j)
+            if (j == 0 || j < loaded) *reinterpret_cast<i32x4*>(place(j * kGroup + lane * 16 / kRowBytes, lane & (kRowBytes / 16 - 1))) = x.q[j];
+        const int g = lane >> 4, t = lane & 15;
+        bf16x8 q[kFrags];   // of rows that are not there, whatever the corner holds: their sums are not used
+#pragma unroll
+        for (int i = 0; i < kFrags; ++i)
+            q[i] = *reinterpret_cast<const bf16x8*>(place(t, FP8 ? 2 * g + (i >> 1) * 8 + (i & 1) : g + 4 * i));
 #pragma unroll
         for (int p = 0; p < PS; ++p) {
             if constexpr (FP8) {
-                bf16x8 f[4];
+                f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = widen(x.p[p][i / 2][i % 2 * 2], x.p[p][i / 2][i % 2 * 2 + 1]);
+                for (int i = 0; i < 4; ++i)
+                    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(x.p[p][i / 2][i % 2 * 2], x.p[p][i / 2][i % 2 * 2 + 1]), q[i], d, 0, 0, 0);
 #pragma unroll
-                for (int q = 0; q < QS; ++q) {
-                    f32x4 d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[i], __builtin_bit_cast(bf16x8, x.q[q][i]), d, 0, 0, 0);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[p][q][r] = __builtin_fmaf(d[r], x.m[p / kPer], acc[p][q][r]);
-                }
+                for (int r = 0; r < 4; ++r) acc[p][r] = __builtin_fmaf(d[r], x.m[p / kPer], acc[p][r]);
             } else {
 #pragma unroll
-                for (int q = 0; q < QS; ++q)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x.p[p][c]),
-                                                                           __builtin_bit_cast(bf16x8, x.q[q][c]), acc[p][q], 0, 0, 0);
+                for (int c = 0; c < 2; ++c)
+                    acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x.p[p][c]), q[c], acc[p], 0, 0, 0);
             }
         }
     }
-    // Steps first, first + stride, .. below end, AHEAD of them on their way.  The loads stay in this order (the
-    // scheduler is fenced off), so that a use waits for its own only.
-    template <int AHEAD>
-    __device__ __forceinline__ void run(f32x4 (&acc)[PS][QS], int first, int stride, int end, int lane) const {
-#pragma unroll
-        for (int p = 0; p < PS; ++p)
-#pragma unroll
-            for (int q = 0; q < QS; ++q) acc[p][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const int past = (ld + kStepBytes - 1) / kStepBytes;   // a step that loads nothing
-        auto clip = [&](int s) { return s < end ? s : past; };
+    // One item after another, the next one's loads behind the last of this one's, so that nothing runs dry between
+    // them, AHEAD steps on their way; the loads stay in order (the scheduler is fenced off), so that a use waits for its own
+    // only.  next(first, stride, end) points this at the next item (descriptors, rows) and says which steps; false: there is
+    // none.  done(acc) gets the sums of the item before.
+    template <int AHEAD, class Next, class Done>
+    __device__ __forceinline__ void stream(Next next, Done done, int lane) {
+        int first, stride, end;
+        bool more = next(&first, &stride, &end);
+        if (!more) return;
+        const int past = (ld + kStepBytes - 1) / kStepBytes;
         Step ring[AHEAD];
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-            load(ring[u], clip(first + u * stride), lane);
+        auto fetch = [&](int u, int step) {
+            load(ring[u], step < end ? step : past, lane);
             __builtin_amdgcn_sched_barrier(0);
-        }
-        for (int s = first; s < end; s += AHEAD * stride) {
+        };
 #pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                multiply(ring[u], acc);
-                load(ring[u], clip(s + (AHEAD + u) * stride), lane);
-                __builtin_amdgcn_sched_barrier(0);
+        for (int u = 0; u < AHEAD; ++u) fetch(u, first + u * stride);
+        while (more) {
+            f32x4 acc[PS];
+#pragma unroll
+            for (int p = 0; p < PS; ++p) acc[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+            const int loaded = groups;   // of this item; next() sets the following one's
+            for (bool last = false; !last;) {
+                first += AHEAD * stride;
+                last = first >= end;
+                if (last) {
+                    more = next(&first, &stride, &end);
+                    if (!more) end = first;   // nothing
+                }
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u) {
+                    multiply(ring[u], acc, loaded, lane);
+                    fetch(u, first + u * stride);
+                }
             }
+            done(acc);
         }
     }
 };
