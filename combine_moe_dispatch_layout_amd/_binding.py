@@ -706,8 +706,7 @@ def moe_swiglu_backward(ctx, grad_out, gate_up, handle, grad_gate_up=None, order
         grad_gate_up = _expert_out(ctx, 2 * features, torch.bfloat16, order)
     po = _expert_rows(ctx, grad_gate_up, torch.bfloat16, 2 * features, order, "grad_gate_up")
     _check(load_library().moe_swiglu_backward(ctx.handle, pd, pg, features, order, ctypes.byref(handle.c), po, _stream()),
-           "moe_swiglu_backward", "moe_route", "moe_route_backward", "moe_linear", "moe_linear_backward",
-           "moe_linear_workspace", "moe_linear_backward_workspace", "moe_layer", "moe_layer_fp8")
+           "moe_swiglu_backward")
     return grad_gate_up
 
 
