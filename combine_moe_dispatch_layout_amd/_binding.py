@@ -711,10 +711,12 @@ def moe_swiglu_backward(ctx, grad_out, gate_up, handle, grad_gate_up=None, order
 
 
 # ---------------------------------------------------------------- around the experts
-def _arg(ctx, t, dtype, shape, name):
-    """Pointer of a contiguous tensor of this dtype and shape on the context's device."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == ctx.device:
-        return t.data_ptr()
+# These calls are made per layer and token, and some of their kernels take a few microseconds: what is right passes one
+# test per tensor, sizes are read once, and outputs that a call makes itself are not looked at again.
+_BF16, _F32, _I64 = torch.bfloat16, torch.float32, torch.int64
+
+
+def _bad(ctx, t, dtype, shape, name):
     if not (t.is_cuda and t.dtype is dtype and t.is_contiguous()):
         raise TypeError("%s must be a contiguous %s CUDA tensor" % (name, dtype))
     if t.get_device() != ctx.device:
@@ -722,17 +724,34 @@ def _arg(ctx, t, dtype, shape, name):
     raise ValueError("%s must be %s, is %s" % (name, tuple(shape), tuple(t.shape)))
 
 
-def _empty(ctx, shape, dtype):
-    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", ctx.device))
+def _arg(ctx, t, dtype, shape, name):
+    """Pointer of a contiguous tensor of this dtype and shape on the context's device."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == ctx.device:
+        return t.data_ptr()
+    _bad(ctx, t, dtype, shape, name)
 
 
-def _workspace(ctx, t, nbytes):
-    """Pointer of at least nbytes bytes (the tensor that a call made for itself may go when it returns: its memory is
-    used again in the order of the stream), and the tensor."""
+def _opt(ctx, t, dtype, shape, name):
+    """The same of a tensor that may be left out."""
+    return None if t is None else _arg(ctx, t, dtype, shape, name)
+
+
+def _layer_sizes(ctx):
+    """Experts, hidden, slots and the device, as Python has them (fixed per context, so cached)."""
+    sizes = ctx.__dict__.get("_sizes")
+    if sizes is None:
+        c = ctx.cfg
+        sizes = ctx.__dict__["_sizes"] = (c.num_experts, c.hidden, c.topk, torch.device("cuda", ctx.device))
+    return sizes
+
+
+def _workspace(ctx, like, t, nbytes):
+    """Pointer of at least nbytes bytes, and the tensor that holds them (one that a call made for itself may go when the call
+    returns: its memory is used again in the order of the stream)."""
     if nbytes == 0:
         return None, None
     if t is None:
-        t = _empty(ctx, nbytes, torch.uint8)
+        t = like.new_empty((nbytes + 1) // 2)   # `like` is bf16
     elif not (t.is_cuda and t.is_contiguous() and t.get_device() == ctx.device):
         raise TypeError("workspace must be a contiguous CUDA tensor on cuda:%d" % ctx.device)
     elif t.numel() * t.element_size() < nbytes:
@@ -740,20 +759,34 @@ def _workspace(ctx, t, nbytes):
     return t.data_ptr(), t
 
 
-def _logits(ctx, t):
-    """Pointer, type and row stride of a router's logits [T, E]."""
-    kind = {torch.float32: MOE_LOGIT_F32, torch.bfloat16: MOE_LOGIT_BF16}.get(t.dtype)
+_LOGIT_TYPES = {torch.float32: MOE_LOGIT_F32, torch.bfloat16: MOE_LOGIT_BF16}
+
+
+def _logits(ctx, t, E):
+    """Tokens, pointer, type and row stride of a router's logits [T, E]."""
+    kind = _LOGIT_TYPES.get(t.dtype)
     if kind is None or not t.is_cuda:
         raise TypeError("logits must be a float32 or bfloat16 CUDA tensor")
     if t.get_device() != ctx.device:
         raise ValueError("logits is on %s, the context on cuda:%d" % (t.device, ctx.device))
-    E = ctx.cfg.num_experts
-    if t.dim() != 2 or t.shape[1] != E or (E > 1 and t.stride(1) != 1):
-        raise ValueError("logits must be [T, %d], its rows contiguous" % E)
-    stride = t.stride(0) if t.shape[0] > 1 else E
-    if stride < E:
-        raise ValueError("rows of logits overlap")
-    return t.data_ptr(), kind, stride
+    shape = t.shape
+    if len(shape) == 2 and shape[1] == E:
+        if t.is_contiguous():
+            return shape[0], t.data_ptr(), kind, E
+        stride, columns = t.stride()
+        if E == 1 or columns == 1:
+            if shape[0] <= 1:
+                stride = E
+            if stride < E:
+                raise ValueError("rows of logits overlap")
+            return shape[0], t.data_ptr(), kind, stride
+    raise ValueError("logits must be [T, %d], its rows contiguous" % E)
+
+
+@functools.lru_cache(maxsize=256)
+def _router(score, groups, topk_groups, group_top, normalize, scale):
+    r = moe_router(score, groups, topk_groups, group_top, int(bool(normalize)), scale)
+    return r, ctypes.byref(r)
 
 
 def moe_route(ctx, logits, score=MOE_SCORE_SOFTMAX, bias=None, groups=1, topk_groups=1, group_top=1, normalize=True, scale=1.0,
@@ -761,31 +794,39 @@ def moe_route(ctx, logits, score=MOE_SCORE_SOFTMAX, bias=None, groups=1, topk_gr
     """The k experts of each token and their weights, from logits fp32 or bf16 [T, E] (any row stride): returns
     (topk_idx int64 [T, k], topk_weights fp32 [T, k]).  bias (fp32 [E]) is added to the scores for the choice alone; of
     `groups` groups of neighbouring experts the topk_groups with the largest sums of their group_top best scores stay."""
-    p, kind, stride = _logits(ctx, logits)
-    T, k = logits.shape[0], ctx.cfg.topk
-    pb = _arg(ctx, bias, torch.float32, (ctx.cfg.num_experts,), "bias") if bias is not None else None
+    E, _, k, device = _layer_sizes(ctx)
+    T, p, kind, stride = _logits(ctx, logits, E)
     if topk_idx is None:
-        topk_idx = _empty(ctx, (T, k), torch.int64)
+        topk_idx = torch.empty((T, k), dtype=_I64, device=device)
+        pi = topk_idx.data_ptr()
+    else:
+        pi = _arg(ctx, topk_idx, _I64, (T, k), "topk_idx")
     if topk_weights is None:
-        topk_weights = _empty(ctx, (T, k), torch.float32)
-    router = moe_router(score, groups, topk_groups, group_top, int(bool(normalize)), scale)
-    _check(load_library().moe_route(ctx.handle, p, kind, stride, T, ctypes.byref(router), pb,
-                                    _arg(ctx, topk_idx, torch.int64, (T, k), "topk_idx"),
-                                    _arg(ctx, topk_weights, torch.float32, (T, k), "topk_weights"), _stream()), "moe_route")
+        topk_weights = torch.empty((T, k), dtype=_F32, device=device)
+        pw = topk_weights.data_ptr()
+    else:
+        pw = _arg(ctx, topk_weights, _F32, (T, k), "topk_weights")
+    st = load_library().moe_route(ctx.handle, p, kind, stride, T, _router(score, groups, topk_groups, group_top, normalize, scale)[1],
+                                  _opt(ctx, bias, _F32, (E,), "bias"), pi, pw, _stream())
+    if st != MOE_OK:
+        raise MoeError(st, "moe_route")
     return topk_idx, topk_weights
 
 
 def moe_route_backward(ctx, grad_weights, logits, topk_idx, score=MOE_SCORE_SOFTMAX, normalize=True, scale=1.0, grad_logits=None):
     """Gradient of moe_route's weights for the logits: fp32 [T, E].  score, normalize and scale as they were there."""
-    p, kind, stride = _logits(ctx, logits)
-    T, E, k = logits.shape[0], ctx.cfg.num_experts, ctx.cfg.topk
+    E, _, k, device = _layer_sizes(ctx)
+    T, p, kind, stride = _logits(ctx, logits, E)
     if grad_logits is None:
-        grad_logits = _empty(ctx, (T, E), torch.float32)
-    router = moe_router(score, 1, 1, 1, int(bool(normalize)), scale)
-    _check(load_library().moe_route_backward(ctx.handle, _arg(ctx, grad_weights, torch.float32, (T, k), "grad_weights"), p, kind,
-                                             stride, _arg(ctx, topk_idx, torch.int64, (T, k), "topk_idx"), T, ctypes.byref(router),
-                                             _arg(ctx, grad_logits, torch.float32, (T, E), "grad_logits"), _stream()),
-           "moe_route_backward")
+        grad_logits = torch.empty((T, E), dtype=_F32, device=device)
+        pg = grad_logits.data_ptr()
+    else:
+        pg = _arg(ctx, grad_logits, _F32, (T, E), "grad_logits")
+    st = load_library().moe_route_backward(ctx.handle, _arg(ctx, grad_weights, _F32, (T, k), "grad_weights"), p, kind, stride,
+                                           _arg(ctx, topk_idx, _I64, (T, k), "topk_idx"), T,
+                                           _router(score, 1, 1, 1, normalize, scale)[1], pg, _stream())
+    if st != MOE_OK:
+        raise MoeError(st, "moe_route_backward")
     return grad_logits
 
 
@@ -794,12 +835,15 @@ _OUT_TYPES = {torch.bfloat16: MOE_OUT_BF16, torch.float32: MOE_OUT_F32}
 
 def _linear_sizes(x, weights, act):
     """Rows, in_features, features and the matrix's rows."""
-    if x.dim() != 2 or weights.dim() != 2:
+    xs, ws = x.shape, weights.shape
+    if len(xs) != 2 or len(ws) != 2:
         raise ValueError("x must be [T, in_features] and weights [M, in_features]")
-    M, K = weights.shape
-    if act == MOE_ACT_SWIGLU and M % 2:
+    M, K = ws
+    if act != MOE_ACT_SWIGLU:
+        return xs[0], K, M, M
+    if M % 2:
         raise ValueError("weights of a gated product have 2 * features rows")
-    return x.shape[0], K, M // 2 if act == MOE_ACT_SWIGLU else M, M
+    return xs[0], K, M // 2, M
 
 
 @functools.lru_cache(maxsize=4096)
@@ -816,18 +860,24 @@ def moe_linear(ctx, x, weights, bias=None, act=MOE_ACT_NONE, residual=None, out=
     [T, F], bf16 or fp32 (out's dtype, or out_dtype), F = M, or M / 2 for MOE_ACT_SWIGLU.  pre: bf16 [T, M], receives
     what moe_linear_backward needs.  workspace: moe_linear_workspace bytes."""
     T, K, F, M = _linear_sizes(x, weights, act)
+    px, pw = _arg(ctx, x, _BF16, (T, K), "x"), _arg(ctx, weights, _BF16, (M, K), "weights")
     if out is None:
-        out = _empty(ctx, (T, F), out_dtype)
-    kind = _OUT_TYPES.get(out.dtype)
-    if kind is None:
-        raise TypeError("out must be bfloat16 or float32")
-    bf16 = torch.bfloat16
-    ps, workspace = _workspace(ctx, workspace, moe_linear_workspace(T, K, F, act))
-    _check(load_library().moe_linear(
-        ctx.handle, _arg(ctx, x, bf16, (T, K), "x"), T, _arg(ctx, weights, bf16, (M, K), "weights"), K, F,
-        _arg(ctx, bias, bf16, (M,), "bias") if bias is not None else None, act,
-        _arg(ctx, residual, bf16, (T, F), "residual") if residual is not None else None, _arg(ctx, out, out.dtype, (T, F), "out"),
-        kind, _arg(ctx, pre, bf16, (T, M), "pre") if pre is not None else None, ps, _stream()), "moe_linear")
+        kind = _OUT_TYPES.get(out_dtype)
+        if kind is None:
+            raise TypeError("out must be bfloat16 or float32")
+        out = x.new_empty((T, F)) if kind == MOE_OUT_BF16 else x.new_empty((T, F), dtype=_F32)
+        po = out.data_ptr()
+    else:
+        kind = _OUT_TYPES.get(out.dtype)
+        if kind is None:
+            raise TypeError("out must be bfloat16 or float32")
+        po = _arg(ctx, out, out.dtype, (T, F), "out")
+    ps, workspace = _workspace(ctx, x, workspace, moe_linear_workspace(T, K, F, act))
+    st = load_library().moe_linear(ctx.handle, px, T, pw, K, F, _opt(ctx, bias, _BF16, (M,), "bias"), act,
+                                   _opt(ctx, residual, _BF16, (T, F), "residual"), po, kind, _opt(ctx, pre, _BF16, (T, M), "pre"),
+                                   ps, _stream())
+    if st != MOE_OK:
+        raise MoeError(st, "moe_linear")
     return out
 
 
@@ -844,68 +894,91 @@ def moe_linear_backward(ctx, grad_out, x, weights, act=MOE_ACT_NONE, pre=None, b
                         grad_x=None, grad_weights=None, grad_bias=None, accumulate=False, workspace=None):
     """Gradients of moe_linear: returns (grad_x bf16 [T, K], grad_weights [M, K] bf16 or fp32 as given, grad_bias fp32
     [M]).  grad_out: bf16 or fp32 [T, F]; pre: as moe_linear left it.  grad_bias is None unless bias is true or it is
-    given; need_x and need_weights leave out the others.  accumulate: add to grad_weights and grad_bias."""
+    given; need_x and need_weights leave out the others.  accumulate: add to grad_weights and grad_bias.  workspace:
+    moe_linear_backward_workspace bytes."""
     T, K, F, M = _linear_sizes(x, weights, act)
-    kind = _OUT_TYPES.get(grad_out.dtype)
+    dtype = grad_out.dtype
+    kind = _OUT_TYPES.get(dtype)
     if kind is None:
         raise TypeError("grad_out must be bfloat16 or float32")
     if accumulate and ((need_weights and grad_weights is None) or (bias and grad_bias is None)):
         raise ValueError("accumulate needs grad_weights and grad_bias")
-    bf16, f32 = torch.bfloat16, torch.float32
-    if grad_x is None and need_x:
-        grad_x = _empty(ctx, (T, K), bf16)
-    if grad_weights is None and need_weights:
-        grad_weights = _empty(ctx, (M, K), bf16)
-    if grad_bias is None and bias:
-        grad_bias = _empty(ctx, (M,), f32)
-    if grad_weights is not None and grad_weights.dtype is not bf16 and grad_weights.dtype is not f32:
-        raise TypeError("grad_weights must be bfloat16 or float32")
-    pw, workspace = _workspace(ctx, workspace, moe_linear_backward_workspace(T, K, F, act, grad_out.dtype, grad_bias is not None))
-    _check(load_library().moe_linear_backward(
-        ctx.handle, _arg(ctx, grad_out, grad_out.dtype, (T, F), "grad_out"), kind, T, _arg(ctx, x, bf16, (T, K), "x"),
-        _arg(ctx, weights, bf16, (M, K), "weights"), K, F, act,
-        _arg(ctx, pre, bf16, (T, M), "pre") if pre is not None else None,
-        _arg(ctx, grad_x, bf16, (T, K), "grad_x") if grad_x is not None else None,
-        _arg(ctx, grad_weights, grad_weights.dtype, (M, K), "grad_weights") if grad_weights is not None else None,
-        MOE_GRAD_F32 if grad_weights is not None and grad_weights.dtype is f32 else MOE_GRAD_BF16, int(bool(accumulate)),
-        _arg(ctx, grad_bias, f32, (M,), "grad_bias") if grad_bias is not None else None, pw, _stream()), "moe_linear_backward")
+    pd, px, pw = _arg(ctx, grad_out, dtype, (T, F), "grad_out"), _arg(ctx, x, _BF16, (T, K), "x"), _arg(ctx, weights, _BF16, (M, K), "weights")
+    pp = _opt(ctx, pre, _BF16, (T, M), "pre")
+    if grad_x is not None:
+        pgx = _arg(ctx, grad_x, _BF16, (T, K), "grad_x")
+    elif need_x:
+        grad_x = torch.empty_like(x)
+        pgx = grad_x.data_ptr()
+    else:
+        pgx = None
+    grad_type = MOE_GRAD_BF16
+    if grad_weights is not None:
+        if grad_weights.dtype is _F32:
+            grad_type = MOE_GRAD_F32
+        elif grad_weights.dtype is not _BF16:
+            raise TypeError("grad_weights must be bfloat16 or float32")
+        pgw = _arg(ctx, grad_weights, grad_weights.dtype, (M, K), "grad_weights")
+    elif need_weights:
+        grad_weights = torch.empty_like(weights)
+        pgw = grad_weights.data_ptr()
+    else:
+        pgw = None
+    if grad_bias is not None:
+        pgb = _arg(ctx, grad_bias, _F32, (M,), "grad_bias")
+    elif bias:
+        grad_bias = x.new_empty(M, dtype=_F32)
+        pgb = grad_bias.data_ptr()
+    else:
+        pgb = None
+    ps, workspace = _workspace(ctx, x, workspace, moe_linear_backward_workspace(T, K, F, act, dtype, grad_bias is not None))
+    st = load_library().moe_linear_backward(ctx.handle, pd, kind, T, px, pw, K, F, act, pp, pgx, pgw, grad_type, int(bool(accumulate)),
+                                            pgb, ps, _stream())
+    if st != MOE_OK:
+        raise MoeError(st, "moe_linear_backward")
     return grad_x, grad_weights, grad_bias
 
 
 def _layer_args(ctx, x, topk_idx, topk_weights, w1, w2, dtype, residual, out, workspace):
-    c = ctx.cfg
-    if x.dim() != 2 or w2.dim() != 3:
-        raise ValueError("x must be [T, %d] and w2 [%d, %d, features]" % (c.hidden, c.num_experts, c.hidden))
-    T, E, H, k, I = x.shape[0], c.num_experts, c.hidden, c.topk, w2.shape[2]
-    bf16 = torch.bfloat16
+    E, H, k, _ = _layer_sizes(ctx)
+    xs, ws = x.shape, w2.shape
+    if len(xs) != 2 or len(ws) != 3:
+        raise ValueError("x must be [T, %d] and w2 [%d, %d, features]" % (H, E, H))
+    T, I = xs[0], ws[2]
+    px = _arg(ctx, x, _BF16, (T, H), "x")
     if out is None:
-        out = _empty(ctx, (T, H), bf16)
-    ps, workspace = _workspace(ctx, workspace, T * k * I * 2)
-    return (T, I, out, workspace, _arg(ctx, x, bf16, (T, H), "x"), _arg(ctx, topk_idx, torch.int64, (T, k), "topk_idx"),
-            _arg(ctx, topk_weights, torch.float32, (T, k), "topk_weights"), _arg(ctx, w1, dtype, (E, 2 * I, H), "w1"),
-            _arg(ctx, w2, dtype, (E, H, I), "w2"), _arg(ctx, residual, bf16, (T, H), "residual") if residual is not None else None,
-            _arg(ctx, out, bf16, (T, H), "out"), ps)
+        out = torch.empty_like(x)
+        po = out.data_ptr()
+    else:
+        po = _arg(ctx, out, _BF16, (T, H), "out")
+    ps, workspace = _workspace(ctx, x, workspace, T * k * I * 2)
+    return (T, I, out, workspace, px, _arg(ctx, topk_idx, _I64, (T, k), "topk_idx"), _arg(ctx, topk_weights, _F32, (T, k), "topk_weights"),
+            _arg(ctx, w1, dtype, (E, 2 * I, H), "w1"), _arg(ctx, w2, dtype, (E, H, I), "w2"), _opt(ctx, residual, _BF16, (T, H), "residual"),
+            po, ps)
 
 
 def moe_layer(ctx, x, topk_idx, topk_weights, w1, w2, residual=None, out=None, workspace=None):
     """The experts of a few tokens (T * k at most MOE_LAYER_MAX_ROWS) in one call: x bf16 [T, H], topk_idx int64 and
     topk_weights fp32 [T, k], w1 bf16 [E, 2I, H] (gates first), w2 bf16 [E, H, I], residual bf16 [T, H] -> bf16 [T, H].
     workspace: at least T * k * I * 2 bytes."""
-    T, I, out, workspace, px, pi, pw, p1, p2, pr, po, ps = _layer_args(ctx, x, topk_idx, topk_weights, w1, w2, torch.bfloat16, residual,
-                                                                       out, workspace)
-    _check(load_library().moe_layer(ctx.handle, px, pi, pw, T, p1, p2, I, pr, po, ps, _stream()), "moe_layer")
+    T, I, out, workspace, px, pi, pw, p1, p2, pr, po, ps = _layer_args(ctx, x, topk_idx, topk_weights, w1, w2, _BF16, residual, out, workspace)
+    st = load_library().moe_layer(ctx.handle, px, pi, pw, T, p1, p2, I, pr, po, ps, _stream())
+    if st != MOE_OK:
+        raise MoeError(st, "moe_layer")
     return out
 
 
 def moe_layer_fp8(ctx, x, topk_idx, topk_weights, w1, w1_scales, w2, w2_scales, residual=None, out=None, workspace=None):
     """moe_layer with matrices of E4M3 codes (uint8) and fp32 scales of 128 x 128 blocks, w1_scales [E, 2I/128, H/128]
     and w2_scales [E, H/128, I/128]."""
-    T, I, out, workspace, px, pi, pw, p1, p2, pr, po, ps = _layer_args(ctx, x, topk_idx, topk_weights, w1, w2, torch.uint8, residual,
-                                                                       out, workspace)
-    E, H = ctx.cfg.num_experts, ctx.cfg.hidden
-    s1 = _arg(ctx, w1_scales, torch.float32, (E, 2 * I // 128, H // 128), "w1_scales")
-    s2 = _arg(ctx, w2_scales, torch.float32, (E, H // 128, I // 128), "w2_scales")
-    _check(load_library().moe_layer_fp8(ctx.handle, px, pi, pw, T, p1, s1, p2, s2, I, pr, po, ps, _stream()), "moe_layer_fp8")
+    T, I, out, workspace, px, pi, pw, p1, p2, pr, po, ps = _layer_args(ctx, x, topk_idx, topk_weights, w1, w2, torch.uint8, residual, out,
+                                                                       workspace)
+    E, H, _, _ = _layer_sizes(ctx)
+    s1 = _arg(ctx, w1_scales, _F32, (E, 2 * I // 128, H // 128), "w1_scales")
+    s2 = _arg(ctx, w2_scales, _F32, (E, H // 128, I // 128), "w2_scales")
+    st = load_library().moe_layer_fp8(ctx.handle, px, pi, pw, T, p1, s1, p2, s2, I, pr, po, ps, _stream())
+    if st != MOE_OK:
+        raise MoeError(st, "moe_layer_fp8")
     return out
 
 
