@@ -19,6 +19,7 @@ struct RouteArgs {
     int32_t T, E, k;
     int32_t groups, keep, top; // groups of E / groups experts, how many stay, scores that make a group's
     uint32_t group_magic;      // ceil(2^32 / (E / groups)), 0 for groups of one expert
+    int32_t group_lanes;       // the largest power of two of lanes that each group can have, at most 32
     int32_t sigmoid, normalize;
     float scale;
 };

@@ -138,6 +138,8 @@ MOE_API moe_status moe_route(moe_ctx* ctx, const void* logits, int32_t logit_typ
     a.top = router->group_top;
     const uint64_t size = (uint64_t)(c.num_experts / router->groups);
     a.group_magic = size > 1 ? (uint32_t)(((1ull << 32) + size - 1) / size) : 0;
+    a.group_lanes = 32;
+    while (a.group_lanes * router->groups > 64) a.group_lanes /= 2;
     a.sigmoid = router->score == MOE_SCORE_SIGMOID;
     a.normalize = router->normalize;
     a.scale = router->scale;

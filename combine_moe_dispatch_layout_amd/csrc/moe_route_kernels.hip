@@ -1,11 +1,19 @@
 // The router: experts and weights of each token from its logits, and the logits'
 // gradient.
 //
-// A token's logits sit in the registers of W lanes, expert u * W + l in lane l's u-th.
 // What is chosen is decided by keys that are compared exactly: without a bias and
 // without groups the logit itself (binary32; the score grows with it), otherwise
 // score + bias in binary64, so that two experts closer than binary32 can tell are
 // still taken in the formula's order.  The weights need no more than binary32.
+//
+// A token's logits sit in the registers of W lanes, expert u * W + l in lane l's u-th.
+// The k rounds of a maximum over those lanes bound the kernel, by their latency, and
+// with scores an exponential in 64 bits for each logit.  Scores take a whole
+// wavefront for a token: one lane's number then is the same for all, so that the
+// chosen logit comes by a scalar register (4096 tokens of 256 experts in 8 groups, 8
+// chosen: 9 us; on 16 lanes 17.5).  Logits of up to 256 experts take 16 lanes, whose
+// maximum needs no step between rows of lanes (8192 tokens of 64 experts, 6 chosen:
+// 4.8 us; a wavefront each 7.1).
 #include <type_traits>
 
 #include "moe_ep.h"
@@ -62,6 +70,32 @@ struct Add {
     __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
 };
 
+// Lane `from`'s value, for all (it is the same for all of them).
+__device__ __forceinline__ float lane_of(float v, int from) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), from));
+}
+__device__ __forceinline__ double lane_of(double v, int from) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), from) << 32 |
+                                          (uint32_t)__builtin_amdgcn_readlane((int)b, from));
+}
+
+// The row broadcasts of a reduction: CTRL 0x142 gives rows 1 and 3 the last lane of the row before, 0x143 the upper half lane
+// 31; the others keep their own.
+template <int CTRL>
+__device__ __forceinline__ uint32_t from_row32(uint32_t v) {
+    return __builtin_amdgcn_update_dpp(v, v, CTRL, CTRL == 0x142 ? 0xA : 0xC, 0xF, false);
+}
+template <int CTRL, class T>
+__device__ __forceinline__ T from_row(T v) {
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(T, from_row32<CTRL>(__builtin_bit_cast(uint32_t, v)));
+    } else {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        return __builtin_bit_cast(T, ((uint64_t)from_row32<CTRL>((uint32_t)(b >> 32)) << 32) | from_row32<CTRL>((uint32_t)b));
+    }
+}
+
 template <class Key>
 __device__ __forceinline__ Key lowest() { return -(Key)__builtin_inff(); }
 
@@ -73,7 +107,28 @@ __device__ __forceinline__ float logit_of(const void* logits, int64_t at, bool b
 // 1 / (1 + e^-v) and its complement, both without cancellation.
 __device__ __forceinline__ float sigmoid32(float v) { return 1.0f / (1.0f + expf(-v)); }
 
-// A token on W lanes, PER logits a lane.  Key: float where keys are logits, double where they are scores.
+// The largest of a token's lanes' values, for all of them.
+template <int W, class T>
+__device__ __forceinline__ T largest(T v) {
+    v = Max()(v, other_of<1>(v));
+    v = Max()(v, other_of<2>(v));
+    v = Max()(v, other_of<4>(v));
+    v = Max()(v, other_of<8>(v));
+    if constexpr (W == 16) return v;
+    // rows of 16: each second one gets the one before, then the upper half the lower; the last lane has all
+    v = Max()(v, from_row<0x142>(v));
+    v = Max()(v, from_row<0x143>(v));
+    return lane_of(v, 63);
+}
+
+// 1 / d of d in [1, 2], to about a step
+__device__ __forceinline__ double inverse(double d) {
+    double r = __builtin_amdgcn_rcp(d);
+    r = __builtin_fma(r, __builtin_fma(-d, r, 1.0), r);
+    return __builtin_fma(r, __builtin_fma(-d, r, 1.0), r);
+}
+
+// A token on W lanes, PER logits a lane.  Key: float where keys are logits, double where they are scores (W = 64).
 template <bool BF16, class Key, int W, int PER>
 __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a) {
     constexpr bool kScored = sizeof(Key) == 8;
@@ -87,18 +142,22 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a) {
     for (int u = 0; u < PER; ++u) {
         const int e = u * W + l;
         v[u] = live && e < a.E ? logit_of(a.logits, t * a.stride + e, BF16) : kNone;
-        // infinite or NaN: not chosen, reported; -inf: not chosen
-        if (!(v[u] < __builtin_inff())) {
+    }
+#pragma unroll
+    for (int u = 0; u < PER; ++u)
+        if (!(v[u] < __builtin_inff())) {   // infinite or NaN: not chosen, and reported; -inf: not chosen
             bad = true;
             v[u] = kNone;
         }
-    }
     if (__ballot(bad) != 0 && lane == 0) atomicOr(a.err, kErrNonFinite);
-    float top = v[0];
+    float top = 0.0f;
+    if (!a.sigmoid) {
+        top = v[0];
 #pragma unroll
-    for (int u = 1; u < PER; ++u) top = fmaxf(top, v[u]);
-    top = over<W>(top, Max());
-    if (!(top > kNone)) top = 0.0f;   // nothing can be chosen: every exponential is zero
+        for (int u = 1; u < PER; ++u) top = fmaxf(top, v[u]);
+        top = largest<W>(top);
+        if (!(top > kNone)) top = 0.0f;   // nothing can be chosen: every exponential is zero
+    }
 
     Key key[PER];
     float total = 0.0f;   // of the softmax's exponentials
@@ -111,72 +170,71 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a) {
             total = over<W>(total, Add());
         }
     } else {
-        double sum = 0.0;
+        static_assert(W == 64);
         if (a.sigmoid) {
 #pragma unroll
-            for (int u = 0; u < PER; ++u) key[u] = 1.0 / (1.0 + exp(-(double)v[u]));
+            for (int u = 0; u < PER; ++u) {
+                const double x = v[u], tail = exp(-fabs(x));   // the smaller of the score and its complement, times a number from 1 to 2
+                key[u] = (x < 0.0 ? tail : 1.0) * inverse(1.0 + tail);
+            }
         } else {
+            double sum = 0.0;
 #pragma unroll
             for (int u = 0; u < PER; ++u) {
                 key[u] = exp((double)v[u] - (double)top);
                 sum += key[u];
             }
-            sum = over<W>(sum, Add());
+            sum = over<64>(sum, Add());
             total = (float)sum;
-            if (!(sum > 0.0)) sum = 1.0;
+            const double by = sum > 0.0 ? 1.0 / sum : 0.0;
 #pragma unroll
-            for (int u = 0; u < PER; ++u) key[u] /= sum;
+            for (int u = 0; u < PER; ++u) key[u] *= by;
         }
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
-            const int e = u * W + l;
+            const int e = u * 64 + lane;
             if (a.bias != nullptr && e < a.E) key[u] += (double)a.bias[e];
             if (!(v[u] > kNone) || key[u] != key[u]) key[u] = lowest<Key>();
         }
         if (a.groups > 1) {
-            // A group's score by one lane, its experts in turn, through LDS.
+            // Group g's best two by `per` lanes, from g * per on, which take its experts in turn from LDS and put their own
+            // together; then every group counts those before it.
             extern __shared__ double shared[];
-            double* mine = shared + (threadIdx.x / W) * a.E;
+            double* mine = shared + (threadIdx.x >> 6) * a.E;
 #pragma unroll
             for (int u = 0; u < PER; ++u)
-                if (u * W + l < a.E) mine[u * W + l] = key[u];
+                if (u * 64 + lane < a.E) mine[u * 64 + lane] = key[u];
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-            const int size = a.E / a.groups;
-            double score[64 / W];   // of group i * W + l
-#pragma unroll
-            for (int i = 0; i < 64 / W; ++i) {
-                const int g = i * W + l;
-                double first = lowest<Key>(), second = lowest<Key>();
-                if (g < a.groups)
-                    for (int n = 0; n < size; ++n) {
-                        const double x = mine[g * size + n];
-                        second = fmax(second, fmin(first, x));
-                        first = fmax(first, x);
-                    }
-                score[i] = a.top > 1 && second > lowest<Key>() ? first + second : first;
+            const int size = a.E / a.groups, per = a.group_lanes, g = lane / per;
+            double first = lowest<Key>(), second = lowest<Key>();
+            if (g < a.groups)
+                for (int n = lane & (per - 1); n < size; n += per) {
+                    const double x = mine[g * size + n];
+                    second = Max()(second, first < x ? first : x);
+                    first = Max()(first, x);
+                }
+            auto join = [&](double f, double s) {
+                const double low = first < f ? first : f;
+                first = Max()(first, f);
+                second = Max()(Max()(second, s), low);
+            };
+            if (per > 1) join(other_of<1>(first), other_of<1>(second));
+            if (per > 2) join(other_of<2>(first), other_of<2>(second));
+            if (per > 4) join(other_of<4>(first), other_of<4>(second));
+            if (per > 8) join(other_of<8>(first), other_of<8>(second));
+            if (per > 16) join(other_of<16>(first), other_of<16>(second));
+            const double score = a.top > 1 && second > lowest<Key>() ? first + second : first;
+            int rank = 0;
+            for (int j = 0; j < a.groups; ++j) {
+                const double s = lane_of(score, j * per);
+                rank += s > score || (s == score && j < g);
             }
-            uint64_t kept = 0;
-            for (int n = 0; n < a.keep; ++n) {
-                double m = score[0];
-#pragma unroll
-                for (int i = 1; i < 64 / W; ++i) m = fmax(m, score[i]);
-                m = over<W>(m, Max());
-                if (!(m > lowest<Key>())) break;
-                int g = INT32_MAX;
-#pragma unroll
-                for (int i = 64 / W - 1; i >= 0; --i)
-                    if (score[i] == m) g = i * W + l;
-                g = over<W>(g, Min());
-                kept |= 1ull << g;
-#pragma unroll
-                for (int i = 0; i < 64 / W; ++i)
-                    if (i * W + l == g) score[i] = lowest<Key>();
-            }
+            const uint64_t kept = __ballot(g < a.groups && rank < a.keep);
 #pragma unroll
             for (int u = 0; u < PER; ++u) {
-                const uint32_t e = u * W + l;
-                const uint32_t g = a.group_magic ? __umulhi(e, a.group_magic) : e;
-                if (!(kept >> (g & 63) & 1)) key[u] = lowest<Key>();
+                const uint32_t e = u * 64 + lane;
+                const uint32_t of = a.group_magic ? __umulhi(e, a.group_magic) : e;
+                if (!(kept >> (of * per & 63) & 1)) key[u] = lowest<Key>();
             }
         }
     }
@@ -191,22 +249,38 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a) {
         mine_v[i] = kNone;
     }
     for (int j = 0; j < a.k; ++j) {
-        Key m = key[0];
+        Key m = key[PER - 1];
+        int at = PER - 1;
+        float x = v[PER - 1];
 #pragma unroll
-        for (int u = 1; u < PER; ++u) m = Max()(m, key[u]);
-        m = over<W>(m, Max());
-        if (__ballot(m > lowest<Key>()) == 0) break;
-        int e = INT32_MAX;
-        float x = kNone;
-#pragma unroll
-        for (int u = PER - 1; u >= 0; --u)
-            if (key[u] == m) {
-                e = u * W + l;
+        for (int u = PER - 2; u >= 0; --u)
+            if (key[u] >= m) {
+                m = key[u];
+                at = u;
                 x = v[u];
             }
-        const int chosen = over<W>(e, Min());
-        x = over<W>(e == chosen ? x : kNone, Max());   // its logit
-        if (m > lowest<Key>()) {
+        const Key best = largest<W>(m);
+        const bool found = best > lowest<Key>();
+        if (__ballot(found) == 0) break;
+        int chosen;
+        if constexpr (W == 64) {
+            const uint64_t equal = __ballot(m == best);
+            int from = __ffsll((unsigned long long)equal) - 1;
+            if (equal & (equal - 1)) {   // the one with the lowest register, then lane
+#pragma unroll
+                for (int u = PER - 1; u >= 0; --u) {
+                    const uint64_t here = __ballot(m == best && at == u);
+                    if (here != 0) from = __ffsll((unsigned long long)here) - 1;
+                }
+            }
+            chosen = __builtin_amdgcn_readlane(at, from) * W + from;
+            x = lane_of(x, from);
+        } else {
+            const int e = m == best ? at * W + l : INT32_MAX;
+            chosen = over<W>(e, Min());
+            x = over<W>(e == chosen ? x : kNone, Max());
+        }
+        if (found) {
 #pragma unroll
             for (int u = 0; u < PER; ++u)
                 if (u * W + l == chosen) key[u] = lowest<Key>();
@@ -222,7 +296,7 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a) {
     float peak = kNone;
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) peak = fmaxf(peak, mine_v[i]);
-    peak = over<W>(peak, Max());
+    peak = largest<W>(peak);
     float w[kSlots], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
@@ -235,8 +309,13 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a) {
         } else w[i] = expf(x - (a.normalize ? peak : top));
         sum += w[i];
     }
-    sum = over<W>(sum, Add());
-    const float by = !a.normalize ? (a.sigmoid ? a.scale : a.scale / (total > 0.0f ? total : 1.0f)) : sum > 0.0f ? a.scale / sum : 0.0f;
+    float by = a.scale;
+    if (a.normalize) {
+        sum = over<W>(sum, Add());
+        by = sum > 0.0f ? a.scale / sum : 0.0f;
+    } else if (!a.sigmoid) {
+        by = a.scale / (total > 0.0f ? total : 1.0f);
+    }
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
         const int j = i * W + l;
@@ -358,14 +437,27 @@ hipError_t by_experts(int E, F16 on16, F64 on64) {
 template <bool BF16, class Key>
 hipError_t route(const RouteArgs& a, hipStream_t s) {
     auto go = [&](auto w, auto per) {
-        constexpr int W = decltype(w)::value, PER = decltype(per)::value;
-        const int tokens = kThreads / W;
+        constexpr int W = decltype(w)::value, tokens = kThreads / W;
         const size_t lds = sizeof(Key) == 8 && a.groups > 1 ? (size_t)tokens * a.E * sizeof(double) : 0;
-        k_route<BF16, Key, W, PER><<<dim3((unsigned)((a.T + tokens - 1) / tokens)), dim3(kThreads), lds, s>>>(a);
+        k_route<BF16, Key, W, decltype(per)::value><<<dim3((unsigned)((a.T + tokens - 1) / tokens)), dim3(kThreads), lds, s>>>(a);
         return hipGetLastError();
     };
-    return by_experts(a.E, [&](auto per) { return go(std::integral_constant<int, 16>(), per); },
-                      [&](auto per) { return go(std::integral_constant<int, 64>(), per); });
+    using std::integral_constant;
+    if constexpr (sizeof(Key) == 4) {
+        const integral_constant<int, 16> w;
+        if (a.E <= 16) return go(w, integral_constant<int, 1>());
+        if (a.E <= 64) return go(w, integral_constant<int, 4>());
+        if (a.E <= 128) return go(w, integral_constant<int, 8>());
+        if (a.E <= 256) return go(w, integral_constant<int, 16>());
+    }
+    const integral_constant<int, 64> w;
+    if constexpr (sizeof(Key) == 8) {
+        if (a.E <= 64) return go(w, integral_constant<int, 1>());
+        if (a.E <= 128) return go(w, integral_constant<int, 2>());
+        if (a.E <= 256) return go(w, integral_constant<int, 4>());
+    }
+    if (a.E <= 512) return go(w, integral_constant<int, 8>());
+    return go(w, integral_constant<int, 16>());
 }
 
 template <bool BF16>

@@ -315,10 +315,10 @@ def test_binding_rejects_cpu_tensors_without_a_gpu():
 
     class Ctx:
         cfg, device, handle = moe.make_config(4, 8, 16, 1, 2), 0, None
-    with pytest.raises(TypeError):
-        moe.moe_route(Ctx, torch.zeros(4, 16))
-    with pytest.raises(TypeError):
-        moe.moe_route_backward(Ctx, torch.zeros(4, 2), torch.zeros(4, 16), torch.zeros(4, 2, dtype=torch.int64))
+    with pytest.raises(TypeError, match="logits must be"):
+        moe.moe_route(Ctx(), torch.zeros(4, 16))
+    with pytest.raises(TypeError, match="logits must be"):
+        moe.moe_route_backward(Ctx(), torch.zeros(4, 2), torch.zeros(4, 16), torch.zeros(4, 2, dtype=torch.int64))
 
 
 @gpu_only
