@@ -84,6 +84,9 @@ struct LinearGradArgs {
 
 hipError_t launch_layer(const LayerArgs& a, bool fp8, hipStream_t s);
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
+// Whether one launch has enough workgroups.
+bool linear_fits(int64_t T, int64_t M);
+bool linear_bwd_fits(int64_t T, int64_t F);
 int64_t linear_workspace(int64_t T, int64_t K, int64_t F, bool gated);   // bytes
 // The backward's products where linear_bwd_here() says so; the others are the expert products' gradients.
 bool linear_bwd_here(int64_t R, int64_t C);

@@ -31,13 +31,14 @@ moe_status check_tokens(const moe_ctx* ctx, int32_t T) {
 }
 
 // ---------------------------------------------------------------- router
-moe_status check_router(const moe_config& c, const moe_router* r, const void* logits, int32_t type, int64_t stride) {
+moe_status check_router(const moe_config& c, int32_t T, const moe_router* r, const void* logits, int32_t type, int64_t stride) {
     if (r == nullptr || (type != MOE_LOGIT_F32 && type != MOE_LOGIT_BF16) || stride < c.num_experts) return MOE_ERR_INVALID_ARG;
     if ((r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) || (r->normalize != 0 && r->normalize != 1) ||
         !std::isfinite(r->scale))
         return MOE_ERR_INVALID_ARG;
     if (r->groups < 1 || r->topk_groups < 1 || r->topk_groups > r->groups || (r->group_top != 1 && r->group_top != 2))
         return MOE_ERR_INVALID_ARG;
+    if (T >= 1 << 26) return MOE_ERR_UNSUPPORTED;   // of 64 lanes each: a launch has fewer than 2^32
     if (r->groups > MOE_MAX_GROUPS || c.num_experts % r->groups != 0) return MOE_ERR_UNSUPPORTED;
     return aligned(logits, type == MOE_LOGIT_F32 ? 4 : 2) ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
@@ -88,6 +89,8 @@ moe_status run_layer(moe_ctx* ctx, const void* x, const int64_t* idx, const floa
     if (fp8 && (s1 == nullptr || s2 == nullptr || !aligned(s1, 4) || !aligned(s2, 4))) return MOE_ERR_INVALID_ARG;
     for (const void* p : {x, w1, w2, static_cast<const void*>(idx), static_cast<const void*>(weights), static_cast<const void*>(workspace)})
         if (out == p) return MOE_ERR_INVALID_ARG;
+    for (const void* p : {x, w1, w2, static_cast<const void*>(idx), static_cast<const void*>(weights), residual})
+        if (workspace == p) return MOE_ERR_INVALID_ARG;
     LayerArgs a = {};
     a.x = x;
     a.idx = idx;
@@ -117,11 +120,12 @@ MOE_API moe_status moe_route(moe_ctx* ctx, const void* logits, int32_t logit_typ
     moe_status st = check_tokens(ctx, num_tokens);
     if (st != MOE_OK) return st;
     const moe_config& c = ctx->cfg;
-    st = check_router(c, router, logits, logit_type, logits_stride);
+    st = check_router(c, num_tokens, router, logits, logit_type, logits_stride);
     if (st != MOE_OK) return st;
     if (num_tokens == 0) return MOE_OK;
     if (logits == nullptr || topk_idx == nullptr || topk_weights == nullptr || !aligned(bias, 4) || !aligned(topk_idx, 8) ||
-        !aligned(topk_weights, 4))
+        !aligned(topk_weights, 4) || topk_idx == logits || topk_weights == logits || topk_weights == bias ||
+        static_cast<const void*>(topk_idx) == bias || static_cast<const void*>(topk_idx) == topk_weights)
         return MOE_ERR_INVALID_ARG;
     RouteArgs a = {};
     a.logits = logits;
@@ -153,11 +157,11 @@ MOE_API moe_status moe_route_backward(moe_ctx* ctx, const float* grad_weights, c
     moe_status st = check_tokens(ctx, num_tokens);
     if (st != MOE_OK) return st;
     const moe_config& c = ctx->cfg;
-    st = check_router(c, router, logits, logit_type, logits_stride);
+    st = check_router(c, num_tokens, router, logits, logit_type, logits_stride);
     if (st != MOE_OK) return st;
     if (num_tokens == 0) return MOE_OK;
     if (grad_weights == nullptr || logits == nullptr || topk_idx == nullptr || grad_logits == nullptr || grad_logits == logits ||
-        grad_logits == grad_weights || !aligned(grad_weights, 4) || !aligned(topk_idx, 8) || !aligned(grad_logits, 4))
+        grad_logits == grad_weights || static_cast<const void*>(grad_logits) == topk_idx || !aligned(grad_weights, 4) || !aligned(topk_idx, 8) || !aligned(grad_logits, 4))
         return MOE_ERR_INVALID_ARG;
     RouteBwdArgs a = {};
     a.grad = grad_weights;
@@ -182,6 +186,7 @@ MOE_API moe_status moe_linear(moe_ctx* ctx, const void* x, int32_t num_rows, con
     if (ctx == nullptr || !on_ctx_device(ctx)) return MOE_ERR_INVALID_ARG;
     const moe_status st = check_linear(num_rows, in_features, features, act, out_type);
     if (st != MOE_OK) return st;
+    if (!linear_fits(num_rows, columns(features, act))) return MOE_ERR_UNSUPPORTED;
     if (num_rows == 0) return MOE_OK;
     for (const void* p : {x, weights, static_cast<const void*>(out)})
         if (p == nullptr || !aligned16(p)) return MOE_ERR_INVALID_ARG;
@@ -213,6 +218,7 @@ MOE_API moe_status moe_linear_workspace(int32_t num_rows, int32_t in_features, i
     if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
     const moe_status st = check_linear(num_rows, in_features, features, act, MOE_OUT_BF16);
     if (st != MOE_OK) return st;
+    if (!linear_fits(num_rows, columns(features, act))) return MOE_ERR_UNSUPPORTED;
     *bytes = (size_t)linear_workspace(num_rows, in_features, features, act == MOE_ACT_SWIGLU);
     return MOE_OK;
 }
@@ -222,6 +228,7 @@ MOE_API moe_status moe_linear_backward_workspace(int32_t num_rows, int32_t in_fe
     if (bytes == nullptr || (with_bias != 0 && with_bias != 1)) return MOE_ERR_INVALID_ARG;
     const moe_status st = check_linear(num_rows, in_features, features, act, out_type);
     if (st != MOE_OK) return st;
+    if (!linear_bwd_fits(num_rows, features)) return MOE_ERR_UNSUPPORTED;
     *bytes = plan_backward(num_rows, in_features, features, act, out_type, with_bias != 0).total;
     return MOE_OK;
 }
@@ -233,6 +240,7 @@ MOE_API moe_status moe_linear_backward(moe_ctx* ctx, const void* grad_out, int32
     if (ctx == nullptr || !on_ctx_device(ctx)) return MOE_ERR_INVALID_ARG;
     const moe_status st = check_linear(num_rows, in_features, features, act, out_type);
     if (st != MOE_OK) return st;
+    if (!linear_bwd_fits(num_rows, features)) return MOE_ERR_UNSUPPORTED;
     if ((grad_type != MOE_GRAD_BF16 && grad_type != MOE_GRAD_F32) || (accumulate != 0 && accumulate != 1)) return MOE_ERR_INVALID_ARG;
     const BackwardPlan plan = plan_backward(num_rows, in_features, features, act, out_type, grad_bias != nullptr);
     const bool any = num_rows > 0;

@@ -606,6 +606,8 @@ enum { kTile128, kTile64, kTile32, kTiles, kWide };
 constexpr int kTileCols[kTiles] = {128, 64, 64}, kTileRows[kTiles] = {128, 64, 32};
 constexpr float kStepUs[kTiles] = {0.65f, 0.33f, 0.2f}, kL2Us = 1.0f / 12e6f, kPartUs = 8.0f / 5e6f, kJoinUs = 4.0f, kWideUs = 1.6f;
 
+constexpr int64_t kMostTiles = (1 << 23) - 256;   // of up to 512 threads: a launch has fewer than 2^32
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // tiles: how many kinds there are.  cols counts matrix rows (a gated product's are twice its results).
@@ -613,6 +615,7 @@ Plan plan_tiles(int64_t rows, int64_t cols, int64_t steps, int tiles) {
     Plan best = {kTile64, 1, 1e30f};
     for (int t = 0; t < tiles; ++t) {
         const int64_t n = ceil_div(rows, kTileRows[t]) * ceil_div(cols, kTileCols[t]);
+        if (n >= kMostTiles) continue;
         for (int split = 1; split <= 16 && (split == 1 || steps >= 4 * split); split *= 2) {
             const float traffic = (float)n * steps * (kTileCols[t] + kTileRows[t]) * kStepBytes * kL2Us;
             const float latency = (float)ceil_div(steps, split) * ceil_div(n * split, 512) * kStepUs[t];
@@ -626,7 +629,7 @@ Plan plan_tiles(int64_t rows, int64_t cols, int64_t steps, int tiles) {
 // Up to 12 rows whose matrix a workgroup for each 16 columns reads well (1 x 7168 -> 4096 13.2, in tiles 15.2; 12 x 4096 -> 4096 10.4
 // and 11.3), or is short (8 x 1024 -> 1024 5.1 and 6.4); not so 4 x 7168 -> 2048 gated (21.6 and 16.1), 8 x 7168 -> 256 (13.4 and
 // 9.7) or 16 x 4096 -> 4096.
-bool few_rows(int64_t T, int64_t K, int64_t F) { return T <= 12 && (F >= 192 * 16 || K <= 1024); }
+bool few_rows(int64_t T, int64_t K, int64_t F) { return T <= 12 && (F >= 2560 || K <= 1024); }
 
 Plan plan_linear(int64_t T, int64_t K, int64_t M) {
     const int64_t steps = ceil_div(K * 2, kStepBytes);
@@ -647,7 +650,6 @@ hipError_t linear(const LinearArgs& a, hipStream_t s) {
     if (p.tile == kTile64) return launch_tile<GATED, 64, 64, 2, 2, 4>(a, p.split, s);
     if (p.tile == kTile32) return launch_tile<GATED, 64, 32, 2, 2, 4>(a, p.split, s);
     const int64_t blocks = ceil_div(ceil_div(M, kTileP) * ceil_div(a.T, 256), 256) * 256;
-    if (blocks * 64 * kWaves >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
     k_linear<GATED><<<dim3((unsigned)blocks), dim3(64 * kWaves), 0, s>>>(a);
     return hipGetLastError();
 }
@@ -662,6 +664,9 @@ hipError_t linear_bwd(const LinearBwdArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) { return a.act == MOE_ACT_SWIGLU ? linear<true>(a, s) : linear<false>(a, s); }
+
+bool linear_fits(int64_t T, int64_t M) { return ceil_div(M, kTileP) * ceil_div(T, 256) <= kMostTiles; }
+bool linear_bwd_fits(int64_t T, int64_t F) { return ceil_div(T, 8 * kGradWaves) * ceil_div(F, kGradSlice) <= kMostTiles / 2; }
 
 int64_t linear_workspace(int64_t T, int64_t K, int64_t F, bool gated) {
     if (T == 0 || few_rows(T, K, F)) return 0;
@@ -692,7 +697,6 @@ hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t s) {
     const bool gated = a.act == MOE_ACT_SWIGLU;
     const int M = gated ? 2 * a.F : a.F, per = grad_rows(a.T);
     const int64_t sums = linear_sum_blocks(a.T), blocks = (a.T > 0 ? sums > 0 ? sums : 1 : 0) * ((a.F + kGradSlice - 1) / kGradSlice);
-    if (blocks * 64 * kGradWaves >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
     if (blocks > 0) {
         if (gated) k_linear_grad<true><<<dim3((unsigned)blocks), dim3(64 * kGradWaves), 0, s>>>(a, per);
         else k_linear_grad<false><<<dim3((unsigned)blocks), dim3(64 * kGradWaves), 0, s>>>(a, per);

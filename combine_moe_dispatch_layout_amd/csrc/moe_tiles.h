@@ -37,8 +37,8 @@ __device__ __forceinline__ u32x2 bf16_pack(f32x4 v) {
     return u32x2{bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16)};
 }
 
-// Every descriptor covers one stage of one tile, at most 256 rows of 2 * MOE_MAX_FEATURES bytes.
-static_assert(256ll * 2 * MOE_MAX_FEATURES < kOob, "");
+// A descriptor covers one stage of one tile, at most 256 rows of 2 * MOE_MAX_FEATURES bytes, or all rows of a few tokens.
+static_assert(256ll * 2 * MOE_MAX_FEATURES < kOob && 2ll * MOE_LAYER_MAX_ROWS * MOE_MAX_FEATURES < kOob, "");
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const void* p, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, max(bytes, 0), 0x00020000);
 }

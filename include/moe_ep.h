@@ -463,7 +463,8 @@ moe_status moe_swiglu_backward(moe_ctx* ctx, const void* grad_out, const void* g
 /* What stands before the dispatch (an addition: the pages begin with topk_idx, and
  * name group-limited gating, which these calls have): the experts and weights of
  * each token from its logits, in the form that moe_dispatch, moe_combine and moe_layer
- * read.  E and k are the context's; num_tokens is at most max_tokens. */
+ * read.  E and k are the context's; num_tokens is at most max_tokens, and below 2^26
+ * (MOE_ERR_UNSUPPORTED). */
 typedef enum moe_score {
     MOE_SCORE_SOFTMAX = 0,     /* s = softmax of the token's logits, over all its experts */
     MOE_SCORE_SIGMOID = 1      /* s = 1 / (1 + exp(-logit)) */
@@ -561,7 +562,8 @@ moe_status moe_linear_workspace(int32_t num_rows, int32_t in_features, int32_t f
  *   accumulate  1: grad_weights and grad_bias are added to what they hold
  *   workspace   moe_linear_backward_workspace bytes, 16-byte aligned: holds d, rounded to bf16 for the products
  *               (grad_bias adds the binary32 values), and sums; NULL if that is 0
- * With no rows grad_weights and grad_bias are zeroed (or left, with accumulate). */
+ * With no rows grad_weights and grad_bias are zeroed (or left, with accumulate).  More tiles of 128 rows by 512 of
+ * grad_out's columns than 2^22 - 128 are MOE_ERR_UNSUPPORTED. */
 moe_status moe_linear_backward(moe_ctx* ctx, const void* grad_out, int32_t out_type, int32_t num_rows,
                                const void* x, const void* weights, int32_t in_features,
                                int32_t features, int32_t act, const void* pre, void* grad_x,

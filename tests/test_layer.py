@@ -347,7 +347,7 @@ def test_refusals(gpu):
     for name in ("x", "idx", "w", "w1", "w2", "out", "ws"):
         assert call(**{name: None}) == m.MOE_ERR_INVALID_ARG, name
         assert call(**{name: good[name] + 2}) == m.MOE_ERR_INVALID_ARG, name
-    for kwargs in (dict(out=good["x"]), dict(out=good["w1"]), dict(out=good["ws"]), dict(I=0), dict(T=-1), dict(res=good["x"] + 4)):
+    for kwargs in (dict(out=good["x"]), dict(out=good["w1"]), dict(out=good["ws"]), dict(ws=good["x"]), dict(ws=good["w2"]), dict(ws=good["x"], res=good["x"]), dict(I=0), dict(T=-1), dict(res=good["x"] + 4)):
         assert call(**kwargs) == m.MOE_ERR_INVALID_ARG, kwargs
     assert call(I=76) == call(I=32776) == m.MOE_ERR_UNSUPPORTED
     q = Layer(m, (2, uniform(2, 1, 2)), 128, 128, fp8=True)

@@ -152,6 +152,27 @@ def test_outputs_past_32_bits(gpu):
 
 
 @gpu_only
+def test_a_billion_rows(gpu):
+    """More tiles of 128 rows than a launch has workgroups for (2^32 threads)."""
+    ctx = context(gpu)
+    T = 2 ** 30 + 5
+    if torch.cuda.mem_get_info()[0] < 3 * T * 16:
+        pytest.skip("needs 52 GB")
+    x = torch.zeros(T, 8, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(8, 8, dtype=torch.bfloat16, device="cuda")
+    w[:, 2] = torch.arange(1, 9, device="cuda").bfloat16()
+    at = [0, 127, 2 ** 29 - 1, 2 ** 29, 2 ** 30 - 1, 2 ** 30, 2 ** 30 + 4]
+    for i, r in enumerate(at):
+        x[r, 2] = float(i + 1)
+    out = gpu.moe_linear(ctx, x, w)
+    for i, r in enumerate(at):
+        assert torch.equal(out[r], w[:, 2] * (i + 1)), r
+    out[torch.tensor(at, device="cuda")] = 0
+    assert not out.view(torch.int64).any()
+    ctx.close()
+
+
+@gpu_only
 @pytest.mark.parametrize("act", ACTS)
 def test_extreme_sums(gpu, act):
     """Sums up to the ends of bf16's range stay finite where the function is, and NaN and infinities stay in their rows."""
@@ -375,6 +396,13 @@ def test_workspace_sizes():
     assert back(0, 64, 64, act=GELU, bias=True) == 0
     assert moe.moe_linear_workspace(0, 64, 64) == moe.moe_linear_workspace(1, 512, 64) == moe.moe_linear_workspace(8192, 4096, 4096) == 0
     assert moe.moe_linear_workspace(24, 7168, 256) >= 2 * 24 * 256 * 4
+    # more tiles than a launch has workgroups for
+    assert moe.moe_linear_workspace(2 ** 31 - 65536, 8, 256) == 0 and back(2 ** 29 - 16384, 8, 512, act=SWIGLU) > 0
+    for query in (lambda: moe.moe_linear_workspace(2 ** 31 - 65535, 8, 256), lambda: moe.moe_linear_workspace(2 ** 30, 8, 264),
+                  lambda: back(2 ** 29 - 16383, 8, 512, act=SWIGLU), lambda: back(2 ** 28, 8, 520)):
+        with pytest.raises(moe.MoeError) as e:
+            query()
+        assert e.value.status == moe.MOE_ERR_UNSUPPORTED
 
 
 def moe_bytes(moe):

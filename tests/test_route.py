@@ -349,13 +349,20 @@ def test_refusals(gpu):
     p, call = v.data_ptr(), lambda *a: lib.moe_route(ctx.handle, a[0], a[1], a[2], 4, ctypes.byref(r), None, a[3], a[4], None)
     bad = [(None, 0, 16, idx.data_ptr(), w.data_ptr()), (p, 2, 16, idx.data_ptr(), w.data_ptr()), (p, 0, 15, idx.data_ptr(), w.data_ptr()),
            (p + 2, 0, 16, idx.data_ptr(), w.data_ptr()), (p, 0, 16, None, w.data_ptr()), (p, 0, 16, idx.data_ptr() + 4, w.data_ptr()),
-           (p, 0, 16, idx.data_ptr(), None)]
+           (p, 0, 16, idx.data_ptr(), None), (p, 0, 16, p, w.data_ptr()), (p, 0, 16, idx.data_ptr(), p), (p, 0, 16, idx.data_ptr(), idx.data_ptr())]
     assert [call(*a) for a in bad] == [gpu.MOE_ERR_INVALID_ARG] * len(bad)
     back = lambda *a: lib.moe_route_backward(ctx.handle, a[0], p, 0, 16, a[1], 4, ctypes.byref(r), a[2], None)
-    bad = [(None, idx.data_ptr(), gl.data_ptr()), (w.data_ptr(), None, gl.data_ptr()), (w.data_ptr(), idx.data_ptr(), None), (w.data_ptr(), idx.data_ptr(), p)]
+    bad = [(None, idx.data_ptr(), gl.data_ptr()), (w.data_ptr(), None, gl.data_ptr()), (w.data_ptr(), idx.data_ptr(), None), (w.data_ptr(), idx.data_ptr(), p),
+           (w.data_ptr(), idx.data_ptr(), idx.data_ptr())]
     assert [back(*a) for a in bad] == [gpu.MOE_ERR_INVALID_ARG] * len(bad)
     r.normalize = 2
     assert call(p, 0, 16, idx.data_ptr(), w.data_ptr()) == gpu.MOE_ERR_INVALID_ARG
     empty = gpu.moe_route(ctx, v[:0])
     assert empty[0].shape == (0, 2) and gpu.moe_route_backward(ctx, w[:0], v[:0], idx[:0]).shape == (0, 16)
     ctx.close()
+    many = gpu.Context(gpu.make_config(2 ** 26, 8, 4, 1, 1))   # more tokens than a launch has lanes for
+    r.normalize = 1
+    assert lib.moe_route(many.handle, p, 0, 4, 2 ** 26, ctypes.byref(r), None, idx.data_ptr(), w.data_ptr(), None) == gpu.MOE_ERR_UNSUPPORTED
+    assert lib.moe_route_backward(many.handle, w.data_ptr(), p, 0, 4, idx.data_ptr(), 2 ** 26, ctypes.byref(r), gl.data_ptr(),
+                                  None) == gpu.MOE_ERR_UNSUPPORTED
+    many.close()
