@@ -458,12 +458,12 @@ __global__ __launch_bounds__(256) void k_linear_bwd_join(LinearBwdArgs a, int sp
 }
 
 // ---------------------------------------------------------------- gradient before the activation
-// grad_pre = grad act'(pre), and the sums of its columns (of the binary32 values): a workgroup takes 512 columns, eight a
-// lane, of its wavefronts' share of rows, whose sums meet in LDS.  Bound by memory.
-constexpr int kGradWaves = 16, kGradSlice = 512;
-// Rows of a wavefront: all of a few, so that one workgroup has every row of its columns and writes their sums itself;
-// else 8 (the sums of 128 rows are 1/64 of what a bf16 gradient takes).
-__host__ __device__ inline int grad_rows(int T) { return T <= 8 * kGradWaves ? (T + kGradWaves - 1) / kGradWaves : 8; }
+// grad_pre = grad act'(pre), and the sums of its columns (of the binary32 values): a workgroup of 16 wavefronts takes 128 rows
+// of a slice of columns, eight a lane; the sums meet in LDS.  Up to 128 rows are in one workgroup, which writes their sums
+// itself; its wavefronts then take four rows of 128 columns at once, because the time is that of their loads one after the
+// other.  Else a wavefront's row is 512 columns long, and the kernel is bound by memory (the sums of 128 rows are 1/64 of what a
+// bf16 gradient takes).
+constexpr int kGradWaves = 16, kGradRows = 128, kGradSlice = 512, kGradSliceFew = 128;
 
 __device__ __forceinline__ void load_grad(const LinearGradArgs& a, int64_t at, float (&d)[8]) {
     if (a.grad_f32) {
@@ -479,17 +479,17 @@ __device__ __forceinline__ void load_grad(const LinearGradArgs& a, int64_t at, f
     }
 }
 
-template <bool GATED>
-__global__ __launch_bounds__(64 * kGradWaves) void k_linear_grad(LinearGradArgs a, int per) {
-    constexpr int NP = GATED ? 2 : 1;
-    __shared__ f32x4 part[kGradWaves][2][64];
-    const int slices = (a.F + kGradSlice - 1) / kGradSlice, w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int block = (int)(blockIdx.x / slices), col = (int)(blockIdx.x - (unsigned)block * slices) * kGradSlice + lane * 8;
+template <bool GATED, int SLICE>
+__global__ __launch_bounds__(64 * kGradWaves) void k_linear_grad(LinearGradArgs a) {
+    constexpr int NP = GATED ? 2 : 1, kLanes = SLICE / 8, kAtOnce = kGradWaves * (64 / kLanes);   // lanes and workgroup's rows
+    __shared__ f32x4 part[kGradWaves][2][kLanes];
+    const int slices = (a.F + SLICE - 1) / SLICE, w = threadIdx.x >> 6, lane = threadIdx.x & (kLanes - 1);
+    const int block = (int)(blockIdx.x / slices), col = (int)(blockIdx.x - (unsigned)block * slices) * SLICE + lane * 8;
     const int M = NP * a.F;
     float sum[NP][8] = {};
     if (col < a.F) {
-        for (int i = 0; i < per; ++i) {
-            const int r = (block * per + i) * kGradWaves + w;
+        for (int i = 0; i < kGradRows / kAtOnce; ++i) {
+            const int r = block * kGradRows + i * kAtOnce + (int)threadIdx.x / kLanes;
             if (r >= a.T) break;
             float d[8], v[8];
             load_grad(a, (int64_t)r * a.F + col, d);
@@ -526,11 +526,15 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_linear_grad(LinearGradArgs 
     if (a.grad_bias == nullptr) return;
 #pragma unroll
     for (int h = 0; h < NP; ++h) {
+#pragma unroll
+        for (int step = kLanes; step < 64; step *= 2)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum[h][k] += __shfl_xor(sum[h][k], step, 64);
         if (h > 0) __syncthreads();
         part[w][0][lane] = f32x4{sum[h][0], sum[h][1], sum[h][2], sum[h][3]};
         part[w][1][lane] = f32x4{sum[h][4], sum[h][5], sum[h][6], sum[h][7]};
         __syncthreads();
-        if (w < 2 && col < a.F) {   // each of two wavefronts half of a lane's eight
+        if (w < 2 && (int)(threadIdx.x & 63) < kLanes && col < a.F) {   // each of two wavefronts half of a lane's eight
             f32x4 v = part[0][w][lane];
 #pragma unroll
             for (int i = 1; i < kGradWaves; ++i) v += part[i][w][lane];
@@ -666,7 +670,7 @@ hipError_t linear_bwd(const LinearBwdArgs& a, hipStream_t s) {
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) { return a.act == MOE_ACT_SWIGLU ? linear<true>(a, s) : linear<false>(a, s); }
 
 bool linear_fits(int64_t T, int64_t M) { return ceil_div(M, kTileP) * ceil_div(T, 256) <= kMostTiles; }
-bool linear_bwd_fits(int64_t T, int64_t F) { return ceil_div(T, 8 * kGradWaves) * ceil_div(F, kGradSlice) <= kMostTiles / 2; }
+bool linear_bwd_fits(int64_t T, int64_t F) { return ceil_div(T, kGradRows) * ceil_div(F, kGradSlice) <= kMostTiles / 2; }
 
 int64_t linear_workspace(int64_t T, int64_t K, int64_t F, bool gated) {
     if (T == 0 || few_rows(T, K, F)) return 0;
@@ -688,19 +692,15 @@ int64_t linear_bwd_workspace(int64_t R, int64_t C, int64_t X) {
 
 hipError_t launch_linear_bwd(const LinearBwdArgs& a, bool weights, hipStream_t s) { return weights ? linear_bwd<true>(a, s) : linear_bwd<false>(a, s); }
 
-int64_t linear_sum_blocks(int64_t T) {
-    const int64_t rows = (int64_t)kGradWaves * grad_rows((int)T);
-    return T <= rows ? 0 : (T + rows - 1) / rows;
-}
+int64_t linear_sum_blocks(int64_t T) { return T <= kGradRows ? 0 : ceil_div(T, kGradRows); }
 
 hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t s) {
     const bool gated = a.act == MOE_ACT_SWIGLU;
-    const int M = gated ? 2 * a.F : a.F, per = grad_rows(a.T);
-    const int64_t sums = linear_sum_blocks(a.T), blocks = (a.T > 0 ? sums > 0 ? sums : 1 : 0) * ((a.F + kGradSlice - 1) / kGradSlice);
-    if (blocks > 0) {
-        if (gated) k_linear_grad<true><<<dim3((unsigned)blocks), dim3(64 * kGradWaves), 0, s>>>(a, per);
-        else k_linear_grad<false><<<dim3((unsigned)blocks), dim3(64 * kGradWaves), 0, s>>>(a, per);
-    }
+    const int M = gated ? 2 * a.F : a.F;
+    const int64_t sums = linear_sum_blocks(a.T);
+    auto go = [&](auto kernel, int64_t blocks) { kernel<<<dim3((unsigned)blocks), dim3(64 * kGradWaves), 0, s>>>(a); };
+    if (sums > 0) go(gated ? k_linear_grad<true, kGradSlice> : k_linear_grad<false, kGradSlice>, sums * ceil_div(a.F, kGradSlice));
+    else if (a.T > 0) go(gated ? k_linear_grad<true, kGradSliceFew> : k_linear_grad<false, kGradSliceFew>, ceil_div(a.F, kGradSliceFew));
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.grad_bias == nullptr || (a.T > 0 && sums == 0)) return e;
     k_linear_bias<<<dim3((unsigned)((M + 63) / 64)), dim3(1024), 0, s>>>(a.partial, (int)sums, M, a.grad_bias, a.accumulate);

@@ -7,11 +7,11 @@
 // still taken in the formula's order.  The weights need no more than binary32.
 //
 // A token's logits sit in the registers of W lanes, expert u * W + l in lane l's u-th.
-// The k rounds of a maximum over those lanes bound the kernel, by their latency, and
-// with scores an exponential in 64 bits for each logit.  Scores take a whole
-// wavefront for a token: one lane's number then is the same for all, so that the
-// chosen logit comes by a scalar register (4096 tokens of 256 experts in 8 groups, 8
-// chosen: 9 us; on 16 lanes 17.5).  Logits of up to 256 experts take 16 lanes, whose
+// Instructions bound the kernel: the k rounds of a maximum over those lanes, and with
+// scores an exponential in 64 bits for each logit.  Scores take a whole wavefront for
+// a token: what one lane found then is in scalar registers for all, and rounds compare
+// 32 bits (4096 tokens of 256 experts in 8 groups, 8 chosen: 9.7 us; rounds of 64 bits
+// 11.2; on 16 lanes 17.5).  Logits of up to 256 experts take 16 lanes, whose
 // maximum needs no step between rows of lanes (8192 tokens of 64 experts, 6 chosen:
 // 4.8 us; a wavefront each 7.1).
 #include <type_traits>
@@ -71,6 +71,7 @@ struct Add {
 };
 
 // Lane `from`'s value, for all (it is the same for all of them).
+__device__ __forceinline__ int lane_of(int v, int from) { return __builtin_amdgcn_readlane(v, from); }
 __device__ __forceinline__ float lane_of(float v, int from) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), from));
 }
@@ -98,6 +99,12 @@ __device__ __forceinline__ T from_row(T v) {
 
 template <class Key>
 __device__ __forceinline__ Key lowest() { return -(Key)__builtin_inff(); }
+
+// An integer in the order of binary32 numbers, zeros equal.
+__device__ __forceinline__ int ordered(float v) {
+    const int b = __builtin_bit_cast(int, v + 0.0f);
+    return b ^ (b >> 31 & 0x7fffffff);
+}
 
 __device__ __forceinline__ float logit_of(const void* logits, int64_t at, bool bf16) {
     return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[at] << 16)
@@ -248,48 +255,78 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a) {
         mine_e[i] = -1;
         mine_v[i] = kNone;
     }
-    for (int j = 0; j < a.k; ++j) {
-        Key m = key[PER - 1];
-        int at = PER - 1;
-        float x = v[PER - 1];
+    auto keep = [&](int j, int e, float x) {
 #pragma unroll
-        for (int u = PER - 2; u >= 0; --u)
-            if (key[u] >= m) {
-                m = key[u];
-                at = u;
-                x = v[u];
+        for (int i = 0; i < kSlots; ++i)
+            if (i * W + l == j) {
+                mine_e[i] = e;
+                mine_v[i] = x;
             }
-        const Key best = largest<W>(m);
-        const bool found = best > lowest<Key>();
-        if (__ballot(found) == 0) break;
-        int chosen;
-        if constexpr (W == 64) {
-            const uint64_t equal = __ballot(m == best);
-            int from = __ffsll((unsigned long long)equal) - 1;
-            if (equal & (equal - 1)) {   // the one with the lowest register, then lane
+    };
+    if constexpr (W == 64) {
+        // Rounded to binary32, keys keep their order but for ties, and those are rare enough to be settled on the side.
+        int fast[PER];
 #pragma unroll
-                for (int u = PER - 1; u >= 0; --u) {
-                    const uint64_t here = __ballot(m == best && at == u);
-                    if (here != 0) from = __ffsll((unsigned long long)here) - 1;
+        for (int u = 0; u < PER; ++u) fast[u] = ordered((float)key[u]);
+        for (int j = 0; j < a.k; ++j) {
+            int best = fast[0];
+#pragma unroll
+            for (int u = 1; u < PER; ++u) best = Max()(best, fast[u]);
+            best = largest<W>(best);
+            if (best == ordered(kNone)) break;
+            uint64_t equal[PER];
+            int count = 0;
+#pragma unroll
+            for (int u = 0; u < PER; ++u) {
+                equal[u] = __ballot(fast[u] == best);
+                count += __popcll(equal[u]);
+            }
+            if (kScored && count > 1) {
+                Key m = lowest<Key>();
+#pragma unroll
+                for (int u = 0; u < PER; ++u)
+                    if (fast[u] == best) m = Max()(m, key[u]);
+                m = largest<W>(m);
+#pragma unroll
+                for (int u = 0; u < PER; ++u) equal[u] = __ballot(fast[u] == best && key[u] == m);
+            }
+            int chosen = 0, from = 0;
+            float x = kNone;
+#pragma unroll
+            for (int u = PER - 1; u >= 0; --u)
+                if (equal[u] != 0) {
+                    chosen = u;
+                    from = __ffsll((unsigned long long)equal[u]) - 1;
+                    x = lane_of(v[u], from);
                 }
-            }
-            chosen = __builtin_amdgcn_readlane(at, from) * W + from;
-            x = lane_of(x, from);
-        } else {
-            const int e = m == best ? at * W + l : INT32_MAX;
-            chosen = over<W>(e, Min());
-            x = over<W>(e == chosen ? x : kNone, Max());
-        }
-        if (found) {
 #pragma unroll
             for (int u = 0; u < PER; ++u)
-                if (u * W + l == chosen) key[u] = lowest<Key>();
+                if (u == chosen && lane == from) fast[u] = ordered(kNone);
+            keep(j, chosen * W + from, x);
+        }
+    } else {
+        for (int j = 0; j < a.k; ++j) {
+            Key m = key[PER - 1];
+            int e = (PER - 1) * W + l;
+            float x = v[PER - 1];
 #pragma unroll
-            for (int i = 0; i < kSlots; ++i)
-                if (i * W + l == j) {
-                    mine_e[i] = chosen;
-                    mine_v[i] = x;
+            for (int u = PER - 2; u >= 0; --u)
+                if (key[u] >= m) {
+                    m = key[u];
+                    e = u * W + l;
+                    x = v[u];
                 }
+            const Key best = largest<W>(m);
+            if (__ballot(best > lowest<Key>()) == 0) break;
+            e = m == best ? e : INT32_MAX;
+            const int chosen = over<W>(e, Min());
+            x = over<W>(e == chosen ? x : kNone, Max());
+            if (best > lowest<Key>()) {
+#pragma unroll
+                for (int u = 0; u < PER; ++u)
+                    if (u * W + l == chosen) key[u] = lowest<Key>();
+                keep(j, chosen, x);
+            }
         }
     }
     // weights: shares of the chosen scores' sum, or the scores themselves
