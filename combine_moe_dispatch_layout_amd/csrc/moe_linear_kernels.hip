@@ -459,11 +459,13 @@ __global__ __launch_bounds__(256) void k_linear_bwd_join(LinearBwdArgs a, int sp
 
 // ---------------------------------------------------------------- gradient before the activation
 // grad_pre = grad act'(pre), and the sums of its columns (of the binary32 values): a workgroup of 16 wavefronts takes 128 rows
-// of a slice of columns, eight a lane; the sums meet in LDS.  Up to 128 rows are in one workgroup, which writes their sums
-// itself; its wavefronts then take four rows of 128 columns at once, because the time is that of their loads one after the
-// other.  Else a wavefront's row is 512 columns long, and the kernel is bound by memory (the sums of 128 rows are 1/64 of what a
-// bf16 gradient takes).
-constexpr int kGradWaves = 16, kGradRows = 128, kGradSlice = 512, kGradSliceFew = 128;
+// of 128 columns, eight a lane and four rows a wavefront at once; the sums meet in LDS, and go out at once where that is all
+// rows (the sums of 128 rows are 1/64 of what a bf16 gradient takes).  Bound by memory: 8192 x 4096, gelu, 201 MB, 43 us, 4.7 TB/s.
+// Whole wavefronts on a row of 512 columns are as fast there (1% faster from 16384 x 4096 on) but leave most of the chip idle below
+// 256 workgroups, where the time is that of a wavefront's loads one after the other (both products with it, 1024 x 1024 x 1024: 39
+// us against 27).
+constexpr int kGradWaves = 16, kGradRows = 128, kGradSlice = 128;
+constexpr int kGradLanes = kGradSlice / 8, kGradAtOnce = kGradWaves * (64 / kGradLanes);   // a row's lanes, rows at once
 
 __device__ __forceinline__ void load_grad(const LinearGradArgs& a, int64_t at, float (&d)[8]) {
     if (a.grad_f32) {
@@ -479,17 +481,17 @@ __device__ __forceinline__ void load_grad(const LinearGradArgs& a, int64_t at, f
     }
 }
 
-template <bool GATED, int SLICE>
+template <bool GATED>
 __global__ __launch_bounds__(64 * kGradWaves) void k_linear_grad(LinearGradArgs a) {
-    constexpr int NP = GATED ? 2 : 1, kLanes = SLICE / 8, kAtOnce = kGradWaves * (64 / kLanes);   // lanes and workgroup's rows
-    __shared__ f32x4 part[kGradWaves][2][kLanes];
-    const int slices = (a.F + SLICE - 1) / SLICE, w = threadIdx.x >> 6, lane = threadIdx.x & (kLanes - 1);
-    const int block = (int)(blockIdx.x / slices), col = (int)(blockIdx.x - (unsigned)block * slices) * SLICE + lane * 8;
+    constexpr int NP = GATED ? 2 : 1;
+    __shared__ f32x4 part[kGradWaves][2][kGradLanes];
+    const int slices = (a.F + kGradSlice - 1) / kGradSlice, w = threadIdx.x >> 6, lane = threadIdx.x & (kGradLanes - 1);
+    const int block = (int)(blockIdx.x / slices), col = (int)(blockIdx.x - (unsigned)block * slices) * kGradSlice + lane * 8;
     const int M = NP * a.F;
     float sum[NP][8] = {};
     if (col < a.F) {
-        for (int i = 0; i < kGradRows / kAtOnce; ++i) {
-            const int r = block * kGradRows + i * kAtOnce + (int)threadIdx.x / kLanes;
+        for (int i = 0; i < kGradRows / kGradAtOnce; ++i) {
+            const int r = block * kGradRows + i * kGradAtOnce + (int)threadIdx.x / kGradLanes;
             if (r >= a.T) break;
             float d[8], v[8];
             load_grad(a, (int64_t)r * a.F + col, d);
@@ -527,14 +529,14 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_linear_grad(LinearGradArgs 
 #pragma unroll
     for (int h = 0; h < NP; ++h) {
 #pragma unroll
-        for (int step = kLanes; step < 64; step *= 2)
+        for (int step = kGradLanes; step < 64; step *= 2)
 #pragma unroll
             for (int k = 0; k < 8; ++k) sum[h][k] += __shfl_xor(sum[h][k], step, 64);
         if (h > 0) __syncthreads();
         part[w][0][lane] = f32x4{sum[h][0], sum[h][1], sum[h][2], sum[h][3]};
         part[w][1][lane] = f32x4{sum[h][4], sum[h][5], sum[h][6], sum[h][7]};
         __syncthreads();
-        if (w < 2 && (int)(threadIdx.x & 63) < kLanes && col < a.F) {   // each of two wavefronts half of a lane's eight
+        if (w < 2 && (int)(threadIdx.x & 63) < kGradLanes && col < a.F) {   // each of two wavefronts half of a lane's eight
             f32x4 v = part[0][w][lane];
 #pragma unroll
             for (int i = 1; i < kGradWaves; ++i) v += part[i][w][lane];
@@ -698,9 +700,11 @@ hipError_t launch_linear_grad(const LinearGradArgs& a, hipStream_t s) {
     const bool gated = a.act == MOE_ACT_SWIGLU;
     const int M = gated ? 2 * a.F : a.F;
     const int64_t sums = linear_sum_blocks(a.T);
-    auto go = [&](auto kernel, int64_t blocks) { kernel<<<dim3((unsigned)blocks), dim3(64 * kGradWaves), 0, s>>>(a); };
-    if (sums > 0) go(gated ? k_linear_grad<true, kGradSlice> : k_linear_grad<false, kGradSlice>, sums * ceil_div(a.F, kGradSlice));
-    else if (a.T > 0) go(gated ? k_linear_grad<true, kGradSliceFew> : k_linear_grad<false, kGradSliceFew>, ceil_div(a.F, kGradSliceFew));
+    if (a.T > 0) {
+        const unsigned blocks = (unsigned)(ceil_div(a.T, kGradRows) * ceil_div(a.F, kGradSlice));
+        if (gated) k_linear_grad<true><<<dim3(blocks), dim3(64 * kGradWaves), 0, s>>>(a);
+        else k_linear_grad<false><<<dim3(blocks), dim3(64 * kGradWaves), 0, s>>>(a);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.grad_bias == nullptr || (a.T > 0 && sums == 0)) return e;
     k_linear_bias<<<dim3((unsigned)((M + 63) / 64)), dim3(1024), 0, s>>>(a.partial, (int)sums, M, a.grad_bias, a.accumulate);

@@ -562,7 +562,7 @@ moe_status moe_linear_workspace(int32_t num_rows, int32_t in_features, int32_t f
  *   accumulate  1: grad_weights and grad_bias are added to what they hold
  *   workspace   moe_linear_backward_workspace bytes, 16-byte aligned: holds d, rounded to bf16 for the products
  *               (grad_bias adds the binary32 values), and sums; NULL if that is 0
- * With no rows grad_weights and grad_bias are zeroed (or left, with accumulate).  More tiles of 128 rows by 512 of
+ * With no rows grad_weights and grad_bias are zeroed (or left, with accumulate).  More tiles of 128 rows by 128 of
  * grad_out's columns than 2^22 - 128 are MOE_ERR_UNSUPPORTED. */
 moe_status moe_linear_backward(moe_ctx* ctx, const void* grad_out, int32_t out_type, int32_t num_rows,
                                const void* x, const void* weights, int32_t in_features,

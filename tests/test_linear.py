@@ -397,9 +397,9 @@ def test_workspace_sizes():
     assert moe.moe_linear_workspace(0, 64, 64) == moe.moe_linear_workspace(1, 512, 64) == moe.moe_linear_workspace(8192, 4096, 4096) == 0
     assert moe.moe_linear_workspace(24, 7168, 256) >= 2 * 24 * 256 * 4
     # more tiles than a launch has workgroups for
-    assert moe.moe_linear_workspace(2 ** 31 - 65536, 8, 256) == 0 and back(2 ** 29 - 16384, 8, 512, act=SWIGLU) > 0
+    assert moe.moe_linear_workspace(2 ** 31 - 65536, 8, 256) == 0 and back(2 ** 29 - 16384, 8, 128, act=SWIGLU) > 0
     for query in (lambda: moe.moe_linear_workspace(2 ** 31 - 65535, 8, 256), lambda: moe.moe_linear_workspace(2 ** 30, 8, 264),
-                  lambda: back(2 ** 29 - 16383, 8, 512, act=SWIGLU), lambda: back(2 ** 28, 8, 520)):
+                  lambda: back(2 ** 29 - 16383, 8, 128, act=SWIGLU), lambda: back(2 ** 28, 8, 136)):
         with pytest.raises(moe.MoeError) as e:
             query()
         assert e.value.status == moe.MOE_ERR_UNSUPPORTED
