@@ -8,7 +8,11 @@
 // Bound by reading the matrices of the experts that are chosen.  Both kernels stream them straight into
 // registers, 16 matrix rows by 128 bytes a step, and use each for up to 16 slots; the contraction
 // (k_layer_up) or the experts (k_layer_down) are shared out over the wavefronts of a workgroup and
-// joined in LDS, in an order that sizes and routing decide.
+// joined in LDS, in an order that sizes and routing decide.  One token of 6 of 64 experts, 4096 and 2048 wide, bf16:
+// 302 MB in 58 us, 5.2 TB/s (a bare read in this pattern 6.2); 128 tokens of 8 of 256, 7168 and 2048, E4M3: 11.2 GB in
+// 2.07 ms, 5.4 TB/s (1.31 and 0.69; without the loads of rows and scales 1.22 and 0.59).  A compute unit's vector cache
+// has about 700 requests of 64 bytes on their way, and the rows' count among them: hence rows come in whole lines,
+// through LDS, and no more of them than a tile has.
 //
 // Sums are binary32; the activations are rounded once, to bf16, because the second product's matrix instruction takes
 // bf16.  E4M3 matrices are widened to bf16 exactly, rows and activations are not quantised.
@@ -190,7 +194,8 @@ struct ManyTiles {
 __device__ __forceinline__ float silu(float g) { return g * (1.0f / (1.0f + __expf(-g))); }
 
 // One tile against `cols` times 16 gate columns and the up columns that belong to them, the contraction shared out over the
-// wavefronts.
+// wavefronts.  (Measured against it, 128 tokens, E4M3, both kernels 2.07 ms: the rows held in registers by sixteen wavefronts, so
+// that only the matrix is read, 2.24; two column tiles at a time 2.09 to 2.13, and one token 73 us against 59.)
 template <bool FP8, int NW, int AHEAD>
 __global__ __launch_bounds__(64 * NW) void k_layer_up(LayerArgs a, int cols) {
     constexpr int kSize = FP8 ? 1 : 2;

@@ -161,7 +161,7 @@ __device__ __forceinline__ void leave(const LinearArgs& a, char* mine, const f32
 // ---------------------------------------------------------------- few rows
 // 16 columns and up to 16 rows for a workgroup whose NW wavefronts share out the contraction: the matrix goes straight into
 // registers, and nothing is waited for but a wavefront's own loads.  Their sums meet in LDS and are added in the order of the
-// wavefronts.
+// wavefronts.  Bound by the matrix and a launch: 1 x 2048 -> 7168, 29 MB, 9.3 us, of which 4.7 would be a bare read.
 template <bool GATED, int NW, int AHEAD>
 __global__ __launch_bounds__(64 * NW) void k_linear_few(LinearArgs a) {
     constexpr int NP = GATED ? 2 : 1;
@@ -282,7 +282,8 @@ __device__ __forceinline__ void wide_tile(const LinearArgs& a, int i0, int j0, i
         }
 }
 
-// 256 rows x 256 columns (gated: 128 of each).
+// 256 rows x 256 columns (gated: 128 of each).  Bound by the matrix cores at the clock their power allows: 4096 x 7168 -> 2 x 2048,
+// gated, 240 GFLOP in 176 us, 1.37 PFLOP/s.
 template <bool GATED>
 __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void k_linear(LinearArgs a) {
     constexpr int kCols = GATED ? kTileP / 2 : kTileP, kQ = 128 * kStepBytes;
@@ -319,7 +320,8 @@ struct Part {
     }
 };
 
-// P matrix rows (gated: half of them gates) x Q rows.
+// P matrix rows (gated: half of them gates) x Q rows.  Bound by the operands' way from L2, or, with few steps, by their latency;
+// figures beside plan_tiles().
 template <int P, int Q, int WP, int WQ, int AHEAD, bool GATED>
 __global__ __launch_bounds__(64 * WP * WQ) void k_linear_tile(LinearArgs a, int split, int run) {
     using OpP = typename std::conditional<GATED, StageGated<P, WP * WQ>, StageKC<P, WP * WQ>>::type;

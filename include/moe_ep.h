@@ -577,7 +577,8 @@ moe_status moe_linear_backward_workspace(int32_t num_rows, int32_t in_features, 
 /* ---------------------------------------------------------------- a few tokens */
 /* Everything between the router and the layer's output, for decode-sized
  * batches and inference: what dispatch, expert products, activation and combine
- * give, without receive rows in between.  For a slot (t, j) with expert e = topk_idx[t, j]:
+ * give, without receive rows in between (the faster way up to about 16 tokens).  For
+ * a slot (t, j) with expert e = topk_idx[t, j]:
  *   (g, u) = W1[e] x[t],   y = W2[e] (silu(g) * u)
  *   out[t] = residual[t] + sum over valid j, ascending, of topk_weights[t, j] * y
  *   x             bf16 [num_tokens, H]
