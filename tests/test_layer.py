@@ -229,6 +229,40 @@ def test_streams_and_capture(gpu, fp8):
     c.close()
 
 
+@gpu_only
+def test_two_at_once(gpu):
+    """Two contexts on two streams, a router, a product in parts and a layer each, over the same matrices: as one after the other."""
+    m = gpu
+    E, k, H, I = 16, 3, 1024, 256
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+
+    def mat(*shape):
+        return (torch.randn(*shape, generator=g, device="cuda") * shape[-1] ** -0.5).bfloat16()
+    router, w1, w2 = mat(E, H), mat(E, 2 * I, H), mat(E, H, I)
+    ctxs = [m.Context(m.make_config(T, H, E, 1, k)) for T in (24, 100)]
+    xs = [torch.randn(T, H, generator=g, device="cuda").bfloat16() for T in (24, 100)]
+
+    def run(ctx, x):
+        logits = m.moe_linear(ctx, x, router, out_dtype=torch.float32)
+        idx, w = m.moe_route(ctx, logits, m.MOE_SCORE_SIGMOID, groups=4, topk_groups=2, group_top=2)
+        return logits, idx, w, m.moe_layer(ctx, x, idx, w, w1, w2, residual=x)
+    want = [[t.clone() for t in run(c, x)] for c, x in zip(ctxs, xs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ctxs]
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, x, s) in enumerate(zip(ctxs, xs, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(run(c, x))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for result in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(result, want[i]))
+        assert m.moe_poll_error(ctxs[i]) == (m.MOE_OK, 0)
+        ctxs[i].close()
+
+
 # ---------------------------------------------------------------- together
 @gpu_only
 @pytest.mark.parametrize("T", [1, 5, 40])

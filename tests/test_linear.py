@@ -367,6 +367,25 @@ def test_streams_and_capture(gpu):
     ctx.close()
 
 
+@gpu_only
+@pytest.mark.parametrize("act,T,K,N", [(NONE, 24, 7168, 256), (SWIGLU, 100, 2056, 264), (GELU, 129, 72, 8200), (RELU, 300, 1024, 24)])
+def test_workspace_is_not_left(gpu, act, T, K, N):
+    """Workspaces of exactly the bytes that are asked for; what lies behind stays, and results are the same."""
+    ctx = context(gpu)
+    g = generator(T)
+    M = 2 * N if act == SWIGLU else N
+    x, w, d = randn(g, T, K), randn(g, M, K, scale=K ** -0.5), randn(g, T, N)
+    pre = torch.empty(T, M, dtype=torch.bfloat16, device="cuda")
+    sizes = gpu.moe_linear_workspace(T, K, N, act), gpu.moe_linear_backward_workspace(T, K, N, act, bias=True)
+    ws = [torch.full((n + 64,), 255, dtype=torch.uint8, device="cuda") for n in sizes]
+    out = gpu.moe_linear(ctx, x, w, act=act, pre=pre, workspace=ws[0])
+    grads = gpu.moe_linear_backward(ctx, d, x, w, act=act, pre=pre, bias=True, workspace=ws[1])
+    assert all((a[n:] == 255).all() for a, n in zip(ws, sizes))
+    assert torch.equal(out, gpu.moe_linear(ctx, x, w, act=act))
+    assert all(torch.equal(a, b) for a, b in zip(grads, gpu.moe_linear_backward(ctx, d, x, w, act=act, pre=pre, bias=True)))
+    ctx.close()
+
+
 # ---------------------------------------------------------------- refusals
 def test_null_arguments_rejected():
     import combine_moe_dispatch_layout_amd as moe
