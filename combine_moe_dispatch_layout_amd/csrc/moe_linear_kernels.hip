@@ -383,6 +383,7 @@ __device__ __forceinline__ void add_parts(const float* from, int64_t stride, int
     }
 }
 
+// Bound by memory: four parts of 4096 x 256, 21 MB, 4.7 us.
 template <bool GATED>
 __global__ __launch_bounds__(256) void k_linear_join(LinearArgs a, int split) {
     const int64_t eights = a.F / 8, item = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -419,7 +420,8 @@ __device__ __forceinline__ void put8(const LinearBwdArgs& a, int64_t o, float (&
     }
 }
 
-// WEIGHTS: the contraction runs over rows of both operands; else along the gradient's rows.
+// WEIGHTS: the contraction runs over rows of both operands; else along the gradient's rows.  Bound as k_linear_tile is; figures
+// beside linear_bwd_here().
 template <int P, int Q, int WP, int WQ, int AHEAD, bool WEIGHTS>
 __global__ __launch_bounds__(64 * WP * WQ) void k_linear_bwd(LinearBwdArgs a, int split, int run) {
     using OpP = StageMC<P, WP * WQ>;
