@@ -8,6 +8,7 @@ is missing or a call fails, an exception is raised.
 import ctypes
 import functools
 import os
+from operator import index as _index
 
 import torch
 
@@ -783,17 +784,24 @@ def _logits(ctx, t, E):
     raise ValueError("logits must be [T, %d], its rows contiguous" % E)
 
 
+# What these caches keep is found by its sizes and settings.  They take plain numbers alone: a tensor of one element is a number to
+# ctypes, but as a key it is itself, whatever it holds by then.
 @functools.lru_cache(maxsize=256)
-def _router(score, groups, topk_groups, group_top, normalize, scale):
-    r = moe_router(score, groups, topk_groups, group_top, int(bool(normalize)), scale)
+def _router_struct(score, groups, topk_groups, group_top, normalize, scale):
+    r = moe_router(score, groups, topk_groups, group_top, normalize, scale)
     return r, ctypes.byref(r)
+
+
+def _router(score, groups, topk_groups, group_top, normalize, scale):
+    return _router_struct(_index(score), _index(groups), _index(topk_groups), _index(group_top), bool(normalize), float(scale))[1]
 
 
 def moe_route(ctx, logits, score=MOE_SCORE_SOFTMAX, bias=None, groups=1, topk_groups=1, group_top=1, normalize=True, scale=1.0,
               topk_idx=None, topk_weights=None):
     """The k experts of each token and their weights, from logits fp32 or bf16 [T, E] (any row stride): returns
     (topk_idx int64 [T, k], topk_weights fp32 [T, k]).  bias (fp32 [E]) is added to the scores for the choice alone; of
-    `groups` groups of neighbouring experts the topk_groups with the largest sums of their group_top best scores stay."""
+    `groups` groups of neighbouring experts the topk_groups with the largest sums of their group_top best scores stay.  Settings
+    are numbers; what a tensor in their place holds is read on the host at each call."""
     E, _, k, device = _layer_sizes(ctx)
     T, p, kind, stride = _logits(ctx, logits, E)
     if topk_idx is None:
@@ -806,7 +814,7 @@ def moe_route(ctx, logits, score=MOE_SCORE_SOFTMAX, bias=None, groups=1, topk_gr
         pw = topk_weights.data_ptr()
     else:
         pw = _arg(ctx, topk_weights, _F32, (T, k), "topk_weights")
-    st = load_library().moe_route(ctx.handle, p, kind, stride, T, _router(score, groups, topk_groups, group_top, normalize, scale)[1],
+    st = load_library().moe_route(ctx.handle, p, kind, stride, T, _router(score, groups, topk_groups, group_top, normalize, scale),
                                   _opt(ctx, bias, _F32, (E,), "bias"), pi, pw, _stream())
     if st != MOE_OK:
         raise MoeError(st, "moe_route")
@@ -824,7 +832,7 @@ def moe_route_backward(ctx, grad_weights, logits, topk_idx, score=MOE_SCORE_SOFT
         pg = _arg(ctx, grad_logits, _F32, (T, E), "grad_logits")
     st = load_library().moe_route_backward(ctx.handle, _arg(ctx, grad_weights, _F32, (T, k), "grad_weights"), p, kind, stride,
                                            _arg(ctx, topk_idx, _I64, (T, k), "topk_idx"), T,
-                                           _router(score, 1, 1, 1, normalize, scale)[1], pg, _stream())
+                                           _router(score, 1, 1, 1, normalize, scale), pg, _stream())
     if st != MOE_OK:
         raise MoeError(st, "moe_route_backward")
     return grad_logits
@@ -847,11 +855,15 @@ def _linear_sizes(x, weights, act):
 
 
 @functools.lru_cache(maxsize=4096)
-def moe_linear_workspace(T, in_features, features, act=MOE_ACT_NONE):
-    """Bytes that moe_linear works in (by sizes alone, so kept)."""
+def _linear_bytes(T, in_features, features, act):
     n = ctypes.c_size_t(0)
     _check(load_library().moe_linear_workspace(T, in_features, features, act, ctypes.byref(n)), "moe_linear_workspace")
     return n.value
+
+
+def moe_linear_workspace(T, in_features, features, act=MOE_ACT_NONE):
+    """Bytes that moe_linear works in (by sizes alone, so kept)."""
+    return _linear_bytes(_index(T), _index(in_features), _index(features), _index(act))
 
 
 def moe_linear(ctx, x, weights, bias=None, act=MOE_ACT_NONE, residual=None, out=None, out_dtype=torch.bfloat16, pre=None,
@@ -872,7 +884,7 @@ def moe_linear(ctx, x, weights, bias=None, act=MOE_ACT_NONE, residual=None, out=
         if kind is None:
             raise TypeError("out must be bfloat16 or float32")
         po = _arg(ctx, out, out.dtype, (T, F), "out")
-    ps, workspace = _workspace(ctx, x, workspace, moe_linear_workspace(T, K, F, act))
+    ps, workspace = _workspace(ctx, x, workspace, _linear_bytes(T, K, F, _index(act)))
     st = load_library().moe_linear(ctx.handle, px, T, pw, K, F, _opt(ctx, bias, _BF16, (M,), "bias"), act,
                                    _opt(ctx, residual, _BF16, (T, F), "residual"), po, kind, _opt(ctx, pre, _BF16, (T, M), "pre"),
                                    ps, _stream())
@@ -882,12 +894,16 @@ def moe_linear(ctx, x, weights, bias=None, act=MOE_ACT_NONE, residual=None, out=
 
 
 @functools.lru_cache(maxsize=4096)
+def _linear_backward_bytes(T, in_features, features, act, out_type, bias):
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_linear_backward_workspace(T, in_features, features, act, out_type, bias, ctypes.byref(n)),
+           "moe_linear_backward_workspace")
+    return n.value
+
+
 def moe_linear_backward_workspace(T, in_features, features, act=MOE_ACT_NONE, out_dtype=torch.bfloat16, bias=False):
     """Bytes that moe_linear_backward works in (by sizes and types alone, so kept)."""
-    n = ctypes.c_size_t(0)
-    _check(load_library().moe_linear_backward_workspace(T, in_features, features, act, _OUT_TYPES[out_dtype], int(bool(bias)),
-                                                        ctypes.byref(n)), "moe_linear_backward_workspace")
-    return n.value
+    return _linear_backward_bytes(_index(T), _index(in_features), _index(features), _index(act), _OUT_TYPES[out_dtype], bool(bias))
 
 
 def moe_linear_backward(ctx, grad_out, x, weights, act=MOE_ACT_NONE, pre=None, bias=False, need_x=True, need_weights=True,
@@ -931,7 +947,7 @@ def moe_linear_backward(ctx, grad_out, x, weights, act=MOE_ACT_NONE, pre=None, b
         pgb = grad_bias.data_ptr()
     else:
         pgb = None
-    ps, workspace = _workspace(ctx, x, workspace, moe_linear_backward_workspace(T, K, F, act, dtype, grad_bias is not None))
+    ps, workspace = _workspace(ctx, x, workspace, _linear_backward_bytes(T, K, F, _index(act), kind, grad_bias is not None))
     st = load_library().moe_linear_backward(ctx.handle, pd, kind, T, px, pw, K, F, act, pp, pgx, pgw, grad_type, int(bool(accumulate)),
                                             pgb, ps, _stream())
     if st != MOE_OK:

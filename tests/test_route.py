@@ -301,6 +301,41 @@ def test_captured(gpu):
     ctx.close()
 
 
+# ---------------------------------------------------------------- settings
+def test_settings_are_read_at_every_call():
+    """Settings that are tensors of one element, changed in place between calls: each call takes what they hold."""
+    import combine_moe_dispatch_layout_amd as moe
+    scale, normalize, keep = torch.tensor(2.5), torch.tensor(True), torch.tensor(2)
+    for factor, norm, groups in ((2.5, 1, 2), (5.0, 0, 3), (0.25, 1, 4)):
+        scale.fill_(factor)
+        normalize.fill_(norm)
+        keep.fill_(groups)
+        r = moe._binding._router(SIGMOID, 4, keep, 1, normalize, scale)._obj
+        assert (r.score, r.groups, r.topk_groups, r.group_top, r.normalize, r.scale) == (SIGMOID, 4, groups, 1, norm, factor)
+    rows, flag = torch.tensor(24), torch.tensor(True)
+    first = moe.moe_linear_workspace(rows, 7168, 256), moe.moe_linear_backward_workspace(rows, 7168, 256, bias=flag)
+    rows.fill_(48)
+    flag.fill_(False)
+    second = moe.moe_linear_workspace(rows, 7168, 256), moe.moe_linear_backward_workspace(rows, 7168, 256, bias=flag)
+    assert first == (moe.moe_linear_workspace(24, 7168, 256), moe.moe_linear_backward_workspace(24, 7168, 256, bias=True))
+    assert second == (moe.moe_linear_workspace(48, 7168, 256), moe.moe_linear_backward_workspace(48, 7168, 256))
+    assert first[0] != second[0]
+
+
+@gpu_only
+def test_scale_changed_in_place(gpu):
+    """The factor of the weights and of their gradient as a tensor that the program changes."""
+    g = torch.Generator().manual_seed(11)
+    ctx = gpu.Context(gpu.make_config(9, 8, 16, 1, 3))
+    v, d, scale = logits_of(g, 9, 16).cuda(), torch.randn(9, 3, generator=g).cuda(), torch.tensor(1.0)
+    for factor in (1.0, 2.0, 0.5):   # powers of two: weights and gradients are exact multiples
+        scale.fill_(factor)
+        idx, w = gpu.moe_route(ctx, v, scale=scale)
+        assert torch.equal(w, factor * gpu.moe_route(ctx, v)[1])
+        assert torch.equal(gpu.moe_route_backward(ctx, d, v, idx, scale=scale), factor * gpu.moe_route_backward(ctx, d, v, idx))
+    ctx.close()
+
+
 # ---------------------------------------------------------------- refusals
 def test_null_arguments_rejected():
     import combine_moe_dispatch_layout_amd as moe
