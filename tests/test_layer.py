@@ -155,6 +155,37 @@ def test_long_rows(gpu, fp8):
         c.close()
 
 
+# 1024 slots, so that a workgroup of the first product takes 2, 4, 8 or 16 column tiles of 16 one after another; the last of a
+# row of workgroups takes fewer, with half a tile at the end where bf16 features are no multiple of 16
+@gpu_only
+@pytest.mark.parametrize("E,H,I,fp8", [(40, 64, 648, False), (24, 200, 1512, False), (16, 64, 3400, False), (64, 40, 4104, False), (5, 72, 7704, False),
+                                       (64, 256, 1024, True), (40, 128, 1280, True), (24, 384, 3200, True), (32, 128, 5504, True), (5, 128, 7808, True)])
+def test_many_columns_a_workgroup(gpu, E, H, I, fp8):
+    """Each activation and each output, with scales that differ a lot from block to block."""
+    c = Layer(gpu, (E, uniform(256, 4, E, empty=0.02)), H, I, fp8=fp8)
+    if fp8:
+        g = torch.Generator().manual_seed(I)
+        for n, (rows, cols) in enumerate(((2 * I, H), (H, I))):
+            factor = 4.0 ** torch.randint(-1, 2, c.scales[n].shape, generator=g)
+            c.scales[n] = c.scales[n] * factor.cuda()
+            c.values[n] = c.values[n] * X.expand(factor, rows, cols)
+    c.check()
+    ws = torch.full((c.T * c.k, I), 7.0, dtype=torch.bfloat16, device="cuda")
+    c(workspace=ws)
+    act, step = ws.cpu(), X.F32_STEP
+    for e in range(E):
+        p = torch.nonzero(c.idx.reshape(-1) == e).flatten()
+        x = c.x[p // c.k].double()
+        v, d = x @ c.values[0][e].t(), (H + 192) * step * (x.abs() @ c.values[0][e].abs().t())
+        (g, u), (dg, du) = v.chunk(2, dim=1), d.chunk(2, dim=1)
+        s = F.silu(g)
+        a = s * u
+        da = 1.13 * dg * (u.abs() + du) + s.abs() * du + 128 * step * a.abs()
+        X.check(act[p], a, da + X.BF16_HALF * (a.abs() + da) + 2.0 ** -120, "activations of expert %d" % e)
+    assert (act[c.idx.reshape(-1) < 0] == 7.0).all()   # empty slots have none
+    c.close()
+
+
 @gpu_only
 @pytest.mark.parametrize("many", [False, True])
 def test_bad_ids_and_not_finite(gpu, many):
