@@ -275,6 +275,69 @@ def test_gradient_of_given_experts(gpu, score, normalize):
     ctx.close()
 
 
+def plain_gradient(v, idx, d, score, normalize, scale):
+    """The gradient of one token's weights as sums of differences, none of which cancels in binary64, and the sum of their sizes.
+    v: float64 [E] without NaN or +inf; idx, d: the slots' experts and gradients."""
+    E = v.numel()
+    out, size = torch.zeros(E, dtype=torch.float64), torch.zeros(E, dtype=torch.float64)
+    there = [j for j, e in enumerate(idx.tolist()) if e >= 0]
+    e, d = idx[there], d[there].double()
+    if score == SIGMOID or normalize:   # slots share the sum of their scores, or have nothing to do with each other
+        x = v[e]
+        s, rest = torch.sigmoid(x), torch.sigmoid(-x)
+        if normalize:
+            r = torch.exp(torch.log_softmax(torch.nn.functional.logsigmoid(x) if score == SIGMOID else x, 0))
+            each = r[None, :] * (d[:, None] - d[None, :])
+        else:
+            r, each = s, torch.diag(d)
+        factor = scale * r * (rest if score == SIGMOID else 1.0)
+        out.index_add_(0, e, factor * each.sum(1))
+        size.index_add_(0, e, factor * each.abs().sum(1))
+        return out, size
+    p = torch.softmax(v, 0)
+    of = torch.zeros(E, dtype=torch.float64).index_add_(0, e, d)   # what each expert's slots get together
+    each = p[None, :] * (of[:, None] - of[None, :])
+    return scale * p * each.sum(1), scale * p * each.abs().sum(1)
+
+
+@gpu_only
+@pytest.mark.parametrize("score,normalize", [(SOFTMAX, True), (SOFTMAX, False), (SIGMOID, True), (SIGMOID, False)])
+@pytest.mark.parametrize("E,k", [(8, 2), (12, 12), (64, 6), (100, 20), (256, 32), (257, 6), (1000, 32)])
+def test_gradient_of_a_dominant_expert(gpu, E, k, score, normalize):
+    """One expert far ahead of the others: its own gradient is a small sum over the others, and is as exact as theirs."""
+    g = torch.Generator().manual_seed(E + k)
+    gaps = [0.0, 2.0, 4.0, 6.0, 8.0, 10.0, 12.0, 14.0, 16.0, 18.0]
+    for repeated in (False, True):
+        v = torch.randn(len(gaps), E, generator=g) - (9.0 if score == SIGMOID else 0.0)
+        for t, gap in enumerate(gaps):
+            v[t, 3] = v[t].max() + gap
+        idx = torch.stack([torch.cat((torch.tensor([3]), torch.randperm(E, generator=g)[:k - 1])) for _ in gaps])
+        first = torch.stack([(row[:, None] == row[None, :]).int().argmax(1) for row in idx])
+        if not repeated:   # an empty slot where the dominant expert was drawn once more
+            idx = torch.where(first == torch.arange(k), idx, -1)
+        else:
+            idx[:, 1:] = torch.where(torch.rand(len(gaps), k - 1, generator=g) < 0.3, idx[:, :1], idx[:, 1:])
+        idx = torch.gather(idx, 1, torch.stack([torch.randperm(k, generator=g) for _ in gaps]))
+        # gradients of an expert's slots are added before they are compared with others': of one sign, so that this loses nothing
+        d = 1.0 + torch.rand(len(gaps), k, generator=g)
+        ctx = gpu.Context(gpu.make_config(len(gaps), 8, E, 1, k))
+        got = gpu.moe_route_backward(ctx, d.cuda(), v.cuda(), idx.cuda(), score, normalize=normalize, scale=2.5).double().cpu()
+        for t in range(len(gaps)):
+            ref, size = plain_gradient(v[t].double(), idx[t], d[t], score, normalize, 2.5)
+            # an exponential of a difference x is off by |x| half steps for the difference and two steps of its own, twice in a
+            # product of two shares; their sums by a half step a term; a difference of gradients, products and quotients by ten
+            spread = float(v[t].max() - v[t].min())
+            # sums of an expert's gradients are off by as many half steps as it has slots, whatever their difference to others' is
+            if repeated and score == SOFTMAX and not normalize:
+                p = torch.softmax(v[t].double(), 0)
+                of = torch.zeros(E, dtype=torch.float64).index_add_(0, idx[t], d[t].double())
+                size = size + 2.5 * p * ((p * of).sum() - p * of + (1 - p) * of)
+            tol = (2 * spread + 2 * E + 4 * k + 20) * (STEP / 2) * size + 2.0 ** -110
+            assert ((got[t] - ref).abs() <= tol).all(), (gaps[t], got[t], ref)
+        assert gpu.moe_poll_error(ctx) == (gpu.MOE_OK, 0)
+        ctx.close()
+
+
 @gpu_only
 def test_captured(gpu):
     """A captured routing with its gradient, replayed on new logits."""
