@@ -94,6 +94,33 @@ def test_linear(gpu, T, K, N, act):
     ctx.close()
 
 
+@gpu_only
+def test_gelu_keeps_its_lower_tail(gpu):
+    """v times the normal distribution below v, relative to its own size, down to where binary32 ends."""
+    from scipy.special import log_ndtr
+    ctx = context(gpu)
+    v = torch.cat((torch.linspace(-12.5, 4.0, 60001), -torch.logspace(-6, 1.09, 20000), torch.logspace(-6, 0.6, 9999))).float()
+    rows = (v.numel() + 7) // 8
+    v = torch.nn.functional.pad(v, (0, rows * 8 - v.numel()), value=1.0).reshape(rows, 8)
+    # sums that are exactly v: its 24 bits in three numbers of eight, times one
+    x, rest = torch.zeros(rows, 24), v.clone()
+    for part in range(3):
+        x[:, part::3] = rest.bfloat16().float()
+        rest -= x[:, part::3]
+    assert (rest == 0).all()
+    w = torch.eye(8).repeat_interleave(3, dim=1)
+    xd, wd = x.bfloat16().cuda(), w.bfloat16().cuda()
+    assert torch.equal(gpu.moe_linear(ctx, xd, wd, out_dtype=torch.float32).cpu(), v)
+    got = gpu.moe_linear(ctx, xd, wd, act=GELU, out_dtype=torch.float32).double().cpu()
+    below = torch.from_numpy(log_ndtr(v.double().numpy())).exp()
+    # half steps: the exponent v^2 / 2 is rounded twice and its factor log2(e) once, each worth v^2 / 2; the fit 8; the hardware's
+    # reciprocal one more than a rounding, which enters up to 3.8 times; its exponential two; three products
+    tol = (1.5 * v.double().pow(2) + 20) * (X.F32_STEP / 2)
+    off = (got / (v.double() * below) - 1).abs()
+    assert (off <= tol).all(), (float((off / tol).max()), float(v.flatten()[(off / tol).argmax()]))
+    ctx.close()
+
+
 # products whose contraction is shared out, in each kind of tile, and tiles of 128 x 128 that are not
 @gpu_only
 @pytest.mark.parametrize("act", [NONE, SILU, SWIGLU])
