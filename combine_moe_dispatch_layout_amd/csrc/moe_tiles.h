@@ -652,37 +652,16 @@ struct StageKC {
     }
 };
 
-// The same of R matrix rows whose subtiles of 16 are a gate's and an up's in turn, each from a panel of its own.
+// The same of R matrix rows whose subtiles of 16 are a gate's and an up's in turn, each from a panel of its own: a wavefront
+// loads one subtile.
 template <int R, int NW>
-struct StageGated {
+struct StageGated : StageKC<R, NW> {
     using KC = StageKC<R, NW>;
-    static constexpr int kN = KC::kN, kBytes = KC::kBytes;
-    static_assert(kN == 2 || kN == 4, "");   // a wavefront's first two loads are of one subtile
-    const char* base[2];                     // of its first pair of loads, and of its second
-    int bytes, kbytes;
-    uint32_t voff[2], chunk, at;
+    static_assert(KC::kN == 2, "");
     __device__ __forceinline__ void init(const char* gate, const char* up, int ld, int valid, int w, int lane) {
-        base[0] = kN == 2 && (w & 1) ? up : gate;
-        base[1] = up;
-        bytes = valid * ld;
-        kbytes = ld;
-        chunk = (lane & 7) * 16;
-        at = w * kN * 1024 + (lane >> 3) * kStepBytes + (((lane & 7) ^ (lane >> 3)) << 4);
-        const int row = (kN == 2 ? w >> 1 : w) * 16 + (lane >> 3);
-        voff[0] = (uint32_t)(row * ld) + chunk;
-        voff[1] = (uint32_t)((row + 8) * ld) + chunk;
+        KC::init(w & 1 ? up : gate, ld, valid, w >> 1, lane);
+        KC::at += (w - (w >> 1)) * KC::kN * 1024;   // where subtile w is in the stage
     }
-    __device__ __forceinline__ void load(i32x4 (&r)[kN], int step) const {
-        const int from = step * kStepBytes, n = from < kbytes ? bytes - from : 0;
-        const bool in = (int)chunk < kbytes - from;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) r[i] = load16(descriptor(base[i >> 1] + from, n), in ? voff[i & 1] : kOob);
-    }
-    __device__ __forceinline__ void store(char* to, const i32x4 (&r)[kN]) const {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) *reinterpret_cast<i32x4*>(to + at + i * 1024) = r[i];
-    }
-    __device__ __forceinline__ static bf16x8 frag(const char* stage, int sub, int half, int lane) { return KC::frag(stage, sub, half, lane); }
 };
 
 // 64 contraction rows of W columns a step.  Contraction row c's 32-byte unit u (16 columns) sits at u ^ key(c), so that the
