@@ -349,10 +349,11 @@ hipError_t launch(const LayerArgs& args, hipStream_t s) {
     const int P = a.T * a.k;
     const int tiles = (P < a.E ? P : a.E) + P / kRows;   // at most
     const int up = (a.I + 15) / 16, down = (a.H + 15) / 16;   // at most 2048 each
-    // Column tiles of a workgroup: enough workgroups for four rounds of four a compute unit, so that finding its slots does not
-    // count (128 tokens x 8 of 256 experts, E4M3: 1.32 ms with 8, 1.51 with one).
+    // Column tiles of a workgroup, so that finding its slots does not count: as many as leave more than ten workgroups a compute
+    // unit, of which four run at once.  Both kernels, E4M3, of 256 experts: 128 tokens x 8, 8 column tiles, 2.03 ms (16 2.06, 4 2.00;
+    // one, first kernel, 1.51 against 1.32); 32 tokens, 8, 1.25 (16 1.31, 4 1.22).  bf16, of 64: 64 tokens x 6, 4, 670 us (2 680).
     int cols = 1;
-    while (cols < 16 && (int64_t)tiles * up >= 4096 * cols) cols *= 2;
+    while (cols < 16 && (int64_t)tiles * ((up + 2 * cols - 1) / (2 * cols)) > 10 * 256) cols *= 2;
     k_layer_up<FP8, 4, FP8 ? 2 : 4><<<dim3((unsigned)(tiles * ((up + cols - 1) / cols))), dim3(256), 0, s>>>(a, cols);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -155,11 +155,12 @@ def test_long_rows(gpu, fp8):
         c.close()
 
 
-# 1024 slots, so that a workgroup of the first product takes 2, 4, 8 or 16 column tiles of 16 one after another; the last of a
+# 1024 slots, so that a workgroup of the first product takes 1, 2, 4, 8 or 16 column tiles one after another; the last of a
 # row of workgroups takes fewer, with half a tile at the end where bf16 features are no multiple of 16
 @gpu_only
 @pytest.mark.parametrize("E,H,I,fp8", [(40, 64, 648, False), (24, 200, 1512, False), (16, 64, 3400, False), (64, 40, 4104, False), (5, 72, 7704, False),
-                                       (64, 256, 1024, True), (40, 128, 1280, True), (24, 384, 3200, True), (32, 128, 5504, True), (5, 128, 7808, True)])
+                                       (64, 256, 1024, True), (40, 128, 1280, True), (24, 384, 3200, True), (32, 128, 5504, True), (5, 128, 7808, True),
+                                       (5, 72, 15400, False), (16, 40, 13112, False), (5, 128, 15232, True), (12, 128, 13696, True)])
 def test_many_columns_a_workgroup(gpu, E, H, I, fp8):
     """Each activation and each output, with scales that differ a lot from block to block."""
     c = Layer(gpu, (E, uniform(256, 4, E, empty=0.02)), H, I, fp8=fp8)
