@@ -128,7 +128,7 @@ __device__ __forceinline__ T largest(T v) {
     return lane_of(v, 63);
 }
 
-// 1 / d of d in [1, 2], to about a step
+// 1 / d, to about a step; d and its reciprocal normal numbers
 __device__ __forceinline__ double inverse(double d) {
     double r = __builtin_amdgcn_rcp(d);
     r = __builtin_fma(r, __builtin_fma(-d, r, 1.0), r);
@@ -370,9 +370,10 @@ __global__ __launch_bounds__(kThreads) void k_route(RouteArgs a) {
 //                        that has no slot, for the others c p_i (sum over experts j with slots of p_j (g_i - g_j) + g_i times
 //                        the p of those without)
 // Differences are taken before they are added up: r_i (g_i - sum of r g), which is the same number, loses all of it for
-// an expert that has nearly all of the weight, where the sum is nearly its own g.
+// an expert that has nearly all of the weight, where the sum is nearly its own g.  Sums are
+// binary64: an error of the scores' sum is one of all r together, and that of differences grows with the slots.
 // Bound by latency: loads of the slots, of their logits, sums over the lanes, rounds over the slots, stores (8192 tokens of 64
-// experts, 6 chosen, replayed: shares 4.0 us, 3.6 without differences; softmax 5.2 and 4.1).
+// experts, 6 chosen, replayed: shares 3.9 us, 3.6 without differences; softmax 5.5 and 4.1).
 template <bool BF16, int W, int PER>
 __global__ __launch_bounds__(kThreads) void k_route_bwd(RouteBwdArgs a) {
     constexpr float kNone = -__builtin_inff();
@@ -403,28 +404,32 @@ __global__ __launch_bounds__(kThreads) void k_route_bwd(RouteBwdArgs a) {
         peak = fmaxf(peak, x[i]);
     }
     peak = over<W>(peak, Max());
-    float top = kNone, total = 1.0f;
+    float top = kNone;
+    double sum = 0.0;   // of the scores that share it
     if (spread) {
 #pragma unroll
         for (int u = 0; u < PER; ++u) top = fmaxf(top, v[u]);
         top = over<W>(top, Max());
         if (!(top > kNone)) top = 0.0f;
-        total = 0.0f;
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
-            v[u] = expf(v[u] - top);   // p times the total
-            total += v[u];
+            v[u] = expf(v[u] - top);   // p times the sum
+            sum += v[u];
         }
-        total = over<W>(total, Add());
-        if (!(total > 0.0f)) total = 1.0f;
     }
-    float r[kSlots], sum = 0.0f;
+    float r[kSlots];
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
         if (e[i] < 0) r[i] = 0.0f;
         else if (a.sigmoid) r[i] = a.normalize && peak < 0.0f ? expf(x[i] - peak) / (1.0f + expf(x[i])) : sigmoid32(x[i]);
-        else r[i] = expf(x[i] - (a.normalize ? peak : top)) / total;
-        sum += r[i];
+        else r[i] = expf(x[i] - (a.normalize ? peak : top));
+        if (a.normalize) sum += r[i];
+    }
+    if (a.normalize || spread) {
+        sum = over<W>(sum, Add());
+        sum = sum > 0.0 ? inverse(sum) : 0.0;
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) r[i] = (float)(r[i] * sum);
     }
     // slot j's value, for the token's lanes
     auto slot = [&](const auto (&of)[kSlots], int j) {
@@ -432,18 +437,22 @@ __global__ __launch_bounds__(kThreads) void k_route_bwd(RouteBwdArgs a) {
         else return __shfl(j < W ? of[0] : of[kSlots - 1], (threadIdx.x & 63 & ~(W - 1)) | (j & (W - 1)), 64);
     };
     float d[kSlots], out[PER] = {};
-    if (a.normalize) {
-        sum = over<W>(sum, Add());
+    // d_i = start_i + sum over the slots of r_j (of_i - of_j)
+    auto differences = [&](const float (&of)[kSlots], const float (&start)[kSlots]) {
+        double sums[kSlots];
 #pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-            r[i] = sum > 0.0f ? r[i] / sum : 0.0f;
-            d[i] = 0.0f;
-        }
+        for (int i = 0; i < kSlots; ++i) sums[i] = start[i];
         for (int j = 0; j < a.k; ++j) {
-            const float rj = slot(r, j), gj = slot(g, j);
+            const double rj = slot(r, j), oj = slot(of, j);
 #pragma unroll
-            for (int i = 0; i < kSlots; ++i) d[i] += rj * (g[i] - gj);
+            for (int i = 0; i < kSlots; ++i) sums[i] = __builtin_fma(rj, of[i] - oj, sums[i]);
         }
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) d[i] = (float)sums[i];
+    };
+    if (a.normalize) {
+        const float zero[kSlots] = {};
+        differences(g, zero);
     } else if (spread) {
         // an expert's slots together in its first one, and the experts without any
         float own[kSlots];
@@ -466,23 +475,20 @@ __global__ __launch_bounds__(kThreads) void k_route_bwd(RouteBwdArgs a) {
 #pragma unroll
             for (int u = 0; u < PER; ++u) has |= (uint32_t)(u * W + l == ej) << u;
         }
-        float none = 0.0f, mean = 0.0f;
+        double none = 0.0, mean = 0.0;
 #pragma unroll
         for (int u = 0; u < PER; ++u) none += has >> u & 1 ? 0.0f : v[u];
-        none = over<W>(none, Add()) / total;
+        none = over<W>(none, Add()) * sum;
+        float start[kSlots];
 #pragma unroll
         for (int i = 0; i < kSlots; ++i) {
             if (!first[i]) r[i] = 0.0f;
-            mean += r[i] * own[i];
-            d[i] = none * own[i];
+            mean += (double)r[i] * own[i];
+            start[i] = (float)(none * own[i]);
         }
         mean = over<W>(mean, Add());
-        for (int j = 0; j < a.k; ++j) {
-            const float rj = slot(r, j), oj = slot(own, j);
-#pragma unroll
-            for (int i = 0; i < kSlots; ++i) d[i] += rj * (own[i] - oj);
-        }
-        const float rest = a.scale * mean / total;
+        differences(own, start);
+        const float rest = (float)(a.scale * mean * sum);
 #pragma unroll
         for (int u = 0; u < PER; ++u) out[u] = has >> u & 1 ? 0.0f : -v[u] * rest;
     } else {
