@@ -361,6 +361,24 @@ def test_no_rows(gpu):
 
 
 @gpu_only
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_no_rows_of_a_large_matrix(gpu, dtype):
+    """Gradients of no rows where the matrix has more tiles than the dense product's own kernels take: zeros, or left."""
+    ctx = context(gpu)
+    K, M = 5128, 4112
+    x, w = torch.zeros(0, K, dtype=torch.bfloat16, device="cuda"), torch.ones(M, K, dtype=torch.bfloat16, device="cuda")
+    for act, N in ((NONE, M), (SWIGLU, M // 2)):
+        d, pre = torch.zeros(0, N, dtype=dtype, device="cuda"), torch.zeros(0, M, dtype=torch.bfloat16, device="cuda")
+        gw, gb = torch.full((M, K), 7.0, dtype=dtype, device="cuda"), torch.full((M,), 7.0, device="cuda")
+        gpu.moe_linear_backward(ctx, d, x, w, act=act, pre=pre, bias=True, grad_weights=gw, grad_bias=gb, accumulate=True)
+        assert (gw == 7.0).all() and (gb == 7.0).all()
+        gx, _, _ = gpu.moe_linear_backward(ctx, d, x, w, act=act, pre=pre, bias=True, grad_weights=gw, grad_bias=gb)
+        assert gx.shape == (0, K) and (gw == 0).all() and (gb == 0).all()
+    assert gpu.moe_poll_error(ctx) == (gpu.MOE_OK, 0)
+    ctx.close()
+
+
+@gpu_only
 def test_streams_and_capture(gpu):
     """Forward and backward on a side stream, and captured with the workspace that the binding makes, replayed on new inputs
     beside eager calls of the same context."""
