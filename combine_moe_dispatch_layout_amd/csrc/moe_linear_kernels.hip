@@ -321,8 +321,8 @@ struct Part {
     }
 };
 
-// P matrix rows (gated: half of them gates) x Q rows.  Bound by the operands' way from L2, or, with few steps, by their latency;
-// figures beside plan_tiles().
+// P matrix rows (gated: half of them gates) x Q rows.  Bound by LDS where two workgroups of 128 x 128 share a compute unit, else by
+// the latency of its steps (counters beside StagedBody's operands); times beside plan_tiles().
 template <int P, int Q, int WP, int WQ, int AHEAD, bool GATED>
 __global__ __launch_bounds__(64 * WP * WQ) void k_linear_tile(LinearArgs a, int split, int run) {
     using OpP = typename std::conditional<GATED, StageGated<P, WP * WQ>, StageKC<P, WP * WQ>>::type;
@@ -463,12 +463,14 @@ __global__ __launch_bounds__(256) void k_linear_bwd_join(LinearBwdArgs a, int sp
 }
 
 // ---------------------------------------------------------------- gradient before the activation
-// grad_pre = grad act'(pre), and the sums of its columns (of the binary32 values): a workgroup of 16 wavefronts takes 128 rows
-// of 128 columns, eight a lane and four rows a wavefront at once; the sums meet in LDS, and go out at once where that is all
-// rows (the sums of 128 rows are 1/64 of what a bf16 gradient takes).  Bound by memory: 8192 x 4096, gelu, 201 MB, 43 us, 4.7 TB/s.
-// Whole wavefronts on a row of 512 columns are as fast there (1% faster from 16384 x 4096 on) but leave most of the chip idle below
-// 256 workgroups, where the time is that of a wavefront's loads one after the other (both products with it, 1024 x 1024 x 1024: 39
-// us against 27).
+// grad_pre = grad act'(pre), and the sums of its columns (of the binary32 values).  grad_pre is rounded once, to bf16 (off by
+// at most 2^-8 of its value), also where the gradient comes in binary32: the matrix instruction of both products takes bf16,
+// and as a sum of two such numbers it would cost them twice the operations.  A workgroup of 16 wavefronts takes 128 rows of 128
+// columns, eight a lane and four rows a wavefront at once; the sums meet in LDS, and go out at once where that is all rows (the
+// sums of 128 rows are 1/64 of what a bf16 gradient takes).  Bound by memory: 8192 x 4096, gelu, 201 MB, 43 us, 4.7 TB/s.
+// Whole wavefronts on a row of 512 columns are as fast there (1% faster from 16384 x 4096 on) but leave most of the chip idle
+// below 256 workgroups, where the time is that of a wavefront's loads one after the other (both products with it, 1024 x 1024 x
+// 1024: 39 us against 27).
 constexpr int kGradWaves = 16, kGradRows = 128, kGradSlice = 128;
 constexpr int kGradLanes = kGradSlice / 8, kGradAtOnce = kGradWaves * (64 / kGradLanes);   // a row's lanes, rows at once
 
@@ -596,9 +598,9 @@ hipError_t launch_bwd(const LinearBwdArgs& a, int split, hipStream_t s) {
 
 // ---------------------------------------------------------------- which kernel
 // How a product of `rows` x `cols` results over `steps` steps is shared out: tiles of kTileRows x kTileCols, the contraction
-// in `split` parts.  The shortest of what they are expected to take, us: the operands' way from L2, or the latency of a
-// workgroup's steps; and the partial sums' way to memory and back with a second launch.  Measured, cold matrices, us (tile
-// rows x columns / parts; the choice first):
+// in `split` parts.  The shortest of what they are expected to take, us: the operands at the rate that full compute units take them
+// in (12 TB/s, fitted to the times below; what stands behind it is LDS), or the latency of a workgroup's steps; and the partial
+// sums' way to memory and back with a second launch.  Measured, cold matrices, us (tile rows x columns / parts; the choice first):
 //   4096 x 7168 -> 256     128 x 128 / 4  31   / 1 90    64 x 64 / 1 38
 //   8192 x 4096 -> 64      32 x 64 / 1    19             64 x 64 / 1 24
 //   1024 x 4096 -> 4096    128 x 128 / 1  44   / 2 54    64 x 64 / 1 67   256 x 256 105
@@ -615,7 +617,7 @@ struct Plan {
 };
 enum { kTile128, kTile64, kTile32, kTiles, kWide };
 constexpr int kTileCols[kTiles] = {128, 64, 64}, kTileRows[kTiles] = {128, 64, 32};
-constexpr float kStepUs[kTiles] = {0.65f, 0.33f, 0.2f}, kL2Us = 1.0f / 12e6f, kPartUs = 8.0f / 5e6f, kJoinUs = 4.0f, kWideUs = 1.6f;
+constexpr float kStepUs[kTiles] = {0.65f, 0.33f, 0.2f}, kOperandUs = 1.0f / 12e6f, kPartUs = 8.0f / 5e6f, kJoinUs = 4.0f, kWideUs = 1.6f;
 
 constexpr int64_t kMostTiles = (1 << 23) - 256;   // of up to 512 threads: a launch has fewer than 2^32
 
@@ -628,7 +630,7 @@ Plan plan_tiles(int64_t rows, int64_t cols, int64_t steps, int tiles) {
         const int64_t n = ceil_div(rows, kTileRows[t]) * ceil_div(cols, kTileCols[t]);
         if (n >= kMostTiles) continue;
         for (int split = 1; split <= 16 && (split == 1 || steps >= 4 * split); split *= 2) {
-            const float traffic = (float)n * steps * (kTileCols[t] + kTileRows[t]) * kStepBytes * kL2Us;
+            const float traffic = (float)n * steps * (kTileCols[t] + kTileRows[t]) * kStepBytes * kOperandUs;
             const float latency = (float)ceil_div(steps, split) * ceil_div(n * split, 512) * kStepUs[t];
             const float us = (traffic > latency ? traffic : latency) + (split > 1 ? kJoinUs + (float)split * rows * cols * kPartUs : 0.0f);
             if (us < best.us) best = Plan{t, split, us};

@@ -614,9 +614,12 @@ struct Direct {
 
 // ---------------------------------------------------------------- operands through registers into LDS
 // For tiles that are too few, or too small, to hide a step's latency: operands are loaded into registers several steps
-// ahead (each use waits for its own loads alone) and stored to LDS, which holds two steps.  What bounds many of them
-// is the way from L2: about 12 TB/s of operands, 0.75 PFLOP/s in tiles of 128 x 128.  A third step in LDS, so that fragments
-// are read a barrier ahead, made no difference but for fewer workgroups a compute unit.
+// ahead (each use waits for its own loads alone) and stored to LDS, which holds two steps.  What bounds many tiles of 128 x 128
+// is LDS more than anything else (counters of 2048 x 4096 -> 4096, two workgroups a compute unit: LDS works in 57% of the cycles,
+// the matrix cores in 44%, a third of the wavefronts' time is waiting to issue to LDS; operands come at 14 TB/s).  One workgroup a
+// compute unit alternates between the two (4096 x 7168 -> 256 in four parts: 40% and 30%, operands at 9 TB/s), and tiles of 64 x 64 wait
+// for their steps' latency (64 x 4096 -> 4096 in four parts: 21% and 10%).  There are no bank conflicts.  A third step in LDS, so that fragments are read a barrier ahead, made no difference but for fewer
+// workgroups a compute unit.
 
 // R rows of 128 contraction bytes a step for NW wavefronts, in LoadKC's order.
 template <int R, int NW>

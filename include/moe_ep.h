@@ -560,8 +560,8 @@ moe_status moe_linear_workspace(int32_t num_rows, int32_t in_features, int32_t f
  *   x, weights  as in moe_linear; weights is read for grad_x, x for grad_weights (else NULL will do)
  *   pre         what moe_linear wrote; not read for MOE_ACT_NONE (may be NULL)
  *   accumulate  1: grad_weights and grad_bias are added to what they hold
- *   workspace   moe_linear_backward_workspace bytes, 16-byte aligned: holds d, rounded to bf16 for the products
- *               (grad_bias adds the binary32 values), and sums; NULL if that is 0
+ *   workspace   moe_linear_backward_workspace bytes, 16-byte aligned: holds d, rounded to bf16 for the products, also
+ *               where grad_out is fp32 (grad_bias adds the binary32 values), and sums; NULL if that is 0
  * With no rows grad_weights and grad_bias are zeroed (or left, with accumulate).  More tiles of 128 rows by 128 of
  * grad_out's columns than 2^22 - 128 are MOE_ERR_UNSUPPORTED. */
 moe_status moe_linear_backward(moe_ctx* ctx, const void* grad_out, int32_t out_type, int32_t num_rows,
@@ -577,7 +577,8 @@ moe_status moe_linear_backward_workspace(int32_t num_rows, int32_t in_features, 
 /* ---------------------------------------------------------------- a few tokens */
 /* Everything between the router and the layer's output, for decode-sized
  * batches and inference: what dispatch, expert products, activation and combine
- * give, without receive rows in between (the faster way up to about 16 tokens).  For
+ * give, without receive rows in between.  It is the faster way up to about 16 tokens; from about 32 on those
+ * calls are (256 experts of 7168 and 2048 in E4M3, 8 a token, 128 tokens: 1.86 ms against 2.05).  For
  * a slot (t, j) with expert e = topk_idx[t, j]:
  *   (g, u) = W1[e] x[t],   y = W2[e] (silu(g) * u)
  *   out[t] = residual[t] + sum over valid j, ascending, of topk_weights[t, j] * y
@@ -601,8 +602,9 @@ moe_status moe_layer(moe_ctx* ctx, const void* x, const int64_t* topk_idx, const
 /* The same with matrices of E4M3 codes and a scale for each 128 x 128 block:
  *   w1_scales  fp32 [E, 2 * features / 128, H / 128]
  *   w2_scales  fp32 [E, H / 128, features / 128]
- * H and features multiples of 128.  Rows and activations stay bf16 (the codes are widened exactly): few
- * rows cost nothing beside the matrices, so nothing is lost by quantising them. */
+ * H and features multiples of 128.  Rows and activations stay bf16 and the codes are widened exactly, so that nothing is lost
+ * by quantising rows; they cost little beside the matrices as long as they are few (with their scales an eighth of the time at
+ * 128 tokens of 8 experts, which moe_dispatch, the expert products and moe_combine take 10% less for). */
 moe_status moe_layer_fp8(moe_ctx* ctx, const void* x, const int64_t* topk_idx,
                          const float* topk_weights, int32_t num_tokens, const void* w1,
                          const float* w1_scales, const void* w2, const float* w2_scales,
