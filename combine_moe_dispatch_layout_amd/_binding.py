@@ -69,6 +69,23 @@ class MoeError(RuntimeError):
         super().__init__("%s failed: %s" % (what, status_str(status)))
 
 
+# ctypes passes the lower 32 bits of a number that is longer: sizes and settings are looked at before.
+_INT_MAX = 2 ** 31 - 1
+
+
+def _int32(*values):
+    for v in values:
+        if not -_INT_MAX <= v <= _INT_MAX:
+            raise MoeError(MOE_ERR_UNSUPPORTED, "a size or setting of %d" % v)
+
+
+def _tokens(n):
+    """A batch's tokens, which no context has more than 2^31 - 1 of."""
+    if n > _INT_MAX:
+        raise MoeError(MOE_ERR_CAPACITY, "a batch of %d tokens" % n)
+    return n
+
+
 # ---------------------------------------------------------------- C structs
 class moe_config(ctypes.Structure):
     _fields_ = [("max_tokens", ctypes.c_int32), ("hidden", ctypes.c_int32),
@@ -418,7 +435,7 @@ def moe_dispatch_layout(ctx, topk_idx, num_tokens_per_expert=None, num_tokens_pe
     into the Infinity Cache (moe_dispatch_layout_prefetch)."""
     c = ctx.cfg
     _as_dev(topk_idx, torch.int64, "topk_idx")
-    T = topk_idx.shape[0]
+    T = _tokens(topk_idx.shape[0])
     if topk_idx.dim() != 2 or topk_idx.shape[1] != c.topk:
         raise ValueError("topk_idx must be [T, %d]" % c.topk)
     dev = topk_idx.device
@@ -452,7 +469,7 @@ def moe_dispatch(ctx, x, topk_idx, reuse_layout=False, bufs=None, handle=None):
     _as_dev(x, torch.bfloat16, "x")
     _as_dev(topk_idx, torch.int64, "topk_idx")
     xs = x.shape
-    T = xs[0]
+    T = _tokens(xs[0])
     if len(xs) != 2 or xs[1] != c.hidden or topk_idx.shape != (T, c.topk):
         raise ValueError("x must be [T, %d] and topk_idx [T, %d]" % (c.hidden, c.topk))
     if bufs is None:
@@ -583,7 +600,10 @@ def _mats_shape(ctx, weights):
     shape = weights.shape
     if len(shape) != 3 or shape[0] != ctx.cfg.num_experts:
         raise ValueError("weights must be [%d, out_features, in_features]" % ctx.cfg.num_experts)
-    return shape[1], shape[2]
+    N, K = shape[1], shape[2]
+    if N > _INT_MAX or K > _INT_MAX:
+        _int32(N, K)
+    return N, K
 
 
 def moe_expert_gemm(ctx, rows, weights, handle, out=None, rows_order=MOE_ROWS_RECV, out_order=MOE_ROWS_RECV):
@@ -644,6 +664,7 @@ def moe_expert_gemm_backward_weights(ctx, grad_out, rows, handle, grad_weights=N
     if grad_out.dim() != 2 or rows.dim() != 2:
         raise ValueError("grad_out and rows must have two dimensions")
     N, K = grad_out.shape[1], rows.shape[1]
+    _int32(N, K)
     _check_handle(ctx, handle)
     pg = _expert_rows(ctx, grad_out, torch.bfloat16, N, out_order, "grad_out")
     pr = _expert_rows(ctx, rows, torch.bfloat16, K, rows_order, "rows")
@@ -666,6 +687,7 @@ def _gate_up_features(gate_up):
     shape = gate_up.shape
     if len(shape) != 2 or shape[1] % 2:
         raise ValueError("gate_up must be [rows, 2 * features]")
+    _int32(shape[1] // 2)
     return shape[1] // 2
 
 
@@ -772,6 +794,7 @@ def _logits(ctx, t, E):
         raise ValueError("logits is on %s, the context on cuda:%d" % (t.device, ctx.device))
     shape = t.shape
     if len(shape) == 2 and shape[1] == E:
+        _tokens(shape[0])
         if t.is_contiguous():
             return shape[0], t.data_ptr(), kind, E
         stride, columns = t.stride()
@@ -788,6 +811,7 @@ def _logits(ctx, t, E):
 # ctypes, but as a key it is itself, whatever it holds by then.
 @functools.lru_cache(maxsize=256)
 def _router_struct(score, groups, topk_groups, group_top, normalize, scale):
+    _int32(score, groups, topk_groups, group_top)
     r = moe_router(score, groups, topk_groups, group_top, normalize, scale)
     return r, ctypes.byref(r)
 
@@ -856,6 +880,7 @@ def _linear_sizes(x, weights, act):
 
 @functools.lru_cache(maxsize=4096)
 def _linear_bytes(T, in_features, features, act):
+    _int32(T, in_features, features, act)
     n = ctypes.c_size_t(0)
     _check(load_library().moe_linear_workspace(T, in_features, features, act, ctypes.byref(n)), "moe_linear_workspace")
     return n.value
@@ -872,6 +897,7 @@ def moe_linear(ctx, x, weights, bias=None, act=MOE_ACT_NONE, residual=None, out=
     [T, F], bf16 or fp32 (out's dtype, or out_dtype), F = M, or M / 2 for MOE_ACT_SWIGLU.  pre: bf16 [T, M], receives
     what moe_linear_backward needs.  workspace: moe_linear_workspace bytes."""
     T, K, F, M = _linear_sizes(x, weights, act)
+    nbytes = _linear_bytes(T, K, F, _index(act))
     px, pw = _arg(ctx, x, _BF16, (T, K), "x"), _arg(ctx, weights, _BF16, (M, K), "weights")
     if out is None:
         kind = _OUT_TYPES.get(out_dtype)
@@ -884,7 +910,7 @@ def moe_linear(ctx, x, weights, bias=None, act=MOE_ACT_NONE, residual=None, out=
         if kind is None:
             raise TypeError("out must be bfloat16 or float32")
         po = _arg(ctx, out, out.dtype, (T, F), "out")
-    ps, workspace = _workspace(ctx, x, workspace, _linear_bytes(T, K, F, _index(act)))
+    ps, workspace = _workspace(ctx, x, workspace, nbytes)
     st = load_library().moe_linear(ctx.handle, px, T, pw, K, F, _opt(ctx, bias, _BF16, (M,), "bias"), act,
                                    _opt(ctx, residual, _BF16, (T, F), "residual"), po, kind, _opt(ctx, pre, _BF16, (T, M), "pre"),
                                    ps, _stream())
@@ -895,6 +921,7 @@ def moe_linear(ctx, x, weights, bias=None, act=MOE_ACT_NONE, residual=None, out=
 
 @functools.lru_cache(maxsize=4096)
 def _linear_backward_bytes(T, in_features, features, act, out_type, bias):
+    _int32(T, in_features, features, act)
     n = ctypes.c_size_t(0)
     _check(load_library().moe_linear_backward_workspace(T, in_features, features, act, out_type, bias, ctypes.byref(n)),
            "moe_linear_backward_workspace")
@@ -919,6 +946,7 @@ def moe_linear_backward(ctx, grad_out, x, weights, act=MOE_ACT_NONE, pre=None, b
         raise TypeError("grad_out must be bfloat16 or float32")
     if accumulate and ((need_weights and grad_weights is None) or (bias and grad_bias is None)):
         raise ValueError("accumulate needs grad_weights and grad_bias")
+    nbytes = _linear_backward_bytes(T, K, F, _index(act), kind, bool(bias) or grad_bias is not None)
     pd, px, pw = _arg(ctx, grad_out, dtype, (T, F), "grad_out"), _arg(ctx, x, _BF16, (T, K), "x"), _arg(ctx, weights, _BF16, (M, K), "weights")
     pp = _opt(ctx, pre, _BF16, (T, M), "pre")
     if grad_x is not None:
@@ -947,7 +975,7 @@ def moe_linear_backward(ctx, grad_out, x, weights, act=MOE_ACT_NONE, pre=None, b
         pgb = grad_bias.data_ptr()
     else:
         pgb = None
-    ps, workspace = _workspace(ctx, x, workspace, _linear_backward_bytes(T, K, F, _index(act), kind, grad_bias is not None))
+    ps, workspace = _workspace(ctx, x, workspace, nbytes)
     st = load_library().moe_linear_backward(ctx.handle, pd, kind, T, px, pw, K, F, act, pp, pgx, pgw, grad_type, int(bool(accumulate)),
                                             pgb, ps, _stream())
     if st != MOE_OK:
@@ -960,7 +988,9 @@ def _layer_args(ctx, x, topk_idx, topk_weights, w1, w2, dtype, residual, out, wo
     xs, ws = x.shape, w2.shape
     if len(xs) != 2 or len(ws) != 3:
         raise ValueError("x must be [T, %d] and w2 [%d, %d, features]" % (H, E, H))
-    T, I = xs[0], ws[2]
+    T, I = _tokens(xs[0]), ws[2]
+    if I > _INT_MAX:
+        _int32(I)
     px = _arg(ctx, x, _BF16, (T, H), "x")
     if out is None:
         out = torch.empty_like(x)
@@ -1008,7 +1038,7 @@ def prepare_dispatch(ctx, x, topk_idx, reuse_layout, bufs, handle, stream=None):
     c = ctx.cfg
     _as_dev(x, torch.bfloat16, "x")
     _as_dev(topk_idx, torch.int64, "topk_idx")
-    T = x.shape[0]
+    T = _tokens(x.shape[0])
     if x.dim() != 2 or x.shape[1] != c.hidden or tuple(topk_idx.shape) != (T, c.topk):
         raise ValueError("x must be [T, %d] and topk_idx [T, %d]" % (c.hidden, c.topk))
     _check_bufs(ctx, bufs)
@@ -1075,7 +1105,7 @@ def moe_dispatch_noalloc(scfg, x, topk_idx, bufs, handle, error_word=None):
     c = scfg.cfg
     _as_dev(x, torch.bfloat16, "x")
     _as_dev(topk_idx, torch.int64, "topk_idx")
-    T = x.shape[0]
+    T = _tokens(x.shape[0])
     if x.dim() != 2 or x.shape[1] != c.hidden or tuple(topk_idx.shape) != (T, c.topk):
         raise ValueError("x must be [T, %d] and topk_idx [T, %d]" % (c.hidden, c.topk))
     _check_bufs(scfg, bufs)
